@@ -1,0 +1,323 @@
+// Tiles, matrix fragments and arguments shared by the cross attention kernels.
+//
+// Every product is computed on 32 x 32 blocks of the matrix cores, 16 deep. With l the lane and h = l / 32, a lane holds
+//   an operand fragment: 8 values of row (or column) l % 32, at depths 8 h .. 8 h + 7;
+//   a result block: column l % 32, rows 8 (i / 4) + 4 h + i % 4 for i = 0 .. 15.
+// The depth order of a product may be permuted freely if both operands agree, so a 32 x 32 result block of scores is,
+// as it lies in registers, the right operand of the product that sums over its rows: its values 8 s .. 8 s + 7 are the
+// fragment of rows 16 s + 4 h + {0..3} and 16 s + 8 + 4 h + {0..3}. Probabilities therefore never pass through LDS; the
+// left operand (the transposed tile) is read from LDS in that order, with the hardware's transposing reads for 16-bit
+// types. float32 features use the same fragments, each fed to eight 32 x 32 x 2 float products.
+#pragma once
+
+#include <type_traits>
+
+#include "feature_common.hpp"
+
+namespace gsr {
+
+constexpr int kAttnThreads = 256, kAttnWaves = 4;
+constexpr int kAttnRows = 32 * kAttnWaves;  // rows (queries, or keys in the key gradient) of a workgroup
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+using f32x16 = Vec<float, 16>;
+using u32x4 = Vec<uint32_t, 4>;
+
+// Powers of two by which probabilities are kept too large: a float16 probability below 2^-14 would lose bits, and in a
+// long flat context most are. 2^14 times one is still finite, and the sums divide it out.
+template <typename T>
+constexpr float kLift = std::is_same_v<T, _Float16> ? 14.0f : 0.0f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// a * b + c on one block.
+__device__ __forceinline__ f32x16 mma(Vec<__bf16, 8> a, Vec<__bf16, 8> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(Vec<_Float16, 8> a, Vec<_Float16, 8> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(Vec<float, 8> a, Vec<float, 8> b, f32x16 c) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+  return c;
+}
+
+// The other half's value of the same column (lane ^ 32).
+__device__ __forceinline__ float other_half(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+// n / d by multiplication, for n < 2^31.
+struct FastDiv {
+  uint32_t m, s, d;
+  void set(uint32_t by) {
+    d = by;
+    s = 0;
+    while ((uint64_t(1) << s) < by) ++s;
+    m = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << s) - by)) / by + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
+
+struct AttnArgs {
+  const void *q, *k, *v, *o, *dout;
+  void *out, *dq, *dk, *dv;
+  const int32_t* kv_len;
+  const uint8_t* mask;
+  float *lse, *delta, *part, *part_ml;
+  uint32_t batch, heads, kv_heads, queries, keys, dim;
+  uint32_t rows;   // queries * (heads / kv_heads): the rows that meet one key head
+  uint32_t tiles;  // workgroups across rows (keys in the key gradient)
+  uint32_t splits, works, per_xcd;
+  float scale;
+  FastDiv share;   // row -> query; the rest is the head within its group
+  int64_t qs[3], ks[3], vs[3], os[3], ms[3], dos[3], dqs[3], dks[3], dvs[3];
+};
+
+// What a workgroup works on. Workgroups are dealt to the dies round-robin, so consecutive works (the row tiles of one
+// key head, which read the same keys and values) are given to one die and share its L2.
+struct AttnWork {
+  uint32_t tile, split, kv_head, batch;
+  __device__ __forceinline__ bool set(const AttnArgs& a) {
+    uint32_t w = (blockIdx.x % kFeatXcds) * a.per_xcd + blockIdx.x / kFeatXcds;
+    if (w >= a.works || blockIdx.x / kFeatXcds >= a.per_xcd) return false;
+    tile = w % a.tiles;
+    w /= a.tiles;
+    split = w % a.splits;
+    w /= a.splits;
+    kv_head = w % a.kv_heads;
+    batch = w / a.kv_heads;
+    return true;
+  }
+};
+
+// The (query, head) of a packed row.
+__device__ __forceinline__ void row_of(const AttnArgs& a, uint32_t kv_head, uint32_t row, uint32_t* query,
+                                       uint32_t* head) {
+  *query = a.share.div(row);
+  *head = kv_head * a.share.d + (row - *query * a.share.d);
+}
+
+__device__ __forceinline__ uint32_t keys_of(const AttnArgs& a, uint32_t batch) {
+  return a.kv_len ? uint32_t(min(max(a.kv_len[batch], 0), int32_t(a.keys))) : a.keys;
+}
+
+// An LDS tile of rows of DP elements, in 16-byte chunks. The chunks of a row are permuted (xor) so that both kinds of
+// reads touch each of the 64 banks once per pass: sixteen rows at one chunk (operand fragments), and four adjacent
+// rows at four adjacent chunks (transposing reads).
+template <typename T, int DP>
+struct Tile {
+  static constexpr int kPer = 16 / int(sizeof(T));  // elements per chunk
+  static constexpr int kChunks = DP / kPer;
+  static constexpr int kRowBytes = DP * int(sizeof(T));
+  static constexpr int kLow = kChunks >= 16 ? 0 : (kChunks == 8 ? 1 : 2);
+
+  __device__ static __forceinline__ int swizzle(int r) {
+    return (((r >> kLow) & ((4 >> kLow) - 1)) << 2) | ((r >> 2) & 3);
+  }
+  __device__ static __forceinline__ int at(int r, int chunk) { return r * kRowBytes + ((chunk ^ swizzle(r)) << 4); }
+
+  // Depths 16 kk + 8 h .. + 7 of row r0 + l % 32.
+  __device__ static __forceinline__ Vec<T, 8> frag(const char* s, int r0, int kk) {
+    const int l = threadIdx.x & 63, r = r0 + (l & 31), h = l >> 5;
+    if constexpr (sizeof(T) == 2) {
+      return *reinterpret_cast<const Vec<T, 8>*>(s + at(r, 2 * kk + h));
+    } else {
+      const Vec<T, 4> a = *reinterpret_cast<const Vec<T, 4>*>(s + at(r, 4 * kk + 2 * h));
+      const Vec<T, 4> b = *reinterpret_cast<const Vec<T, 4>*>(s + at(r, 4 * kk + 2 * h + 1));
+      return Vec<T, 8>{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+  }
+
+  // The transposed fragment: element column 32 dt + l % 32 at rows r0 + 4 h + {0..3} and r0 + 8 + 4 h + {0..3}.
+  __device__ static __forceinline__ Vec<T, 8> frag_t(const char* s, int r0, int dt) {
+    const int l = threadIdx.x & 63, h = l >> 5;
+    if constexpr (sizeof(T) == 2) {
+      // sixteen lanes read four rows of sixteen columns; lane j of them receives column j
+      const int r = r0 + 4 * h + ((l & 15) >> 2), chunk = dt * 4 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1);
+      using s16x4 = Vec<short, 4>;
+      using P = __attribute__((address_space(3))) s16x4*;
+      const Vec<T, 4> a = __builtin_bit_cast(
+          Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(s + at(r, chunk) + (l & 1) * 8)));
+      const Vec<T, 4> b = __builtin_bit_cast(
+          Vec<T, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(s + at(r + 8, chunk) + (l & 1) * 8)));
+      return Vec<T, 8>{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    } else {
+      Vec<T, 8> f;
+      const int c = dt * 32 + (l & 31);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = r0 + 4 * h + (j & 3) + (j >> 2) * 8;
+        f[j] = *reinterpret_cast<const T*>(s + at(r, c / kPer) + (c % kPer) * int(sizeof(T)));
+      }
+      return f;
+    }
+  }
+};
+
+// One 16-byte chunk of a row: elements col .. of `dim`, zeros beyond.
+template <typename T>
+__device__ __forceinline__ u32x4 load_chunk(const T* row, int col, int dim) {
+  constexpr int kPer = 16 / int(sizeof(T));
+  u32x4 r = {0, 0, 0, 0};
+  if (col + kPer <= dim) {
+    __builtin_memcpy(&r, row + col, 16);
+  } else {
+    Vec<T, kPer> e;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = col + i < dim ? row[col + i] : T(0.0f);
+    r = __builtin_bit_cast(u32x4, e);
+  }
+  return r;
+}
+
+// An operand fragment straight from a row in memory.
+template <typename T>
+__device__ __forceinline__ Vec<T, 8> load_frag(const T* row, int kk, int dim) {
+  const int col = 16 * kk + 8 * int((threadIdx.x & 63) >> 5);
+  Vec<T, 8> f;
+  if constexpr (sizeof(T) == 2) {
+    f = __builtin_bit_cast(Vec<T, 8>, load_chunk(row, col, dim));
+  } else {
+    const Vec<T, 4> a = __builtin_bit_cast(Vec<T, 4>, load_chunk(row, col, dim));
+    const Vec<T, 4> b = __builtin_bit_cast(Vec<T, 4>, load_chunk(row, col + 4, dim));
+    f = Vec<T, 8>{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  }
+  return f;
+}
+
+template <typename T>
+__device__ __forceinline__ Vec<T, 8> zero_frag() {
+  Vec<T, 8> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = T(0.0f);
+  return f;
+}
+
+// Values 8 s .. 8 s + 7 of a block, rounded to the features' type, as an operand fragment.
+template <typename T>
+__device__ __forceinline__ Vec<T, 8> to_frag(const f32x16& p, int s) {
+  Vec<T, 8> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = T(p[8 * s + j]);
+  return f;
+}
+
+template <typename T>
+__device__ __forceinline__ bool finite_bits(T x) {
+  if constexpr (sizeof(T) == 4)
+    return (__builtin_bit_cast(uint32_t, x) & 0x7f800000u) != 0x7f800000u;
+  else if constexpr (std::is_same_v<T, _Float16>)
+    return (__builtin_bit_cast(uint16_t, x) & 0x7c00u) != 0x7c00u;
+  else
+    return (__builtin_bit_cast(uint16_t, x) & 0x7f80u) != 0x7f80u;
+}
+
+template <typename T>
+__device__ __forceinline__ bool any_nonfinite(u32x4 c) {
+  constexpr int kPer = 16 / int(sizeof(T));
+  const Vec<T, kPer> e = __builtin_bit_cast(Vec<T, kPer>, c);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) bad |= !finite_bits<T>(e[i]);
+  return bad;
+}
+
+// acc[dt] += (transposed tile rows) * (block p), over the block's 32 rows, which are tile rows r0 ..
+// A masked value is 0 in p, but 0 * NaN is NaN: when the tile holds a non-finite element (guard), its finite elements
+// are multiplied alone, and a result becomes NaN where a non-finite one is visible (bit i of `seen`: value i of the
+// block is visible). Plain code, for the rare tile that needs it.
+template <typename T, int DP>
+__device__ __forceinline__ void contract(f32x16* acc, const char* tile, int r0, const f32x16& p, bool guard,
+                                         uint32_t seen) {
+  using L = Tile<T, DP>;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const Vec<T, 8> b = to_frag<T>(p, s);
+    if (!guard) {
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mma(L::frag_t(tile, r0 + 16 * s, dt), b, acc[dt]);
+    } else {
+      Vec<T, 8> vis;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) vis[j] = T((seen >> (8 * s + j)) & 1 ? 1.0f : 0.0f);
+#pragma unroll
+      for (int dt = 0; dt < DP / 32; ++dt) {
+        Vec<T, 8> a = L::frag_t(tile, r0 + 16 * s, dt), odd;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool fin = finite_bits<T>(a[j]);
+          odd[j] = T(fin ? 0.0f : 1.0f);
+          a[j] = fin ? a[j] : T(0.0f);
+        }
+        acc[dt] = mma(a, b, acc[dt]);
+        f32x16 zero = {};
+        const f32x16 hits = mma(odd, vis, zero);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[dt][i] = hits[i] != 0.0f ? __builtin_nanf("") : acc[dt][i];
+      }
+    }
+  }
+}
+
+// Writes a column's accumulated elements (4 adjacent ones per group of the block) times f.
+template <typename T, int DP>
+__device__ __forceinline__ void store_column(T* row, const f32x16* acc, float f, int dim) {
+  const int h = int(threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = dt * 32 + 8 * g + 4 * h;
+      float v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = acc[dt][4 * g + i] * f;
+      if (d < dim) store_f32<4>(row + d, dim - d, v);
+    }
+}
+
+// Host side (attention_fwd.hip): checks the descriptor and the inputs both directions share and fills the arguments.
+// *nothing is set when there is no query or no element to write.
+gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, const void* k, const void* v,
+                          const int32_t* kv_lengths, const uint8_t* mask, const void* o, const char* who,
+                          AttnArgs* a);
+
+// Fills tiles, splits and the grid of a launch: `tiles` workgroups per key head, split over `steps` tiles of the
+// streamed side when they alone do not fill the compute units.
+inline dim3 attention_grid(AttnArgs* a, uint32_t tiles, uint64_t steps, uint32_t want) {
+  const uint64_t base = uint64_t(tiles) * a->kv_heads * a->batch;
+  a->tiles = tiles;
+  a->splits = uint32_t(std::max<uint64_t>(1, std::min<uint64_t>(steps, want / std::max<uint64_t>(1, base))));
+  a->works = uint32_t(base * a->splits);
+  a->per_xcd = (a->works + kFeatXcds - 1) / kFeatXcds;
+  return dim3(a->per_xcd * kFeatXcds);
+}
+
+// Calls f(element type, padded head dimension, whether there is a mask).
+template <typename F>
+void attention_by_kind(uint32_t dtype, uint32_t dim, bool mask, F f) {
+  auto m = [&](auto t, auto dp) {
+    if (mask)
+      f(t, dp, std::true_type());
+    else
+      f(t, dp, std::false_type());
+  };
+  auto d = [&](auto t) {
+    if (dim <= 32)
+      m(t, std::integral_constant<int, 32>());
+    else if (dim <= 64)
+      m(t, std::integral_constant<int, 64>());
+    else
+      m(t, std::integral_constant<int, 128>());
+  };
+  if (dtype == GSR_F32)
+    d(float());
+  else if (dtype == GSR_F16)
+    d(_Float16());
+  else
+    d(__bf16());
+}
+
+}  // namespace gsr

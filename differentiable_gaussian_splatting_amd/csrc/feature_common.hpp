@@ -1,0 +1,72 @@
+// Element types, wide loads and argument checks shared by the feature operators (group norm, rotary positions, cross
+// attention).
+#pragma once
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+#include <utility>
+
+#include "gsr_internal.hpp"
+
+namespace gsr {
+
+constexpr uint32_t kFeatXcds = 8;  // accelerator dies; workgroups are dealt to them round-robin
+
+// Storage types: float, _Float16, __bf16. Conversions to and from float round to nearest even.
+template <typename T, int N>
+using Vec = T __attribute__((ext_vector_type(N)));
+
+// N adjacent elements as floats in one load of any alignment (global memory takes unaligned wide accesses; 16-byte
+// aligned ones touch the fewest cache lines), or the first `n` of them, the rest 0.
+template <int N, typename T>
+__device__ __forceinline__ void load_f32(const T* p, int n, float* f) {
+  if (n >= N) {
+    Vec<T, N> v;
+    __builtin_memcpy(&v, p, sizeof v);
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = float(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = i < n ? float(p[i]) : 0.0f;
+  }
+}
+
+template <int N, typename T>
+__device__ __forceinline__ void store_f32(T* p, int n, const float* f) {
+  if (n >= N) {
+    Vec<T, N> v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = T(f[i]);
+    __builtin_memcpy(p, &v, sizeof v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i] = T(f[i]);
+  }
+}
+
+inline bool misaligned(const void* p, size_t elem) { return reinterpret_cast<uintptr_t>(p) % elem != 0; }
+
+inline size_t elem_bytes(uint32_t dtype) { return dtype == GSR_F32 ? 4 : 2; }
+
+// Whether the elements of an output with these (stride, extent) pairs and `inner` adjacent elements are distinct:
+// sorted by stride, each stride clears the whole extent below it. Negative strides are refused.
+inline bool distinct(std::initializer_list<std::pair<int64_t, uint64_t>> strides, uint64_t inner) {
+  std::pair<int64_t, uint64_t> s[4];
+  int n = 0;
+  for (auto& e : strides) {
+    if (e.second == 0) return true;
+    if (e.second > 1) s[n++] = e;
+  }
+  std::sort(s, s + n);
+  __int128 span = inner;
+  for (int i = 0; i < n; ++i) {
+    if (s[i].first < 0 || __int128(s[i].first) < span) return false;
+    span += __int128(s[i].first) * __int128(s[i].second - 1);
+  }
+  return span < (__int128(1) << 62);
+}
+
+}  // namespace gsr

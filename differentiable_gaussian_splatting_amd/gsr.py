@@ -30,8 +30,13 @@ GSR_BIN_TILE_DEPTH = 2
 GSR_OPT_FORWARD_EXP, GSR_EXP_EXACT, GSR_EXP_FAST = 11, 0, 1
 (GSR_STAGE_BIN, GSR_STAGE_FORWARD, GSR_STAGE_BACKWARD, GSR_STAGE_ADAM, GSR_STAGE_PROJECT_FORWARD,
  GSR_STAGE_PROJECT_BACKWARD, GSR_STAGE_LOSS, GSR_STAGE_DEPTH_SORT, GSR_STAGE_TILE_SORT, GSR_STAGE_TILE_DEPTH,
- GSR_STAGE_TILE_SCAN) = range(11)
+ GSR_STAGE_TILE_SCAN, GSR_STAGE_GROUP_NORM_FORWARD, GSR_STAGE_GROUP_NORM_BACKWARD, GSR_STAGE_ROTARY,
+ GSR_STAGE_ATTENTION_FORWARD, GSR_STAGE_ATTENTION_BACKWARD) = range(16)
 GSR_ADAM_MAX_GROUPS = 8
+GSR_F32, GSR_F16, GSR_BF16 = 0, 1, 2
+GSR_ACT_NONE, GSR_ACT_SILU, GSR_ACT_RELU = 0, 1, 2
+GSR_ROTARY_INTERLEAVED, GSR_ROTARY_HALVES, GSR_ROTARY_MAX_AXES, GSR_ROTARY_MAX_PAIRS = 0, 1, 4, 128
+GSR_ATTENTION_MAX_DIM = 128
 _STATUS = {GSR_EINVAL: "GSR_EINVAL", GSR_ENOMEM: "GSR_ENOMEM", GSR_EHIP: "GSR_EHIP", GSR_EOVERFLOW: "GSR_EOVERFLOW"}
 
 
@@ -55,6 +60,31 @@ class gsr_adam_group(ctypes.Structure):
 class gsr_camera(ctypes.Structure):
     _fields_ = [("R", ctypes.c_float * 9), ("tv", ctypes.c_float * 3), ("fx", ctypes.c_float),
                 ("fy", ctypes.c_float), ("cx", ctypes.c_float), ("cy", ctypes.c_float), ("near", ctypes.c_float)]
+
+
+class gsr_group_norm(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_uint32), ("images", ctypes.c_uint32), ("pixels", ctypes.c_uint32),
+                ("channels", ctypes.c_uint32), ("groups", ctypes.c_uint32), ("activation", ctypes.c_uint32),
+                ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64 * 2), ("y_stride", ctypes.c_int64 * 2),
+                ("dy_stride", ctypes.c_int64 * 2), ("dx_stride", ctypes.c_int64 * 2)]
+
+
+class gsr_rotary(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_uint32), ("batch", ctypes.c_uint32), ("tokens", ctypes.c_uint32),
+                ("heads", ctypes.c_uint32), ("head_dim", ctypes.c_uint32), ("layout", ctypes.c_uint32),
+                ("axes", ctypes.c_uint32), ("axis_pairs", ctypes.c_uint32 * GSR_ROTARY_MAX_AXES),
+                ("base", ctypes.c_float), ("x_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3),
+                ("position_stride", ctypes.c_int64)]
+
+
+class gsr_attention(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_uint32), ("batch", ctypes.c_uint32), ("heads", ctypes.c_uint32),
+                ("kv_heads", ctypes.c_uint32), ("queries", ctypes.c_uint32), ("keys", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("scale", ctypes.c_float), ("q_stride", ctypes.c_int64 * 3),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3), ("o_stride", ctypes.c_int64 * 3),
+                ("mask_stride", ctypes.c_int64 * 3), ("do_stride", ctypes.c_int64 * 3),
+                ("dq_stride", ctypes.c_int64 * 3), ("dk_stride", ctypes.c_int64 * 3),
+                ("dv_stride", ctypes.c_int64 * 3)]
 
 
 def camera(R, tv, fx: float, fy: float, cx: float, cy: float, near: float = 0.01) -> gsr_camera:
@@ -89,6 +119,12 @@ SIGNATURES = {
     "gsr_project_backward": (_I32, [_P, _P, ctypes.POINTER(gsr_camera), _U32, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                     _P, _P]),
     "gsr_loss_l1_ssim": (_I32, [_P, _P, _U32, _U32, _P, _P, _P, _P]),
+    "gsr_group_norm_forward": (_I32, [_P, _P, ctypes.POINTER(gsr_group_norm)] + [_P] * 5),
+    "gsr_group_norm_backward": (_I32, [_P, _P, ctypes.POINTER(gsr_group_norm)] + [_P] * 8),
+    "gsr_rotary_forward": (_I32, [_P, _P, ctypes.POINTER(gsr_rotary), _P, _P, _P]),
+    "gsr_rotary_backward": (_I32, [_P, _P, ctypes.POINTER(gsr_rotary), _P, _P, _P]),
+    "gsr_cross_attention_forward": (_I32, [_P, _P, ctypes.POINTER(gsr_attention)] + [_P] * 7),
+    "gsr_cross_attention_backward": (_I32, [_P, _P, ctypes.POINTER(gsr_attention)] + [_P] * 11),
 }
 
 _lib = None
@@ -425,3 +461,221 @@ def gsr_loss_l1_ssim(ctx: Context, out_rgba: torch.Tensor, target: torch.Tensor,
     ctx.check(load().gsr_loss_l1_ssim(ctx.handle, _stream(stream), W, H, _ptr(out_rgba), _ptr(target), _ptr(v_out),
                                       _ptr(loss)), "gsr_loss_l1_ssim")
     return v_out, loss
+
+
+_DTYPES = {torch.float32: GSR_F32, torch.float16: GSR_F16, torch.bfloat16: GSR_BF16}
+
+
+def _need_feature(t, name, device, dtype=None, shape=None):
+    """A strided feature tensor: on the device, of a supported (or the given) dtype, its last dimension adjacent."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in _DTYPES if dtype is None else t.dtype != dtype:
+        raise TypeError(f"{name} must have dtype {tuple(_DTYPES) if dtype is None else dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be adjacent in memory")
+
+
+def _image_strides(t, name):
+    """(image, pixel) strides of [N, ..., C] features whose dimensions between form one run of pixels."""
+    if t.is_contiguous():
+        pixels = 1
+        for n in t.shape[1:-1]:
+            pixels *= n
+        return pixels * t.shape[-1], t.shape[-1]
+    pixel, run = 0, None
+    for n, st in zip(reversed(t.shape[1:-1]), reversed(t.stride()[1:-1])):
+        if n == 1:
+            continue
+        if run is None:
+            pixel = st
+        elif st != run:
+            raise ValueError(f"the pixels of {name} must be evenly spaced in memory")
+        run = st * n
+    return t.stride(0), pixel
+
+
+def _group_norm_desc(ctx, x, gamma, beta, groups, eps, activation):
+    dev = ctx.device
+    _need_feature(x, "x", dev)
+    if x.dim() < 2:
+        raise ValueError("x must be [images, ..., channels]")
+    C = x.shape[-1]
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _need(t, name, (torch.float32,), C, dev)
+    pixels = 1
+    for n in x.shape[1:-1]:
+        pixels *= n
+    d = gsr_group_norm(_DTYPES[x.dtype], x.shape[0], pixels, C, groups, activation, eps)
+    d.x_stride[:] = _image_strides(x, "x")
+    return d
+
+
+def gsr_group_norm_forward(ctx: Context, x: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Tensor | None,
+                           groups: int, eps: float = 1e-5, activation: int = GSR_ACT_NONE,
+                           y: torch.Tensor | None = None, stats: torch.Tensor | None = None, stream=None):
+    """Group norm and activation of channels-last features x [N, ..., C] (float32, float16 or bfloat16; gamma and beta
+    float32 [C] or None). Returns (y like x, stats float32 [N, groups, 2] = (mean, rstd))."""
+    d = _group_norm_desc(ctx, x, gamma, beta, groups, eps, activation)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if stats is None:
+        stats = torch.empty((x.shape[0], groups, 2), dtype=torch.float32, device=x.device)
+    _need_feature(y, "y", ctx.device, x.dtype, x.shape)
+    _need(stats, "stats", (torch.float32,), x.shape[0] * groups * 2, ctx.device)
+    d.y_stride[:] = _image_strides(y, "y")
+    ctx.check(load().gsr_group_norm_forward(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(x), _ptr(gamma),
+                                            _ptr(beta), _ptr(y), _ptr(stats)), "gsr_group_norm_forward")
+    return y, stats
+
+
+def gsr_group_norm_backward(ctx: Context, x: torch.Tensor, gamma: torch.Tensor | None, beta: torch.Tensor | None,
+                            groups: int, stats: torch.Tensor, dy: torch.Tensor, activation: int = GSR_ACT_NONE,
+                            dx: torch.Tensor | None = None, dgamma: torch.Tensor | None = None,
+                            dbeta: torch.Tensor | None = None, stream=None):
+    """Returns (dx like x, dgamma float32 [C], dbeta float32 [C]) for the upstream gradient dy (like x)."""
+    d = _group_norm_desc(ctx, x, gamma, beta, groups, 0.0, activation)
+    dev, C = ctx.device, x.shape[-1]
+    _need(stats, "stats", (torch.float32,), x.shape[0] * groups * 2, dev)
+    _need_feature(dy, "dy", dev, x.dtype, x.shape)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if dgamma is None:
+        dgamma = torch.empty(C, dtype=torch.float32, device=dev)
+    if dbeta is None:
+        dbeta = torch.empty(C, dtype=torch.float32, device=dev)
+    _need_feature(dx, "dx", dev, x.dtype, x.shape)
+    _need(dgamma, "dgamma", (torch.float32,), C, dev)
+    _need(dbeta, "dbeta", (torch.float32,), C, dev)
+    d.dy_stride[:] = _image_strides(dy, "dy")
+    d.dx_stride[:] = _image_strides(dx, "dx")
+    ctx.check(load().gsr_group_norm_backward(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(x), _ptr(gamma),
+                                             _ptr(beta), _ptr(stats), _ptr(dy), _ptr(dx), _ptr(dgamma), _ptr(dbeta)),
+              "gsr_group_norm_backward")
+    return dx, dgamma, dbeta
+
+
+def _rotary(ctx, x, positions, axis_pairs, base, layout, out, stream, name):
+    dev = ctx.device
+    _need_feature(x, "x", dev)
+    if x.dim() != 4:
+        raise ValueError("x must be [batch, tokens, heads, head_dim]")
+    B, T, H, D = x.shape
+    axes = len(axis_pairs)
+    if not 1 <= axes <= GSR_ROTARY_MAX_AXES:
+        raise ValueError(f"1 to {GSR_ROTARY_MAX_AXES} axes are supported, got {axes}")
+    if not isinstance(positions, torch.Tensor) or positions.dim() != 3 or tuple(positions.shape[1:]) != (T, axes) \
+            or positions.shape[0] not in (1, B):
+        raise ValueError(f"positions must be float32 [{B} or 1, {T}, {axes}]")
+    _need(positions, "positions", (torch.float32,), None, dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    _need_feature(out, "out", dev, x.dtype, x.shape)
+    d = gsr_rotary(_DTYPES[x.dtype], B, T, H, D, layout, axes)
+    d.axis_pairs[:axes] = axis_pairs
+    d.base = base
+    d.x_stride[:] = x.stride()[:3]
+    d.out_stride[:] = out.stride()[:3]
+    d.position_stride = T * axes if positions.shape[0] == B else 0
+    ctx.check(getattr(load(), name)(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(x), _ptr(positions),
+                                    _ptr(out)), name)
+    return out
+
+
+def gsr_rotary_forward(ctx: Context, x: torch.Tensor, positions: torch.Tensor, axis_pairs, base: float = 10000.0,
+                       layout: int = GSR_ROTARY_INTERLEAVED, out: torch.Tensor | None = None, stream=None):
+    """Turns the pairs of x [B, T, H, D] by positions float32 [B or 1, T, axes]; axis_pairs deals the pairs to the
+    axes. `out` may be x. Returns out."""
+    return _rotary(ctx, x, positions, axis_pairs, base, layout, out, stream, "gsr_rotary_forward")
+
+
+def gsr_rotary_backward(ctx: Context, dout: torch.Tensor, positions: torch.Tensor, axis_pairs, base: float = 10000.0,
+                        layout: int = GSR_ROTARY_INTERLEAVED, dx: torch.Tensor | None = None, stream=None):
+    """The gradient of gsr_rotary_forward with respect to x: the pairs of dout turned back. `dx` may be dout."""
+    return _rotary(ctx, dout, positions, axis_pairs, base, layout, dx, stream, "gsr_rotary_backward")
+
+
+def _attention_desc(ctx, q, k, v, scale, kv_lengths, mask):
+    dev = ctx.device
+    _need_feature(q, "q", dev)
+    if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("q must be [batch, queries, heads, dim], k and v [batch, keys, kv_heads, dim]")
+    B, Tq, H, D = q.shape
+    Tk, Hk = k.shape[1], k.shape[2]
+    _need_feature(k, "k", dev, q.dtype, (B, Tk, Hk, D))
+    _need_feature(v, "v", dev, q.dtype, (B, Tk, Hk, D))
+    if kv_lengths is not None:
+        _need(kv_lengths, "kv_lengths", (torch.int32,), B, dev)
+    d = gsr_attention(_DTYPES[q.dtype], B, H, Hk, Tq, Tk, D, D ** -0.5 if scale is None else scale)
+    d.q_stride[:] = q.stride()[:3]
+    d.k_stride[:] = k.stride()[:3]
+    d.v_stride[:] = v.stride()[:3]
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dim() != 4 or mask.shape[3] != Tk or \
+                any(m not in (1, n) for m, n in zip(mask.shape, (B, H, Tq))):
+            raise ValueError(f"mask must be [{B} or 1, {H} or 1, {Tq} or 1, {Tk}]")
+        if mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"mask must have dtype torch.bool or torch.uint8, got {mask.dtype}")
+        if mask.device != dev:
+            raise ValueError(f"mask is on {mask.device}, expected {dev}")
+        if Tk > 1 and mask.stride(3) != 1:
+            raise ValueError("the last dimension of mask must be adjacent in memory")
+        d.mask_stride[:] = [0 if m == 1 else st for m, st in zip(mask.shape, mask.stride()[:3])]
+    return d
+
+
+def gsr_cross_attention_forward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                scale: float | None = None, kv_lengths: torch.Tensor | None = None,
+                                mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                                lse: torch.Tensor | None = None, stream=None):
+    """Attention of q [B, Tq, H, D] to k, v [B, Tk, Hk, D] (H a multiple of Hk; scale 1/sqrt(D) by default) over the
+    keys below kv_lengths int32 [B] where mask (bool or uint8, broadcastable [B, H, Tq, Tk]) is not 0. Returns
+    (out like q, lse float32 [B, H, Tq])."""
+    d = _attention_desc(ctx, q, k, v, scale, kv_lengths, mask)
+    B, Tq, H, _ = q.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
+    _need_feature(out, "out", ctx.device, q.dtype, q.shape)
+    _need(lse, "lse", (torch.float32,), B * H * Tq, ctx.device)
+    d.o_stride[:] = out.stride()[:3]
+    ctx.check(load().gsr_cross_attention_forward(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(q), _ptr(k),
+                                                 _ptr(v), _ptr(kv_lengths), _ptr(mask), _ptr(out), _ptr(lse)),
+              "gsr_cross_attention_forward")
+    return out, lse
+
+
+def gsr_cross_attention_backward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                                 lse: torch.Tensor, dout: torch.Tensor, scale: float | None = None,
+                                 kv_lengths: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                                 dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                                 dv: torch.Tensor | None = None, stream=None):
+    """Returns (dq, dk, dv), shaped like q, k and v, from the forward's inputs and results and dout (like q)."""
+    d = _attention_desc(ctx, q, k, v, scale, kv_lengths, mask)
+    dev = ctx.device
+    B, Tq, H, _ = q.shape
+    _need_feature(out, "out", dev, q.dtype, q.shape)
+    _need_feature(dout, "dout", dev, q.dtype, q.shape)
+    _need(lse, "lse", (torch.float32,), B * H * Tq, dev)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    if dv is None:
+        dv = torch.empty(v.shape, dtype=q.dtype, device=dev)
+    for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        _need_feature(t, name, dev, q.dtype, like.shape)
+    for field, t in (("o_stride", out), ("do_stride", dout), ("dq_stride", dq), ("dk_stride", dk),
+                     ("dv_stride", dv)):
+        getattr(d, field)[:] = t.stride()[:3]
+    ctx.check(load().gsr_cross_attention_backward(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(q), _ptr(k),
+                                                  _ptr(v), _ptr(kv_lengths), _ptr(mask), _ptr(out), _ptr(lse),
+                                                  _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv)),
+              "gsr_cross_attention_backward")
+    return dq, dk, dv

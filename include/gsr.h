@@ -8,7 +8,9 @@
  *                       binned in the view)
  * and, on either side of it, the projection of 3D Gaussians to those splats and the projection's backward pass
  * (gsr_project_forward / gsr_project_backward), and the L1 + SSIM loss that gives the backward its v_out
- * (gsr_loss_l1_ssim).
+ * (gsr_loss_l1_ssim). For models that predict splats from images, in front of the projection: group norm with an
+ * activation over channels-last feature maps (gsr_group_norm_*), rotary positions with several axes (gsr_rotary_*)
+ * and cross attention from splat queries to image tokens (gsr_cross_attention_*), each with its backward pass.
  *
  * Conventions shared by every entry point
  *   - Pointers named as device pointers must point to memory allocated on the context's device (hipMalloc or a
@@ -149,7 +151,12 @@ gsr_status gsr_set_option(gsr_ctx* ctx, int32_t option, int64_t value);
                                      /*   tile-first scheme                                                      */
 #define GSR_STAGE_TILE_SCAN 10       /* inside gsr_bin: the column scan and list starts of the tile-first        */
                                      /*   scheme's counting sort (its scatter is GSR_STAGE_TILE_SORT)            */
-#define GSR_NUM_STAGES 11
+#define GSR_STAGE_GROUP_NORM_FORWARD 11  /* the kernels of gsr_group_norm_forward                                */
+#define GSR_STAGE_GROUP_NORM_BACKWARD 12 /* the kernels of gsr_group_norm_backward                               */
+#define GSR_STAGE_ROTARY 13              /* the rotary kernel, either direction                                  */
+#define GSR_STAGE_ATTENTION_FORWARD 14   /* the kernels of gsr_cross_attention_forward                           */
+#define GSR_STAGE_ATTENTION_BACKWARD 15  /* the kernels of gsr_cross_attention_backward                          */
+#define GSR_NUM_STAGES 16
 
 /* GPU durations in milliseconds of the recorded launches of `stage`, oldest first: the last min(recorded, ring
  * size, max) of them. Waits for the newest one to finish. *count = the number written.
@@ -370,6 +377,132 @@ gsr_status gsr_project_backward(gsr_ctx* ctx, void* stream, const gsr_camera* ca
  * Errors: GSR_EINVAL (null pointers, empty image, misalignment), GSR_ENOMEM, GSR_EHIP. */
 gsr_status gsr_loss_l1_ssim(gsr_ctx* ctx, void* stream, uint32_t width, uint32_t height, const float* out_rgba,
                             const float* target, float* v_out, float* loss);
+
+/* ---------------------------------------------------------------------------------------------------------------
+ * Operators of models that predict splats from images. Features are float32, float16 or bfloat16; sums, softmax
+ * statistics and normalisation statistics are float32, and a 16-bit result is rounded once, to nearest even. All of
+ * them give the same bits on every run. Strides count elements; outputs must not overlap themselves or an input
+ * (except where stated), which is checked for an output's own strides. Any pointer aligned to its element works;
+ * pointers and strides of whole 16 bytes are fastest. */
+#define GSR_F32 0
+#define GSR_F16 1
+#define GSR_BF16 2
+
+#define GSR_ACT_NONE 0
+#define GSR_ACT_SILU 1 /* z / (1 + exp(-z))                     */
+#define GSR_ACT_RELU 2 /* max(z, 0), derivative 0 at 0, NaN kept */
+
+/* Group norm over channels-last features x[image][pixel][channel], then an activation: with mean and var the mean and
+ * the (biased) variance of the pixels * channels / groups values of one image and group,
+ *   rstd = 1 / sqrt(var + eps);  z = (x - mean) rstd gamma[channel] + beta[channel];  y = act(z).
+ * Strides are those of an image and of a pixel; channels are adjacent. */
+typedef struct gsr_group_norm {
+  uint32_t dtype;      /* GSR_F32, GSR_F16 or GSR_BF16: x, y, dy, dx. gamma, beta and their gradients are float32 */
+  uint32_t images, pixels, channels, groups; /* channels a multiple of groups; pixels = height * width            */
+  uint32_t activation; /* GSR_ACT_*                                                                               */
+  float eps;           /* >= 0                                                                                    */
+  int64_t x_stride[2], y_stride[2];   /* (image, pixel)                                                           */
+  int64_t dy_stride[2], dx_stride[2]; /* read by the backward only                                                */
+} gsr_group_norm;
+
+/*   gamma, beta  device [channels] float32, either may be NULL (1 and 0)
+ *   y            written; may be x itself (same strides)
+ *   stats        device [images][groups][2] float32, written: (mean, rstd), for the backward
+ * images, pixels or channels of 0 write nothing. The variance is taken about the mean (no difference of squares), so
+ * features whose mean is far from 0 lose nothing. Uses the context arena as scratch.
+ * Errors: GSR_EINVAL (null pointers, channels not a multiple of groups, unknown dtype or activation, eps < 0 or NaN,
+ * output strides that overlap, pointers not aligned to their element), GSR_EOVERFLOW (pixels * channels / groups >=
+ * 2^31 or images >= 2^16), GSR_ENOMEM, GSR_EHIP. */
+gsr_status gsr_group_norm_forward(gsr_ctx* ctx, void* stream, const gsr_group_norm* desc, const void* x,
+                                  const float* gamma, const float* beta, void* y, float* stats);
+
+/* Backward pass: with xh = (x - mean) rstd, dz = dy act'(z), and over the M = pixels * channels / groups values of an
+ * image and group, dgamma = sum dz xh and dbeta = sum dz (over images and pixels), and
+ *   dx = rstd (dz gamma - (mean of dz gamma) - xh (mean of dz gamma xh)).
+ *   stats   as written by the forward;  dy as y
+ *   dx      written, or NULL to skip it; may be dy itself (same strides)
+ *   dgamma, dbeta  device [channels] float32, overwritten, either may be NULL
+ * Errors: as gsr_group_norm_forward. */
+gsr_status gsr_group_norm_backward(gsr_ctx* ctx, void* stream, const gsr_group_norm* desc, const void* x,
+                                   const float* gamma, const float* beta, const float* stats, const void* dy,
+                                   void* dx, float* dgamma, float* dbeta);
+
+#define GSR_ROTARY_MAX_AXES 4
+#define GSR_ROTARY_MAX_PAIRS 128
+#define GSR_ROTARY_INTERLEAVED 0 /* pair i is elements (2 i, 2 i + 1)                                             */
+#define GSR_ROTARY_HALVES 1      /* pair i is elements (i, i + pairs), pairs the sum over the axes                 */
+
+/* Rotary positions with several axes (time or view, height, width). The pairs of a head are dealt to the axes in
+ * order, axis_pairs[a] to axis a; pair i of axis a turns by the angle p base^(-i / axis_pairs[a]), p the token's
+ * position on that axis:  (u, v) -> (u cos - v sin, u sin + v cos). Elements beyond twice the pairs are copied.
+ * Strides are those of a batch entry, a token and a head; a head's elements are adjacent. */
+typedef struct gsr_rotary {
+  uint32_t dtype; /* x and out */
+  uint32_t batch, tokens, heads, head_dim;
+  uint32_t layout; /* GSR_ROTARY_INTERLEAVED or GSR_ROTARY_HALVES                                                 */
+  uint32_t axes;   /* 1 .. GSR_ROTARY_MAX_AXES                                                                    */
+  uint32_t axis_pairs[GSR_ROTARY_MAX_AXES]; /* their sum at most head_dim / 2 and GSR_ROTARY_MAX_PAIRS             */
+  float base;      /* > 0                                                                                         */
+  int64_t x_stride[3], out_stride[3]; /* (batch entry, token, head)                                               */
+  int64_t position_stride;            /* of a batch entry in `positions`; 0 shares one set                        */
+} gsr_rotary;
+
+/*   positions  device [batch][tokens][axes] float32 (any value, whole or not)
+ *   out        written; may be x itself (same strides)
+ * The angle is reduced to a turn with an exact remainder, so a position costs no accuracy up to 2^24.
+ * Errors: GSR_EINVAL (null pointers, axes or pairs out of range, base not > 0, overlapping output strides, pointers
+ * not aligned to their element), GSR_EOVERFLOW (batch * tokens >= 2^31), GSR_EHIP. */
+gsr_status gsr_rotary_forward(gsr_ctx* ctx, void* stream, const gsr_rotary* desc, const void* x,
+                              const float* positions, void* out);
+
+/* The gradient: each pair turned back by its angle (the transposed rotation), dout read with x_stride and dx written
+ * with out_stride. dx may be dout itself (same strides). Errors: as gsr_rotary_forward. */
+gsr_status gsr_rotary_backward(gsr_ctx* ctx, void* stream, const gsr_rotary* desc, const void* dout,
+                               const float* positions, void* dx);
+
+#define GSR_ATTENTION_MAX_DIM 128
+
+/* Cross attention of queries to the states of an encoder. For batch entry b, head h and query t, over the keys j that
+ * are visible to it (j < kv_lengths[b] and mask(b, h, t, j) != 0), with the key head h / (heads / kv_heads):
+ *   s_j = scale q.k_j;  lse = log sum_j exp(s_j);  p_j = exp(s_j - lse);  o = sum_j p_j v_j.
+ * A query that sees no key gets o = 0, lse = -inf and no gradient. What lies at a key that is not visible (NaN and
+ * infinities too) changes nothing. Strides are those of a batch entry, a token and a head (0 broadcasts an input);
+ * a head's elements are adjacent. The mask's strides are those of a batch entry, a head and a query, its keys are
+ * adjacent bytes. */
+typedef struct gsr_attention {
+  uint32_t dtype; /* q, k, v, o and their gradients */
+  uint32_t batch, heads, kv_heads; /* heads a multiple of kv_heads                                                */
+  uint32_t queries, keys;          /* either may be 0                                                             */
+  uint32_t head_dim;               /* 1 .. GSR_ATTENTION_MAX_DIM                                                  */
+  float scale;                     /* finite, > 0                                                                 */
+  int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3]; /* (batch entry, token, head)                       */
+  int64_t mask_stride[3];                                     /* (batch entry, head, query), 0 broadcasts         */
+  int64_t do_stride[3], dq_stride[3], dk_stride[3], dv_stride[3]; /* read by the backward only                    */
+} gsr_attention;
+
+/*   kv_lengths  device [batch] int32 (clamped to [0, keys]), or NULL: all keys
+ *   mask        device bytes, or NULL: all visible
+ *   o           written;  lse  device [batch][heads][queries] float32, written (for the backward), or NULL
+ * 16-bit features are multiplied on the matrix cores with float32 sums; the probabilities are rounded to the
+ * features' type before their product with v. float32 features are multiplied as float32.
+ * Uses the context arena as scratch when few queries meet many keys (the keys are then split and joined).
+ * Errors: GSR_EINVAL (null pointers, head counts, head_dim or scale out of range, overlapping output strides,
+ * pointers not aligned to their element), GSR_EOVERFLOW (batch * heads * queries or batch * keys * kv_heads >=
+ * 2^31), GSR_ENOMEM, GSR_EHIP. */
+gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, const gsr_attention* desc, const void* q,
+                                       const void* k, const void* v, const int32_t* kv_lengths, const uint8_t* mask,
+                                       void* o, float* lse);
+
+/* Backward pass: dv_j = sum p_j do;  ds_j = scale p_j (do.v_j - do.o);  dq = sum_j ds_j k_j;  dk_j = sum ds_j q, the
+ * sums for a key over the queries of every head that shares it. Gradients of an input broadcast over a stride of 0
+ * are those of each copy.
+ *   o, lse  as written by the forward for the same inputs;  do (`dout`) as o
+ *   dq, dk, dv  written (zero where nothing is visible)
+ * Uses the context arena as scratch. Errors: as gsr_cross_attention_forward. */
+gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, const gsr_attention* desc, const void* q,
+                                        const void* k, const void* v, const int32_t* kv_lengths,
+                                        const uint8_t* mask, const void* o, const float* lse, const void* dout,
+                                        void* dq, void* dk, void* dv);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,227 @@
+"""GPU group norm with an activation against the fp64 oracle (oracle/features.py), element by element within the
+oracle's float32 error bound plus the result's own rounding to its type."""
+import ctypes
+
+import pytest
+import torch
+
+from featurehelp import DTYPES, normal, within
+from gpuhelp import banner
+from oracle import features as of
+
+pytestmark = pytest.mark.gpu
+KIND = {"none": 0, "silu": 1, "relu": 2}
+
+
+@pytest.fixture(scope="module")
+def ctx():
+    from differentiable_gaussian_splatting_amd import gsr
+    c = gsr.Context(0)
+    yield c
+    c.close()
+
+
+def features(seed, n, p, c, dtype, centre=0.7):
+    """Each channel with a centre and a scale of its own."""
+    x = normal(seed, (n, p, c)) * (0.5 + normal(seed + 1, (c,)).abs()) + centre * normal(seed + 2, (c,))
+    return x.to(dtype)
+
+
+def check(ctx, x, gamma, beta, groups, kind, dy, got, eps=1e-5):
+    from differentiable_gaussian_splatting_amd import gsr  # noqa: F401
+    r = of.group_norm(x.double(), None if gamma is None else gamma.double(), None if beta is None else beta.double(),
+                      groups, eps, kind, dy.double())
+    u, tiny = of.ROUND[x.dtype], of.TINY[x.dtype]
+    y, stats, dx, dgamma, dbeta = got
+    within(stats[..., 0], r["mean"], r["e_mean"], "mean")
+    within(stats[..., 1], r["rstd"], r["e_rstd"], "rstd")
+    for name, t in (("y", y), ("dx", dx)):
+        within(t, r[name], r["e_" + name] + u * r[name].abs() + tiny, name)
+    within(dgamma, r["dgamma"], r["e_dgamma"] + of.U32 * r["dgamma"].abs(), "dgamma")
+    within(dbeta, r["dbeta"], r["e_dbeta"] + of.U32 * r["dbeta"].abs(), "dbeta")
+
+
+def both(ctx, x, gamma, beta, groups, kind, dy, eps=1e-5, **kw):
+    from differentiable_gaussian_splatting_amd import gsr
+    d = lambda t: None if t is None else t.cuda()  # noqa: E731
+    y, stats = gsr.gsr_group_norm_forward(ctx, d(x), d(gamma), d(beta), groups, eps, KIND[kind])
+    return (y, stats) + gsr.gsr_group_norm_backward(ctx, d(x), d(gamma), d(beta), groups, stats, d(dy), KIND[kind])
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("n,p,c,groups", [
+    (1, 1, 1, 1), (1, 1, 8, 2), (2, 3, 6, 6), (1, 63, 32, 8), (3, 323, 90, 9), (2, 1000, 40, 4), (1, 65, 2052, 12),
+    (1, 257, 33, 3), (5, 7, 320, 32), (1, 2500, 64, 1), (2, 4096, 16, 16), (1, 20000, 8, 2), (70, 5, 24, 3),
+    (1, 30, 4100, 2)])
+def test_sizes(ctx, dtype, n, p, c, groups):
+    banner(f"group norm {dtype} {n}x{p}x{c} groups {groups}")
+    t = DTYPES[dtype]
+    x, dy = features(n + p, n, p, c, t), normal(p + c, (n, p, c), t)
+    gamma, beta = 1 + 0.2 * normal(1, (c,)), normal(2, (c,))
+    check(ctx, x, gamma, beta, groups, "silu", dy, both(ctx, x, gamma, beta, groups, "silu", dy))
+
+
+@pytest.mark.parametrize("kind", ["none", "relu", "silu"])
+@pytest.mark.parametrize("affine", [False, True])
+def test_activations_with_and_without_affine(ctx, kind, affine):
+    banner(f"group norm {kind} affine {affine}")
+    x, dy = features(3, 2, 150, 24, torch.float32), normal(4, (2, 150, 24))
+    gamma, beta = (normal(5, (24,)), normal(6, (24,))) if affine else (None, None)
+    check(ctx, x, gamma, beta, 4, kind, dy, both(ctx, x, gamma, beta, 4, kind, dy))
+
+
+def test_a_far_mean_and_an_outlier_cost_no_variance(ctx):
+    banner("group norm far mean, outlying first value")
+    x = (1000 + normal(1, (1, 900, 16)))
+    x[0, 0, :] = 1e5  # the shift of the sums of the first thread
+    dy = normal(2, (1, 900, 16))
+    check(ctx, x, None, None, 2, "none", dy, both(ctx, x, None, None, 2, "none", dy))
+
+
+def test_constant_features(ctx):
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("group norm of a constant")
+    x = torch.full((2, 500, 12), 3.25, device="cuda")
+    y, stats = gsr.gsr_group_norm_forward(ctx, x, None, None, 3, 1e-5)
+    assert (y == 0).all() and (stats[..., 0] == 3.25).all()
+    assert torch.allclose(stats[..., 1].cpu(), torch.tensor(1e-5).rsqrt(), rtol=1e-6)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_value_stays_in_its_group(ctx, bad):
+    banner(f"group norm with a {bad}")
+    x, dy = features(3, 2, 700, 24, torch.float32), normal(4, (2, 700, 24))
+    clean = both(ctx, x, None, None, 4, "silu", dy)
+    x2 = x.clone()
+    x2[1, 350, 13] = bad  # group 2 of image 1
+    y, stats, dx, _, _ = both(ctx, x2, None, None, 4, "silu", dy)
+    hit = torch.zeros(2, 4, dtype=torch.bool)
+    hit[1, 2] = True
+    assert torch.equal(stats[..., 1].isnan().cpu(), hit)
+    wide = hit.repeat_interleave(6, 1)[:, None, :].expand(2, 700, 24)
+    for got, ref in ((y, clean[0]), (dx, clean[2])):
+        assert got.cpu()[wide].isnan().all() and torch.equal(got.cpu()[~wide], ref.cpu()[~wide])
+
+
+def test_strided_and_in_place(ctx):
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("group norm strided, in place")
+    wide = features(3, 2, 6 * 11, 40, torch.bfloat16).reshape(2, 6, 11, 40).cuda()
+    x = wide[..., 3:27]  # a channel slice, not 16-byte aligned
+    dy = normal(4, (2, 6, 11, 24), torch.bfloat16).cuda()
+    gamma, beta = normal(5, (24,)).cuda(), normal(6, (24,)).cuda()
+    y, stats = gsr.gsr_group_norm_forward(ctx, x, gamma, beta, 4, 1e-5, 1)
+    xc = x.contiguous()
+    y2, stats2 = gsr.gsr_group_norm_forward(ctx, xc, gamma, beta, 4, 1e-5, 1)
+    assert torch.equal(y, y2) and torch.equal(stats, stats2)
+    dx, dg, db = gsr.gsr_group_norm_backward(ctx, x, gamma, beta, 4, stats, dy, 1)
+    ref = both(ctx, xc.cpu().reshape(2, 66, 24), gamma.cpu(), beta.cpu(), 4, "silu", dy.cpu().reshape(2, 66, 24))
+    assert torch.equal(dx.reshape(2, 66, 24), ref[2]) and torch.equal(dg, ref[3]) and torch.equal(db, ref[4])
+    keep = dy.clone()
+    gsr.gsr_group_norm_backward(ctx, x, gamma, beta, 4, stats, keep, 1, dx=keep)
+    assert torch.equal(keep, dx)
+    before = wide.clone()
+    gsr.gsr_group_norm_forward(ctx, x, gamma, beta, 4, 1e-5, 1, y=x)
+    assert torch.equal(x, y)
+    assert torch.equal(wide[..., :3], before[..., :3]) and torch.equal(wide[..., 27:], before[..., 27:])
+    # one image broadcast over the batch
+    b = xc[:1].expand(3, 6, 11, 24)
+    yb, _ = gsr.gsr_group_norm_forward(ctx, b, gamma, beta, 4, 1e-5, 1)
+    assert all(torch.equal(yb[i], y[0]) for i in range(3))
+
+
+def test_repeats_on_another_stream(ctx):
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("group norm on another stream, repeated")
+    x, dy = features(3, 2, 5000, 48, torch.float16).cuda(), normal(4, (2, 5000, 48), torch.float16).cuda()
+    y, st = gsr.gsr_group_norm_forward(ctx, x, None, None, 6, 1e-5, 1)
+    ref = gsr.gsr_group_norm_backward(ctx, x, None, None, 6, st, dy, 1)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        y2, st2 = gsr.gsr_group_norm_forward(ctx, x, None, None, 6, 1e-5, 1, stream=s)
+        got = gsr.gsr_group_norm_backward(ctx, x, None, None, 6, st2, dy, 1, stream=s)
+        s.synchronize()
+        assert torch.equal(y, y2) and torch.equal(st, st2) and all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+def test_graph_replays(ctx):
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("group norm in a graph")
+    x, dy = features(3, 2, 3000, 48, torch.float32).cuda(), normal(4, (2, 3000, 48)).cuda()
+    y, st = gsr.gsr_group_norm_forward(ctx, x, None, None, 6, 1e-5, 1)
+    ref = (y, st) + gsr.gsr_group_norm_backward(ctx, x, None, None, 6, st, dy, 1)
+    ref = [t.clone() for t in ref]
+    bufs = [torch.empty_like(t) for t in ref]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gsr.gsr_group_norm_forward(ctx, x, None, None, 6, 1e-5, 1, y=bufs[0], stats=bufs[1])
+        gsr.gsr_group_norm_backward(ctx, x, None, None, 6, bufs[1], dy, 1, *bufs[2:])
+    for i in range(3):
+        for b in bufs:
+            b.fill_(float(i))
+        both(ctx, x.cpu()[:1], None, None, 6, "silu", dy.cpu()[:1])  # the same arena, other contents
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(ref, bufs)), i
+
+
+def test_no_pixels_and_optional_outputs(ctx):
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("group norm of nothing")
+    for shape in ((0, 5, 12), (3, 0, 12)):
+        x = torch.empty(shape, device="cuda")
+        y, st = gsr.gsr_group_norm_forward(ctx, x, None, None, 3)
+        assert y.shape == x.shape
+        out = gsr.gsr_group_norm_backward(ctx, x, None, None, 3, st, x, dgamma=torch.ones(12, device="cuda"),
+                                          dbeta=torch.ones(12, device="cuda"))
+        assert (out[1] == 0).all() and (out[2] == 0).all()
+    # dgamma and dbeta alone, and dx alone, give the same values
+    x, dy = features(3, 2, 300, 24, torch.float32).cuda(), normal(4, (2, 300, 24)).cuda()
+    y, st = gsr.gsr_group_norm_forward(ctx, x, None, None, 3, 1e-5, 1)
+    ref = gsr.gsr_group_norm_backward(ctx, x, None, None, 3, st, dy, 1)
+    d = gsr._group_norm_desc(ctx, x, None, None, 3, 0.0, 1)
+    d.dy_stride[:] = d.dx_stride[:] = d.x_stride[:]
+    p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    for use in ((False, True, False), (False, False, True), (True, False, False)):
+        got = [torch.empty_like(t) if u else None for t, u in zip(ref, use)]
+        assert gsr.load().gsr_group_norm_backward(ctx.handle, gsr._stream(None), ctypes.byref(d), p(x), None, None,
+                                                  p(st), p(dy), *[p(t) for t in got]) == 0
+        torch.cuda.synchronize()
+        assert all(g is None or torch.equal(g, r) for g, r in zip(got, ref))
+
+
+def test_refusals(ctx):
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("group norm refusals")
+    x = torch.zeros((2, 10, 12), device="cuda")
+    fwd = lambda *a, **k: gsr.gsr_group_norm_forward(ctx, *a, **k)  # noqa: E731
+    for args in ((x, None, None, 5), (x, None, None, 0), (x, None, None, 3, -1.0), (x, None, None, 3, float("nan")),
+                 (x, None, None, 3, 1e-5, 7)):
+        with pytest.raises(gsr.GsrError) as e:
+            fwd(*args)
+        assert e.value.status == gsr.GSR_EINVAL
+    with pytest.raises(gsr.GsrError, match="overlap"):
+        fwd(x, None, None, 3, y=torch.zeros((1, 10, 12), device="cuda").expand(2, 10, 12))
+    with pytest.raises(TypeError):
+        fwd(x.double(), None, None, 3)
+    with pytest.raises(TypeError):
+        fwd(x, torch.ones(12, device="cuda", dtype=torch.float16), None, 3)
+    with pytest.raises(ValueError):
+        fwd(x, torch.ones(11, device="cuda"), None, 3)
+    with pytest.raises(ValueError):
+        fwd(x.cpu(), None, None, 3)
+    with pytest.raises(ValueError, match="adjacent"):
+        fwd(x.transpose(1, 2), None, None, 2)
+    with pytest.raises(ValueError, match="evenly"):
+        fwd(torch.zeros((2, 6, 8, 12), device="cuda")[:, :, :5], None, None, 3)
+    lib, h = gsr.load(), ctx.handle
+    d = gsr.gsr_group_norm(0, 1, 1 << 31, 4, 4, 0, 1e-5)
+    assert lib.gsr_group_norm_forward(h, None, ctypes.byref(d), *[None] * 5) == gsr.GSR_EOVERFLOW
+    d = gsr.gsr_group_norm(0, 1 << 16, 1, 4, 4, 0, 1e-5)
+    assert lib.gsr_group_norm_forward(h, None, ctypes.byref(d), *[None] * 5) == gsr.GSR_EOVERFLOW
+    d = gsr.gsr_group_norm(0, 1, 1, 4, 4, 0, 1e-5)
+    assert lib.gsr_group_norm_forward(h, None, ctypes.byref(d), *[None] * 5) == gsr.GSR_EINVAL
+    assert lib.gsr_group_norm_forward(h, None, None, *[None] * 5) == gsr.GSR_EINVAL
