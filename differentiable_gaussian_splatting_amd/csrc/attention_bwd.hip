@@ -14,10 +14,17 @@
 namespace gsr {
 namespace {
 
+// Waves that share a SIMD, so that one multiplies while another computes exponentials: two where 256 registers hold a
+// wave's operands and sums.
+template <typename T, int DK, bool kMask>
+constexpr int kWavesPerSimd = sizeof(T) == 2 && DK <= 96 && !(kMask && DK > 64) ? 2 : 1;
+template <typename T, int DK, bool kMask>
+constexpr int kWavesPerSimdKeys = sizeof(T) == 2 && DK <= 96 && !(kMask && DK > 32) ? 2 : 1;
+
 // float16 values of ds, whose size follows the loss's scale, are kept in range by a power of two per column of the
 // accumulator (a query's dq, a key's dk): set from the first block that has a value, lowered when a later block would
 // overflow. Other types need none.
-template <typename T, int DP>
+template <typename T, int DK>
 struct Ranged {
   float f = 0.0f;  // 0: nothing seen yet
   static constexpr bool kOn = std::is_same_v<T, _Float16>;
@@ -34,7 +41,7 @@ struct Ranged {
         const float ratio = change && f != 0.0f ? f_new / f : 1.0f;
         f = f_new;
 #pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt)
+        for (int dt = 0; dt < Tile<T, DK>::kOut; ++dt)
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[dt][i] *= ratio;
       }
@@ -45,28 +52,26 @@ struct Ranged {
   __device__ __forceinline__ float undo() const { return kOn ? (f == 0.0f ? 0.0f : 1.0f / f) : 1.0f; }
 };
 
-template <typename T, int DP, bool kMask>
-__global__ __launch_bounds__(kAttnThreads) void k_attn_dq(AttnArgs a) {
-  using L = Tile<T, DP>;
-  constexpr int KT = 32, kLoads = (KT * L::kChunks + kAttnThreads - 1) / kAttnThreads;
-  __shared__ __attribute__((aligned(16))) char s_k[KT * L::kRowBytes];
-  __shared__ __attribute__((aligned(16))) char s_v[KT * L::kRowBytes];
+template <typename T, int DK, bool kMask>
+__global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k_attn_dq(AttnArgs a) {
+  using L = Tile<T, DK>;
+  constexpr int KT = 32, kTile = KT * L::kRowBytes;
+  __shared__ __attribute__((aligned(16))) char s_tile[4 * kTile];
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim);
-  const uint32_t row = w.tile * kAttnRows + (tid >> 6) * 32 + (lane & 31);
+  const uint32_t row0 = w.tile * kAttnRows + (tid >> 6) * 32, row = row0 + (lane & 31);
   const bool valid = row < a.rows;
-  const bool active = w.tile * kAttnRows + (tid >> 6) * 32 < a.rows;
   uint32_t query = 0, head = 0;
   if (valid) row_of(a, w.kv_head, row, &query, &head);
-  Vec<T, 8> qf[DP / 16], df[DP / 16];
+  const int64_t stat = (int64_t(w.batch) * a.heads + head) * a.queries + query;
+  Vec<T, 8> qf[DK / 16], df[DK / 16];
 #pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) qf[kk] = df[kk] = zero_frag<T>();
+  for (int kk = 0; kk < DK / 16; ++kk) qf[kk] = df[kk] = zero_frag<T>();
   // a row that saw no key (lse = -inf) has p = 0 everywhere; whatever its gradient holds is not looked at
   float lse2 = INFINITY, delta = 0.0f;
   if (valid) {
-    const int64_t at = (int64_t(w.batch) * a.heads + head) * a.queries + query;
-    const float lse = a.lse[at];
+    const float lse = a.lse[stat];
     if (lse != -INFINITY) {
       lse2 = lse * kLog2e;
       const T* qr = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0] + int64_t(query) * a.qs[1] +
@@ -76,7 +81,7 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_dq(AttnArgs a) {
       const T* orow = static_cast<const T*>(a.o) + int64_t(w.batch) * a.os[0] + int64_t(query) * a.os[1] +
                       int64_t(head) * a.os[2];
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
+      for (int kk = 0; kk < DK / 16; ++kk) {
         qf[kk] = load_frag(qr, kk, dim);
         df[kk] = load_frag(dr, kk, dim);
         const Vec<T, 8> of = load_frag(orow, kk, dim);
@@ -86,129 +91,105 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_dq(AttnArgs a) {
     }
   }
   delta += other_half(delta);
-  if (valid && h == 0 && w.split == 0) a.delta[(int64_t(w.batch) * a.heads + head) * a.queries + query] = delta;
+  if (valid && h == 0 && w.split == 0) a.delta[stat] = delta;
   const uint8_t* mask = nullptr;
-  if constexpr (kMask)
+  if (kMask && valid)
     mask = a.mask + int64_t(w.batch) * a.ms[0] + int64_t(head) * a.ms[1] + int64_t(query) * a.ms[2];
   const uint32_t len = keys_of(a, w.batch), tiles = (len + KT - 1) / KT;
   const uint32_t t0 = uint32_t(uint64_t(tiles) * w.split / a.splits);
   const uint32_t t1 = uint32_t(uint64_t(tiles) * (w.split + 1) / a.splits);
-  const T* kb = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(w.kv_head) * a.ks[2];
-  const T* vb = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(w.kv_head) * a.vs[2];
-
-  u32x4 rk[kLoads], rv[kLoads];
-  auto fetch = [&](uint32_t t) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int e = tid + i * kAttnThreads, r = e / L::kChunks, c = e % L::kChunks * L::kPer;
-      const uint32_t key = t * KT + r;
-      rk[i] = rv[i] = u32x4{0, 0, 0, 0};
-      if (key < len && c < dim && r < KT) {
-        rk[i] = load_chunk(kb + int64_t(key) * a.ks[1], c, dim);
-        rv[i] = load_chunk(vb + int64_t(key) * a.vs[1], c, dim);
-      }
-    }
-  };
+  Stream<T, DK, KT> ks, vs;
+  ks.base = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(w.kv_head) * a.ks[2];
+  vs.base = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(w.kv_head) * a.vs[2];
+  ks.stride = a.ks[1];
+  vs.stride = a.vs[1];
 
   const float c = a.scale * kLog2e, delta_s = delta * a.scale;
-  f32x16 acc[DP / 32];
+  f32x16 acc[L::kOut];
 #pragma unroll
-  for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = f32x16{};
-  Ranged<T, DP> range;
-  if (t0 < t1) fetch(t0);
-  for (uint32_t t = t0; t < t1; ++t) {
-    bool odd = false;
+  for (int dt = 0; dt < L::kOut; ++dt) acc[dt] = f32x16{};
+  Ranged<T, DK> range;
+  auto multiply = [&](uint32_t t, const char* s_k, const char* s_v, bool odd, auto edge) {
+    f32x16 s = {}, dp = {};
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int e = tid + i * kAttnThreads, r = e / L::kChunks;
-      if (r < KT) {
-        *reinterpret_cast<u32x4*>(s_k + L::at(r, e % L::kChunks)) = rk[i];
-        *reinterpret_cast<u32x4*>(s_v + L::at(r, e % L::kChunks)) = rv[i];
+    for (int kk = 0; kk < DK / 16; ++kk) s = mma(L::frag(s_k, 0, kk), qf[kk], s);
+#pragma unroll
+    for (int kk = 0; kk < DK / 16; ++kk) dp = mma(L::frag(s_v, 0, kk), df[kk], dp);
+    uint32_t seen = 0;
+    if constexpr (kMask || decltype(edge)::value) {
+      seen = visible<kMask>(mask, t * KT, len);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;
+        dp[i] = (seen >> i) & 1 ? dp[i] : 0.0f;
       }
-      if constexpr (kMask) odd |= any_nonfinite<T>(rk[i]);
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = exp2_fast(fmaf(s[i], c, -lse2)) * fmaf(dp[i], a.scale, -delta_s);
+    range.fit(s, acc);
+    contract<T, DK>(acc, s_k, 0, s, kMask && odd, seen);
+  };
+  if (t0 < t1) {
+    ks.fetch(a, t0 * KT, len);
+    vs.fetch(a, t0 * KT, len);
+  }
+  int at = 0;
+  for (uint32_t t = t0; t < t1; ++t) {
+    char *s_k = s_tile + at, *s_v = s_k + kTile;
+    ks.put(s_k);
+    vs.put(s_v);
+    bool odd = false;
     if constexpr (kMask)
-      odd = __syncthreads_or(odd);
+      odd = __syncthreads_or(ks.nonfinite());
     else
       __syncthreads();
-    if (t + 1 < t1) fetch(t + 1);
-    if (active) {
-      f32x16 s = {}, dp = {};
-#pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) s = mma(L::frag(s_k, 0, kk), qf[kk], s);
-#pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) dp = mma(L::frag(s_v, 0, kk), df[kk], dp);
-      uint32_t seen = 0;
-      const bool some = kMask || (t + 1) * KT > len;
-      if (some) {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const uint32_t key = t * KT + 8 * g + 4 * h;
-          uint32_t bytes = 0x01010101u;
-          if constexpr (kMask) {
-            bytes = 0;
-            if (valid) {
-              if (key + 4 <= len) {
-                __builtin_memcpy(&bytes, mask + key, 4);
-              } else {
-                for (uint32_t i = 0; i < 4; ++i)
-                  if (key + i < len) bytes |= uint32_t(mask[key + i]) << (8 * i);
-              }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool vis = key + i < len && ((bytes >> (8 * i)) & 0xffu) != 0;
-            seen |= uint32_t(vis) << (4 * g + i);
-            s[4 * g + i] = vis ? s[4 * g + i] : -INFINITY;
-            dp[4 * g + i] = vis ? dp[4 * g + i] : 0.0f;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = exp2_fast(fmaf(s[i], c, -lse2)) * fmaf(dp[i], a.scale, -delta_s);
-      range.fit(s, acc);
-      contract<T, DP>(acc, s_k, 0, s, kMask && odd, seen);
+    if (t + 1 < t1) {
+      ks.fetch(a, (t + 1) * KT, len);
+      vs.fetch(a, (t + 1) * KT, len);
     }
-    __syncthreads();
+    if (row0 < a.rows) {
+      if ((t + 1) * KT <= len)
+        multiply(t, s_k, s_v, odd, std::false_type());
+      else
+        multiply(t, s_k, s_v, odd, std::true_type());
+    }
+    at ^= 2 * kTile;
   }
   if (!valid) return;
   if (a.splits > 1) {
-    const int64_t at = (int64_t(w.batch * a.kv_heads + w.kv_head) * a.splits + w.split) * a.rows + row;
-    store_column<float, DP>(a.part + at * dim, acc, range.undo(), dim);
+    const int64_t part = (int64_t(w.batch * a.kv_heads + w.kv_head) * a.splits + w.split) * a.rows + row;
+    store_column<L::kOut>(a.part + part * dim, acc, range.undo(), dim);
     return;
   }
   T* out = static_cast<T*>(a.dq) + int64_t(w.batch) * a.dqs[0] + int64_t(query) * a.dqs[1] +
            int64_t(head) * a.dqs[2];
-  store_column<T, DP>(out, acc, range.undo(), dim);
+  store_column<L::kOut>(out, acc, range.undo(), dim);
 }
 
-template <typename T, int DP, bool kMask>
-__global__ __launch_bounds__(kAttnThreads) void k_attn_dkv(AttnArgs a) {
-  using L = Tile<T, DP>;
-  constexpr int QT = 32, kLoads = (QT * L::kChunks + kAttnThreads - 1) / kAttnThreads;
-  __shared__ __attribute__((aligned(16))) char s_q[QT * L::kRowBytes];
-  __shared__ __attribute__((aligned(16))) char s_d[QT * L::kRowBytes];
-  __shared__ __attribute__((aligned(16))) float s_lse[QT];
-  __shared__ __attribute__((aligned(16))) float s_delta[QT];
-  __shared__ int64_t s_mask[QT];
+template <typename T, int DK, bool kMask>
+__global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) void k_attn_dkv(AttnArgs a) {
+  using L = Tile<T, DK>;
+  constexpr int QT = 32, kTile = QT * L::kRowBytes;
+  __shared__ __attribute__((aligned(16))) char s_tile[4 * kTile];
+  __shared__ __attribute__((aligned(16))) float s_lse[2][QT];
+  __shared__ __attribute__((aligned(16))) float s_delta[2][QT];
+  __shared__ int64_t s_mask[2][kMask ? QT : 1];
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim);
-  const uint32_t key = w.tile * kAttnRows + (tid >> 6) * 32 + (lane & 31);
+  const uint32_t key0 = w.tile * kAttnRows + (tid >> 6) * 32, key = key0 + (lane & 31);
   const uint32_t len = keys_of(a, w.batch);
   const bool valid = key < len;
-  const bool active = w.tile * kAttnRows + (tid >> 6) * 32 < len;
-  Vec<T, 8> kf[DP / 16], vf[DP / 16];
+  Vec<T, 8> kf[DK / 16], vf[DK / 16];
 #pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) kf[kk] = vf[kk] = zero_frag<T>();
+  for (int kk = 0; kk < DK / 16; ++kk) kf[kk] = vf[kk] = zero_frag<T>();
   if (valid) {
     const T* kr = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(key) * a.ks[1] +
                   int64_t(w.kv_head) * a.ks[2];
     const T* vr = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(key) * a.vs[1] +
                   int64_t(w.kv_head) * a.vs[2];
 #pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) {
+    for (int kk = 0; kk < DK / 16; ++kk) {
       kf[kk] = load_frag(kr, kk, dim);
       vf[kk] = load_frag(vr, kk, dim);
     }
@@ -216,144 +197,164 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_dkv(AttnArgs a) {
   const uint32_t tiles = w.tile * kAttnRows < len ? (a.rows + QT - 1) / QT : 0;  // no visible key: nothing to sum
   const uint32_t t0 = uint32_t(uint64_t(tiles) * w.split / a.splits);
   const uint32_t t1 = uint32_t(uint64_t(tiles) * (w.split + 1) / a.splits);
-  const T* qb = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0];
-  const T* db = static_cast<const T*>(a.dout) + int64_t(w.batch) * a.dos[0];
+  // with one query head to a key head, the rows are the queries, a constant stride apart
+  const bool plain = a.share.d == 1;
   const int64_t stat0 = int64_t(w.batch) * a.heads * a.queries;
-
-  // A streamed row that saw no key is taken as zeros, whatever it holds (its lse2 of +inf makes p = 0).
-  u32x4 rq[kLoads], rd[kLoads];
-  float lse2 = INFINITY, delta = 0.0f;
+  Stream<T, DK, QT> qs, ds;
+  qs.base = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0] + (plain ? int64_t(w.kv_head) * a.qs[2] : 0);
+  ds.base = static_cast<const T*>(a.dout) + int64_t(w.batch) * a.dos[0] + (plain ? int64_t(w.kv_head) * a.dos[2] : 0);
+  qs.stride = a.qs[1];
+  ds.stride = a.dos[1];
+  float lse = -INFINITY, delta = 0.0f;       // of row tid of the tile (the first QT threads)
+  float row_lse[Stream<T, DK, QT>::kLoads];  // of the rows this thread copies
   int64_t mask_at = 0;
+  auto stat_of = [&](uint32_t row) {
+    uint32_t query, head;
+    row_of(a, w.kv_head, row, &query, &head);
+    return stat0 + int64_t(head) * a.queries + query;
+  };
   auto fetch = [&](uint32_t t) {
+    if (plain) {
+      qs.fetch(a, t * QT, a.rows);
+      ds.fetch(a, t * QT, a.rows);
+    } else {
+      qs.fetch_rows(a, w.kv_head, t * QT, a.qs);
+      ds.fetch_rows(a, w.kv_head, t * QT, a.dos);
+    }
+    if constexpr (kMask) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int e = tid + i * kAttnThreads, r = e / L::kChunks, c = e % L::kChunks * L::kPer;
-      const uint32_t row = t * QT + r;
-      rq[i] = rd[i] = u32x4{0, 0, 0, 0};
-      if (row < a.rows && c < dim && r < QT) {
-        uint32_t query, head;
-        row_of(a, w.kv_head, row, &query, &head);
-        if (a.lse[stat0 + int64_t(head) * a.queries + query] != -INFINITY) {
-          rq[i] = load_chunk(qb + int64_t(query) * a.qs[1] + int64_t(head) * a.qs[2], c, dim);
-          rd[i] = load_chunk(db + int64_t(query) * a.dos[1] + int64_t(head) * a.dos[2], c, dim);
-        }
+      for (int i = 0; i < qs.kLoads; ++i) {
+        const uint32_t row = t * QT + qs.row() + i * qs.kPass;
+        row_lse[i] = row < a.rows ? a.lse[stat_of(row)] : -INFINITY;
       }
     }
     if (tid < QT) {
-      lse2 = INFINITY;
+      const uint32_t row = t * QT + tid;
+      lse = -INFINITY;
       delta = 0.0f;
       mask_at = 0;
-      const uint32_t row = t * QT + tid;
       if (row < a.rows) {
-        uint32_t query, head;
-        row_of(a, w.kv_head, row, &query, &head);
-        const float lse = a.lse[stat0 + int64_t(head) * a.queries + query];
-        if (lse != -INFINITY) {
-          lse2 = lse * kLog2e;
-          delta = a.delta[stat0 + int64_t(head) * a.queries + query] * a.scale;
+        const int64_t at = stat_of(row);
+        lse = a.lse[at];
+        delta = a.delta[at];
+        if constexpr (kMask) {
+          uint32_t query, head;
+          row_of(a, w.kv_head, row, &query, &head);
+          mask_at = int64_t(head) * a.ms[1] + int64_t(query) * a.ms[2];
         }
-        if constexpr (kMask) mask_at = int64_t(head) * a.ms[1] + int64_t(query) * a.ms[2];
       }
     }
   };
 
-  constexpr float kDown = std::is_same_v<T, _Float16> ? 1.0f / 16384.0f : 1.0f;  // undoes kLift
-  const float c = a.scale * kLog2e;
+  constexpr float kDown = std::is_same_v<T, _Float16> ? 1.0f / 16384.0f : 1.0f;  // undoes kLiftBack
+  const float c = a.scale * kLog2e, scale = a.scale * kDown;
   const uint8_t* mask = kMask ? a.mask + int64_t(w.batch) * a.ms[0] + key : nullptr;
-  f32x16 dk[DP / 32], dv[DP / 32];
+  f32x16 dk[L::kOut], dv[L::kOut];
 #pragma unroll
-  for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = dv[dt] = f32x16{};
-  Ranged<T, DP> range;
+  for (int dt = 0; dt < L::kOut; ++dt) dk[dt] = dv[dt] = f32x16{};
+  Ranged<T, DK> range;
   if (t0 < t1) fetch(t0);
+  int buf = 0;
   for (uint32_t t = t0; t < t1; ++t) {
-    bool odd = false;
+    char *s_q = s_tile + buf * 2 * kTile, *s_d = s_q + kTile;
+    if constexpr (kMask) {
+      // a row that saw no key is taken as zeros, whatever it holds
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int e = tid + i * kAttnThreads, r = e / L::kChunks;
-      if (r < QT) {
-        *reinterpret_cast<u32x4*>(s_q + L::at(r, e % L::kChunks)) = rq[i];
-        *reinterpret_cast<u32x4*>(s_d + L::at(r, e % L::kChunks)) = rd[i];
-      }
-      if constexpr (kMask) odd |= any_nonfinite<T>(rq[i]) || any_nonfinite<T>(rd[i]);
+      for (int i = 0; i < qs.kLoads; ++i)
+        if (row_lse[i] == -INFINITY) qs.reg[i] = ds.reg[i] = u32x4{0, 0, 0, 0};
     }
+    qs.put(s_q);
+    ds.put(s_d);
     if (tid < QT) {
-      s_lse[tid] = lse2;
-      s_delta[tid] = delta;
-      if constexpr (kMask) s_mask[tid] = mask_at;
+      // -inf becomes +inf: p = 0 for a row that saw no key or does not exist
+      s_lse[buf][tid] = lse == -INFINITY ? -INFINITY : kLiftBack<T> - lse * kLog2e;
+      s_delta[buf][tid] = lse == -INFINITY ? 0.0f : -delta * scale;
+      if constexpr (kMask) s_mask[buf][tid] = mask_at;
     }
+    bool odd = false;
     if constexpr (kMask)
-      odd = __syncthreads_or(odd);
+      odd = __syncthreads_or(qs.nonfinite() || ds.nonfinite());
     else
       __syncthreads();
     if (t + 1 < t1) fetch(t + 1);
-    if (active) {
+    if (key0 < len) {
       f32x16 s = {}, dp = {};
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) s = mma(L::frag(s_q, 0, kk), kf[kk], s);
+      for (int kk = 0; kk < DK / 16; ++kk) s = mma(L::frag(s_q, 0, kk), kf[kk], s);
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) dp = mma(L::frag(s_d, 0, kk), vf[kk], dp);
+      for (int kk = 0; kk < DK / 16; ++kk) dp = mma(L::frag(s_d, 0, kk), vf[kk], dp);
       uint32_t seen = 0;
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const Vec<float, 4> ls = *reinterpret_cast<const Vec<float, 4>*>(s_lse + 8 * g + 4 * h);
-        const Vec<float, 4> dl = *reinterpret_cast<const Vec<float, 4>*>(s_delta + 8 * g + 4 * h);
+        const Vec<float, 4> ls = *reinterpret_cast<const Vec<float, 4>*>(&s_lse[buf][8 * g + 4 * h]);
+        const Vec<float, 4> dl = *reinterpret_cast<const Vec<float, 4>*>(&s_delta[buf][8 * g + 4 * h]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = 4 * g + i;
-          bool vis = valid;
+          s[e] = exp2_fast(fmaf(s[e], c, ls[i]));
+          dp[e] = s[e] * fmaf(dp[e], scale, dl[i]);
           if constexpr (kMask) {
-            const uint32_t row = t * QT + 8 * g + 4 * h + i;
-            if (valid && row < a.rows) vis = mask[s_mask[8 * g + 4 * h + i]] != 0;
-            vis = vis && ls[i] != INFINITY;
+            const bool vis = valid && ls[i] != -INFINITY && mask[s_mask[buf][8 * g + 4 * h + i]] != 0;
             seen |= uint32_t(vis) << e;
+            s[e] = vis ? s[e] : 0.0f;
+            dp[e] = vis ? dp[e] : 0.0f;
           }
-          const float p = vis ? exp2_fast(fmaf(s[e], c, kLift<T> - ls[i])) : 0.0f;
-          s[e] = p;
-          dp[e] = vis ? p * (fmaf(dp[e], a.scale, -dl[i]) * kDown) : 0.0f;
         }
       }
-      contract<T, DP>(dv, s_d, 0, s, kMask && odd, seen);
+      contract<T, DK>(dv, s_d, 0, s, kMask && odd, seen);
       range.fit(dp, dk);
-      contract<T, DP>(dk, s_q, 0, dp, kMask && odd, seen);
+      contract<T, DK>(dk, s_q, 0, dp, kMask && odd, seen);
     }
-    __syncthreads();
+    buf ^= 1;
   }
   if (key >= a.keys) return;
+  if (!valid) {  // past the length: zeros
+#pragma unroll
+    for (int dt = 0; dt < L::kOut; ++dt) dk[dt] = dv[dt] = f32x16{};
+  }
   if (a.splits > 1) {
     const int64_t group = int64_t(w.batch) * a.kv_heads + w.kv_head, all = int64_t(a.batch) * a.kv_heads;
-    const int64_t at = (group * a.splits + w.split) * a.keys + key;
-    store_column<float, DP>(a.part + at * dim, dk, range.undo(), dim);
-    store_column<float, DP>(a.part + (all * a.splits * a.keys + at) * dim, dv, kDown, dim);
+    const int64_t part = (group * a.splits + w.split) * a.keys + key;
+    store_column<L::kOut>(a.part + part * dim, dk, range.undo(), dim);
+    store_column<L::kOut>(a.part + (all * a.splits * a.keys + part) * dim, dv, kDown, dim);
     return;
   }
   T* ok = static_cast<T*>(a.dk) + int64_t(w.batch) * a.dks[0] + int64_t(key) * a.dks[1] + int64_t(w.kv_head) * a.dks[2];
   T* ov = static_cast<T*>(a.dv) + int64_t(w.batch) * a.dvs[0] + int64_t(key) * a.dvs[1] + int64_t(w.kv_head) * a.dvs[2];
-  store_column<T, DP>(ok, dk, range.undo(), dim);
-  store_column<T, DP>(ov, dv, kDown, dim);
+  store_column<L::kOut>(ok, dk, range.undo(), dim);
+  store_column<L::kOut>(ov, dv, kDown, dim);
 }
 
-// Adds the parts of split rows: a thread per (row, element). blockIdx.y = 1 adds dv after dk.
+// Adds the parts of split rows in order: a thread per (row, four elements). blockIdx.y = 1 adds dv after dk.
 template <typename T, bool kKeys>
 __global__ __launch_bounds__(kAttnThreads) void k_attn_add(AttnArgs a) {
   const uint64_t id = uint64_t(blockIdx.x) * kAttnThreads + threadIdx.x;
-  const uint32_t per = kKeys ? a.keys : a.rows;
+  const uint32_t per = kKeys ? a.keys : a.rows, quads = (a.dim + 3) / 4;
   const uint64_t rows = uint64_t(a.batch) * a.kv_heads * per;
-  if (id >= rows * a.dim) return;
-  const uint32_t d = uint32_t(id % a.dim);
-  const uint64_t at = id / a.dim, group = at / per;
+  if (id >= rows * quads) return;
+  const uint32_t d = uint32_t(id % quads) * 4;
+  const int n = int(a.dim - d);
+  const uint64_t at = id / quads, group = at / per;
   const uint32_t row = uint32_t(at % per), kv_head = uint32_t(group % a.kv_heads), b = uint32_t(group / a.kv_heads);
   const float* part = a.part + (group * a.splits * per + row) * a.dim + d;
   if (kKeys && blockIdx.y) part += rows * a.splits * a.dim;
-  float v = 0.0f;
-  for (uint32_t s = 0; s < a.splits; ++s) v += part[uint64_t(s) * per * a.dim];
+  float v[4] = {};
+#pragma unroll 4
+  for (uint32_t s = 0; s < a.splits; ++s) {
+    float x[4];
+    load_f32<4>(part + uint64_t(s) * per * a.dim, n, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += x[i];
+  }
   if constexpr (kKeys) {
     const int64_t* st = blockIdx.y ? a.dvs : a.dks;
     T* out = static_cast<T*>(blockIdx.y ? a.dv : a.dk);
-    out[int64_t(b) * st[0] + int64_t(row) * st[1] + int64_t(kv_head) * st[2] + d] = T(v);
+    store_f32<4>(out + int64_t(b) * st[0] + int64_t(row) * st[1] + int64_t(kv_head) * st[2] + d, n, v);
   } else {
     uint32_t query, head;
     row_of(a, kv_head, row, &query, &head);
-    static_cast<T*>(a.dq)[int64_t(b) * a.dqs[0] + int64_t(query) * a.dqs[1] + int64_t(head) * a.dqs[2] + d] = T(v);
+    store_f32<4>(static_cast<T*>(a.dq) + int64_t(b) * a.dqs[0] + int64_t(query) * a.dqs[1] +
+                     int64_t(head) * a.dqs[2] + d, n, v);
   }
 }
 
@@ -406,20 +407,20 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
   a.part = b.part = a.delta + deltas;
   hipStream_t s = static_cast<hipStream_t>(stream);
   timing_mark(ctx, GSR_STAGE_ATTENTION_BACKWARD, s, false);
-  attention_by_kind(d->dtype, a.dim, mask != nullptr && a.keys, [&](auto t, auto dp, auto masked) {
+  attention_by_kind(d->dtype, a.dim, mask != nullptr && a.keys, [&](auto t, auto dk_, auto masked) {
     using T = decltype(t);
-    constexpr int DP = decltype(dp)::value;
+    constexpr int DK = decltype(dk_)::value;
     constexpr bool kMask = decltype(masked)::value;
     const dim3 block(kAttnThreads);
     auto blocks = [&](uint64_t n) { return uint32_t((n + kAttnThreads - 1) / kAttnThreads); };
     if (has_q) {
-      hipLaunchKernelGGL((k_attn_dq<T, DP, kMask>), grid_q, block, 0, s, a);
-      if (a.splits > 1) hipLaunchKernelGGL((k_attn_add<T, false>), dim3(blocks(groups * a.rows * a.dim)), block, 0, s, a);
+      hipLaunchKernelGGL((k_attn_dq<T, DK, kMask>), grid_q, block, 0, s, a);
+      if (a.splits > 1) hipLaunchKernelGGL((k_attn_add<T, false>), dim3(blocks(groups * a.rows * ((a.dim + 3) / 4))), block, 0, s, a);
     }
     if (has_k) {
-      hipLaunchKernelGGL((k_attn_dkv<T, DP, kMask>), grid_k, block, 0, s, b);
+      hipLaunchKernelGGL((k_attn_dkv<T, DK, kMask>), grid_k, block, 0, s, b);
       if (b.splits > 1)
-        hipLaunchKernelGGL((k_attn_add<T, true>), dim3(blocks(groups * b.keys * b.dim), 2), block, 0, s, b);
+        hipLaunchKernelGGL((k_attn_add<T, true>), dim3(blocks(groups * b.keys * ((b.dim + 3) / 4)), 2), block, 0, s, b);
     }
   });
   timing_mark(ctx, GSR_STAGE_ATTENTION_BACKWARD, s, true);

@@ -24,9 +24,12 @@ using f32x16 = Vec<float, 16>;
 using u32x4 = Vec<uint32_t, 4>;
 
 // Powers of two by which probabilities are kept too large: a float16 probability below 2^-14 would lose bits, and in a
-// long flat context most are. 2^14 times one is still finite, and the sums divide it out.
+// long flat context most are. The forward's are at most 2^8 (kSlack) over the running maximum, so 2^7 more stays
+// finite; the backward's are at most 1. The sums divide them out.
 template <typename T>
-constexpr float kLift = std::is_same_v<T, _Float16> ? 14.0f : 0.0f;
+constexpr float kLift = std::is_same_v<T, _Float16> ? 7.0f : 0.0f;
+template <typename T>
+constexpr float kLiftBack = std::is_same_v<T, _Float16> ? 14.0f : 0.0f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -71,6 +74,7 @@ struct AttnArgs {
   uint32_t rows;   // queries * (heads / kv_heads): the rows that meet one key head
   uint32_t tiles;  // workgroups across rows (keys in the key gradient)
   uint32_t splits, works, per_xcd;
+  bool whole;      // a row is a whole number of 16-byte chunks
   float scale;
   FastDiv share;   // row -> query; the rest is the head within its group
   int64_t qs[3], ks[3], vs[3], os[3], ms[3], dos[3], dqs[3], dks[3], dvs[3];
@@ -104,14 +108,18 @@ __device__ __forceinline__ uint32_t keys_of(const AttnArgs& a, uint32_t batch) {
   return a.kv_len ? uint32_t(min(max(a.kv_len[batch], 0), int32_t(a.keys))) : a.keys;
 }
 
-// An LDS tile of rows of DP elements, in 16-byte chunks. The chunks of a row are permuted (xor) so that both kinds of
-// reads touch each of the 64 banks once per pass: sixteen rows at one chunk (operand fragments), and four adjacent
-// rows at four adjacent chunks (transposing reads).
-template <typename T, int DP>
+// An LDS tile of rows of DK elements (a multiple of 16, the head dimension padded with zeros), in 16-byte chunks, each
+// row starting a power of two apart. The chunks of a row are permuted (xor) so that both kinds of reads touch each of
+// the 64 banks once per pass: sixteen rows at one chunk (operand fragments), and four adjacent rows at four adjacent
+// chunks (transposing reads).
+template <typename T, int DK>
 struct Tile {
-  static constexpr int kPer = 16 / int(sizeof(T));  // elements per chunk
-  static constexpr int kChunks = DP / kPer;
-  static constexpr int kRowBytes = DP * int(sizeof(T));
+  static constexpr int kPer = 16 / int(sizeof(T));                 // elements per chunk
+  static constexpr int kUsed = DK / kPer;                          // chunks of a row that hold elements
+  static constexpr int kRow = DK <= 32 ? 32 : (DK <= 64 ? 64 : 128);  // elements from row to row
+  static constexpr int kChunks = kRow / kPer;
+  static constexpr int kRowBytes = kRow * int(sizeof(T));
+  static constexpr int kOut = (DK + 31) / 32;                      // 32-wide blocks of the transposed tile
   static constexpr int kLow = kChunks >= 16 ? 0 : (kChunks == 8 ? 1 : 2);
 
   __device__ static __forceinline__ int swizzle(int r) {
@@ -173,6 +181,87 @@ __device__ __forceinline__ u32x4 load_chunk(const T* row, int col, int dim) {
   return r;
 }
 
+template <typename T>
+__device__ __forceinline__ bool finite_bits(T x) {
+  if constexpr (sizeof(T) == 4)
+    return (__builtin_bit_cast(uint32_t, x) & 0x7f800000u) != 0x7f800000u;
+  else if constexpr (std::is_same_v<T, _Float16>)
+    return (__builtin_bit_cast(uint16_t, x) & 0x7c00u) != 0x7c00u;
+  else
+    return (__builtin_bit_cast(uint16_t, x) & 0x7f80u) != 0x7f80u;
+}
+
+template <typename T>
+__device__ __forceinline__ bool any_nonfinite(u32x4 c) {
+  constexpr int kPer = 16 / int(sizeof(T));
+  const Vec<T, kPer> e = __builtin_bit_cast(Vec<T, kPer>, c);
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) bad |= !finite_bits<T>(e[i]);
+  return bad;
+}
+
+// Copies tiles of R rows, a constant stride apart, to LDS through registers: thread (row, chunk) = (tid / kCols,
+// tid % kCols) takes kLoads rows.
+template <typename T, int DK, int R>
+struct Stream {
+  using L = Tile<T, DK>;
+  static constexpr int kCols = L::kUsed <= 4 ? 4 : (L::kUsed <= 8 ? 8 : (L::kUsed <= 16 ? 16 : 32));
+  static constexpr int kPass = kAttnThreads / kCols;
+  static constexpr int kLoads = (R + kPass - 1) / kPass;
+  const T* base;
+  int64_t stride;
+  u32x4 reg[kLoads];
+
+  __device__ static __forceinline__ int row() { return int(threadIdx.x) / kCols; }
+  __device__ static __forceinline__ int chunk() { return int(threadIdx.x) % kCols; }
+
+  // Rows first .. of the tile, those from `end` on as zeros.
+  __device__ __forceinline__ void fetch(const AttnArgs& a, uint32_t first, uint32_t end) {
+    const int c = chunk() * L::kPer, dim = int(a.dim);
+    const T* p = base + int64_t(first + row()) * stride + c;
+    const bool full = first + R <= end && R % kPass == 0 && a.whole;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = row() + i * kPass;
+      reg[i] = u32x4{0, 0, 0, 0};
+      if (full) {
+        if (c < dim) __builtin_memcpy(&reg[i], p + i * kPass * stride, 16);
+      } else if (c < dim && r < R && first + r < end) {
+        reg[i] = load_chunk(p - c + i * kPass * stride, c, dim);
+      }
+    }
+  }
+  // The same of packed rows first .. of a key head, `base` and the strides those of a batch entry.
+  __device__ __forceinline__ void fetch_rows(const AttnArgs& a, uint32_t kv_head, uint32_t first, const int64_t* st) {
+    const int c = chunk() * L::kPer, dim = int(a.dim);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = row() + i * kPass;
+      reg[i] = u32x4{0, 0, 0, 0};
+      if (c < dim && r < R && first + r < a.rows) {
+        uint32_t query, head;
+        row_of(a, kv_head, first + r, &query, &head);
+        reg[i] = load_chunk(base + int64_t(query) * st[1] + int64_t(head) * st[2], c, dim);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(char* s) const {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = row() + i * kPass;
+      if ((R % kPass == 0 || r < R) && (kCols == L::kUsed || chunk() < L::kUsed))
+        *reinterpret_cast<u32x4*>(s + L::at(r, chunk())) = reg[i];
+    }
+  }
+  __device__ __forceinline__ bool nonfinite() const {
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) bad |= any_nonfinite<T>(reg[i]);
+    return bad;
+  }
+};
+
 // An operand fragment straight from a row in memory.
 template <typename T>
 __device__ __forceinline__ Vec<T, 8> load_frag(const T* row, int kk, int dim) {
@@ -205,46 +294,26 @@ __device__ __forceinline__ Vec<T, 8> to_frag(const f32x16& p, int s) {
   return f;
 }
 
-template <typename T>
-__device__ __forceinline__ bool finite_bits(T x) {
-  if constexpr (sizeof(T) == 4)
-    return (__builtin_bit_cast(uint32_t, x) & 0x7f800000u) != 0x7f800000u;
-  else if constexpr (std::is_same_v<T, _Float16>)
-    return (__builtin_bit_cast(uint16_t, x) & 0x7c00u) != 0x7c00u;
-  else
-    return (__builtin_bit_cast(uint16_t, x) & 0x7f80u) != 0x7f80u;
-}
-
-template <typename T>
-__device__ __forceinline__ bool any_nonfinite(u32x4 c) {
-  constexpr int kPer = 16 / int(sizeof(T));
-  const Vec<T, kPer> e = __builtin_bit_cast(Vec<T, kPer>, c);
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) bad |= !finite_bits<T>(e[i]);
-  return bad;
-}
-
 // acc[dt] += (transposed tile rows) * (block p), over the block's 32 rows, which are tile rows r0 ..
 // A masked value is 0 in p, but 0 * NaN is NaN: when the tile holds a non-finite element (guard), its finite elements
 // are multiplied alone, and a result becomes NaN where a non-finite one is visible (bit i of `seen`: value i of the
 // block is visible). Plain code, for the rare tile that needs it.
-template <typename T, int DP>
+template <typename T, int DK>
 __device__ __forceinline__ void contract(f32x16* acc, const char* tile, int r0, const f32x16& p, bool guard,
                                          uint32_t seen) {
-  using L = Tile<T, DP>;
+  using L = Tile<T, DK>;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const Vec<T, 8> b = to_frag<T>(p, s);
     if (!guard) {
 #pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt) acc[dt] = mma(L::frag_t(tile, r0 + 16 * s, dt), b, acc[dt]);
+      for (int dt = 0; dt < L::kOut; ++dt) acc[dt] = mma(L::frag_t(tile, r0 + 16 * s, dt), b, acc[dt]);
     } else {
       Vec<T, 8> vis;
 #pragma unroll
       for (int j = 0; j < 8; ++j) vis[j] = T((seen >> (8 * s + j)) & 1 ? 1.0f : 0.0f);
 #pragma unroll
-      for (int dt = 0; dt < DP / 32; ++dt) {
+      for (int dt = 0; dt < L::kOut; ++dt) {
         Vec<T, 8> a = L::frag_t(tile, r0 + 16 * s, dt), odd;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -263,11 +332,11 @@ __device__ __forceinline__ void contract(f32x16* acc, const char* tile, int r0, 
 }
 
 // Writes a column's accumulated elements (4 adjacent ones per group of the block) times f.
-template <typename T, int DP>
+template <int kOut, typename T>
 __device__ __forceinline__ void store_column(T* row, const f32x16* acc, float f, int dim) {
   const int h = int(threadIdx.x & 63) >> 5;
 #pragma unroll
-  for (int dt = 0; dt < DP / 32; ++dt)
+  for (int dt = 0; dt < kOut; ++dt)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int d = dt * 32 + 8 * g + 4 * h;
@@ -276,6 +345,34 @@ __device__ __forceinline__ void store_column(T* row, const f32x16* acc, float f,
       for (int i = 0; i < 4; ++i) v[i] = acc[dt][4 * g + i] * f;
       if (d < dim) store_f32<4>(row + d, dim - d, v);
     }
+}
+
+// The visible ones of the 32 keys from `key0` on, as this lane's 16 values of the block see them. `mask` is the row's
+// (null: a row beyond the last sees nothing).
+template <bool kMask>
+__device__ __forceinline__ uint32_t visible(const uint8_t* mask, uint32_t key0, uint32_t len) {
+  const uint32_t h = (threadIdx.x & 63) >> 5;
+  uint32_t seen = 0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t key = key0 + 8 * g + 4 * h;
+    uint32_t bytes = 0x01010101u;
+    if constexpr (kMask) {
+      bytes = 0;
+      if (mask) {
+        if (key + 4 <= len) {
+          __builtin_memcpy(&bytes, mask + key, 4);
+        } else {
+          for (uint32_t i = 0; i < 4; ++i)
+            if (key + i < len) bytes |= uint32_t(mask[key + i]) << (8 * i);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      seen |= uint32_t(key + i < len && ((bytes >> (8 * i)) & 0xffu) != 0) << (4 * g + i);
+  }
+  return seen;
 }
 
 // Host side (attention_fwd.hip): checks the descriptor and the inputs both directions share and fills the arguments.
@@ -295,20 +392,24 @@ inline dim3 attention_grid(AttnArgs* a, uint32_t tiles, uint64_t steps, uint32_t
   return dim3(a->per_xcd * kFeatXcds);
 }
 
-// Calls f(element type, padded head dimension, whether there is a mask).
+// Calls f(element type, head dimension padded to a multiple of 16, whether there is a mask).
 template <typename F>
 void attention_by_kind(uint32_t dtype, uint32_t dim, bool mask, F f) {
-  auto m = [&](auto t, auto dp) {
+  auto m = [&](auto t, auto dk) {
     if (mask)
-      f(t, dp, std::true_type());
+      f(t, dk, std::true_type());
     else
-      f(t, dp, std::false_type());
+      f(t, dk, std::false_type());
   };
   auto d = [&](auto t) {
     if (dim <= 32)
       m(t, std::integral_constant<int, 32>());
+    else if (dim <= 48)
+      m(t, std::integral_constant<int, 48>());
     else if (dim <= 64)
       m(t, std::integral_constant<int, 64>());
+    else if (dim <= 96)
+      m(t, std::integral_constant<int, 96>());
     else
       m(t, std::integral_constant<int, 128>());
   };

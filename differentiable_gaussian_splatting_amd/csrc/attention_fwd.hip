@@ -2,10 +2,12 @@
 // the softmax (in base 2: exp(scale s) = 2^(c s), c = scale log2 e).
 //
 // A workgroup holds 128 rows (query, head of one key head's group: heads that share keys share the tiles), 32 to a
-// wave, and streams tiles of keys and values through LDS; the next tile's loads are in flight while a tile is
-// multiplied. Scores are computed transposed (keys down, queries across), so that a query's maximum and sum are a
-// lane's own registers plus one exchange between the wave's halves. With few rows and many keys, the keys are split
-// over workgroups and k_attn_join adds the parts in order.
+// wave, and streams tiles of keys and values through LDS, double buffered: a tile's loads are in flight while the one
+// before it is multiplied, and one barrier a tile suffices. Scores are computed transposed (keys down, queries
+// across), so that a query's maximum and sum are a lane's own registers plus one exchange between the wave's halves.
+// With at most 32 rows (a served token) the waves take 32 keys each of a tile of 128 instead, and their results are
+// joined in LDS. With few rows and many keys, the keys are split over workgroups and k_attn_join adds the parts in
+// order.
 #include <type_traits>
 
 #include "attention_common.hpp"
@@ -13,184 +15,245 @@
 namespace gsr {
 namespace {
 
-template <typename T, int DP>
-constexpr int kKeyTile = sizeof(T) == 2 ? 64 : 32;
+// The maximum a row's exponents are taken relative to follows its true maximum only when that has moved by more than
+// this power of two: rescaling the accumulators is then rare, and a probability of 2^8 is as exact as one of 1.
+constexpr float kSlack = 8.0f;
 
-template <typename T, int DP, bool kMask>
-__global__ __launch_bounds__(kAttnThreads) void k_attn_fwd(AttnArgs a) {
-  using L = Tile<T, DP>;
-  constexpr int KT = kKeyTile<T, DP>, kBlocks = KT / 32, kLoads = (KT * L::kChunks + kAttnThreads - 1) / kAttnThreads;
-  __shared__ __attribute__((aligned(16))) char s_k[KT * L::kRowBytes];
-  __shared__ __attribute__((aligned(16))) char s_v[KT * L::kRowBytes];
+// One row's softmax state and output, a column of the transposed blocks.
+template <typename T, int DK>
+struct Running {
+  using L = Tile<T, DK>;
+  float m = -INFINITY;  // reference exponent; -inf while no key was seen
+  float m_c = 0.0f;     // the same, 0 while no key was seen
+  float l = 0.0f;       // this half's sum of 2^(c s - m_c + kLift)
+  f32x16 o[L::kOut];
+
+  // Adds kBlocks blocks of scores of the keys in tile rows r0 .., whose values are rows of s_v.
+  template <int kBlocks>
+  __device__ __forceinline__ void add(f32x16* s, float c, const char* s_v, int r0, bool guard, const uint32_t* seen) {
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
+    top = fmaxf(top, other_half(top)) * c;
+    if (__any(top > m + kSlack)) {
+      const float m_new = fmaxf(m, top), mc_new = m_new == -INFINITY ? 0.0f : m_new;
+      const float f = m == -INFINITY ? 0.0f : exp2_fast(m_c - mc_new);
+      m = m_new;
+      m_c = mc_new;
+      l *= f;
+#pragma unroll
+      for (int dt = 0; dt < L::kOut; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+    }
+    const float lift = kLift<T> - m_c;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[b][i] = exp2_fast(fmaf(s[b][i], c, lift));
+        l += s[b][i];
+      }
+      contract<T, DK>(o, s_v, r0 + 32 * b, s[b], guard, seen[b]);
+    }
+  }
+};
+
+template <typename T, int DK>
+constexpr int kKeyTile = sizeof(T) == 2 && DK <= 64 ? 64 : 32;  // keys of a tile; wider heads leave registers for 32
+
+// kFew: at most 32 rows, the waves share them and split each tile's keys.
+template <typename T, int DK, bool kMask, bool kFew>
+__global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64) ? 2 : 1) void k_attn_fwd(AttnArgs a) {
+  using L = Tile<T, DK>;
+  constexpr int KT = kFew ? 128 : kKeyTile<T, DK>, kBlocks = kFew ? 1 : KT / 32;
+  constexpr int kTile = KT * L::kRowBytes, kBuffers = kFew ? 1 : 2;
+  constexpr int kJoin = kFew ? kAttnWaves * 32 * (L::kOut * 32 + 4) * 4 : 0;  // the waves' outputs
+  constexpr int kBytes = 2 * kBuffers * kTile > kJoin ? 2 * kBuffers * kTile : kJoin;
+  __shared__ __attribute__((aligned(16))) char s_tile[kBytes];
+  __shared__ float2 s_ml[kFew ? kAttnWaves * 32 : 1];
   AttnWork w;
   if (!w.set(a)) return;
-  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim);
-  const uint32_t row = w.tile * kAttnRows + (tid >> 6) * 32 + (lane & 31);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, dim = int(a.dim);
+  const uint32_t row0 = kFew ? 0 : w.tile * kAttnRows + wave * 32;
+  const uint32_t row = row0 + (lane & 31);
   const bool valid = row < a.rows;
-  const bool active = w.tile * kAttnRows + (tid >> 6) * 32 < a.rows;  // the wave has a row
   uint32_t query = 0, head = 0;
   if (valid) row_of(a, w.kv_head, row, &query, &head);
-  Vec<T, 8> qf[DP / 16];
+  Vec<T, 8> qf[DK / 16];
 #pragma unroll
-  for (int kk = 0; kk < DP / 16; ++kk) qf[kk] = zero_frag<T>();
+  for (int kk = 0; kk < DK / 16; ++kk) qf[kk] = zero_frag<T>();
   if (valid) {
     const T* qr = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0] + int64_t(query) * a.qs[1] +
                   int64_t(head) * a.qs[2];
 #pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) qf[kk] = load_frag(qr, kk, dim);
+    for (int kk = 0; kk < DK / 16; ++kk) qf[kk] = load_frag(qr, kk, dim);
   }
   const uint8_t* mask = nullptr;
-  if constexpr (kMask)
+  if (kMask && valid)
     mask = a.mask + int64_t(w.batch) * a.ms[0] + int64_t(head) * a.ms[1] + int64_t(query) * a.ms[2];
   const uint32_t len = keys_of(a, w.batch), tiles = (len + KT - 1) / KT;
   const uint32_t t0 = uint32_t(uint64_t(tiles) * w.split / a.splits);
   const uint32_t t1 = uint32_t(uint64_t(tiles) * (w.split + 1) / a.splits);
-  const T* kb = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(w.kv_head) * a.ks[2];
-  const T* vb = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(w.kv_head) * a.vs[2];
-
-  u32x4 rk[kLoads], rv[kLoads];
-  auto fetch = [&](uint32_t t) {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int e = tid + i * kAttnThreads, r = e / L::kChunks, c = e % L::kChunks * L::kPer;
-      const uint32_t key = t * KT + r;
-      rk[i] = rv[i] = u32x4{0, 0, 0, 0};
-      if (key < len && c < dim && r < KT) {
-        rk[i] = load_chunk(kb + int64_t(key) * a.ks[1], c, dim);
-        rv[i] = load_chunk(vb + int64_t(key) * a.vs[1], c, dim);
-      }
-    }
-  };
+  Stream<T, DK, KT> ks, vs;
+  ks.base = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(w.kv_head) * a.ks[2];
+  vs.base = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(w.kv_head) * a.vs[2];
+  ks.stride = a.ks[1];
+  vs.stride = a.vs[1];
 
   const float c = a.scale * kLog2e;
-  f32x16 o[DP / 32];
+  const int r0 = kFew ? wave * 32 : 0;  // the tile rows of this wave's keys
+  Running<T, DK> run;
 #pragma unroll
-  for (int dt = 0; dt < DP / 32; ++dt) o[dt] = f32x16{};
-  float m = -INFINITY, m_c = 0.0f, l = 0.0f;  // running maximum of the scores, c times it (0 while there is none), sum
-  if (t0 < t1) fetch(t0);
-  for (uint32_t t = t0; t < t1; ++t) {
-    bool odd = false;
+  for (int dt = 0; dt < L::kOut; ++dt) run.o[dt] = f32x16{};
+  auto multiply = [&](uint32_t t, const char* s_k, const char* s_v, bool odd, auto edge) {
+    f32x16 s[kBlocks];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int e = tid + i * kAttnThreads, r = e / L::kChunks;
-      if (r < KT) {
-        *reinterpret_cast<u32x4*>(s_k + L::at(r, e % L::kChunks)) = rk[i];
-        *reinterpret_cast<u32x4*>(s_v + L::at(r, e % L::kChunks)) = rv[i];
-      }
-      if constexpr (kMask) odd |= any_nonfinite<T>(rv[i]);
+    for (int b = 0; b < kBlocks; ++b) {
+      s[b] = f32x16{};
+#pragma unroll
+      for (int kk = 0; kk < DK / 16; ++kk) s[b] = mma(L::frag(s_k, r0 + 32 * b, kk), qf[kk], s[b]);
     }
+    uint32_t seen[kBlocks] = {};
+    if constexpr (kMask || decltype(edge)::value) {
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        seen[b] = visible<kMask>(mask, t * KT + r0 + 32 * b, len);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[b][i] = (seen[b] >> i) & 1 ? s[b][i] : -INFINITY;
+      }
+    }
+    run.template add<kBlocks>(s, c, s_v, r0, kMask && odd, seen);
+  };
+  if (t0 < t1) {
+    ks.fetch(a, t0 * KT, len);
+    vs.fetch(a, t0 * KT, len);
+  }
+  int at = 0;
+  for (uint32_t t = t0; t < t1; ++t) {
+    char *s_k = s_tile + at, *s_v = s_k + kTile;
+    ks.put(s_k);
+    vs.put(s_v);
+    bool odd = false;
     if constexpr (kMask)
-      odd = __syncthreads_or(odd);
+      odd = __syncthreads_or(vs.nonfinite());
     else
       __syncthreads();
-    if (t + 1 < t1) fetch(t + 1);
-    if (active) {
-      f32x16 s[kBlocks];
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-        s[b] = f32x16{};
-#pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) s[b] = mma(L::frag(s_k, 32 * b, kk), qf[kk], s[b]);
-      }
-      uint32_t seen[kBlocks];
-      if (kMask || (t + 1) * KT > len) {
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          seen[b] = 0;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t key = t * KT + 32 * b + 8 * g + 4 * h;
-            uint32_t bytes = 0x01010101u;
-            if constexpr (kMask) {
-              bytes = 0;
-              if (valid) {
-                if (key + 4 <= len) {
-                  __builtin_memcpy(&bytes, mask + key, 4);
-                } else {
-                  for (uint32_t i = 0; i < 4; ++i)
-                    if (key + i < len) bytes |= uint32_t(mask[key + i]) << (8 * i);
-                }
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool vis = key + i < len && ((bytes >> (8 * i)) & 0xffu) != 0;
-              seen[b] |= uint32_t(vis) << (4 * g + i);
-              s[b][4 * g + i] = vis ? s[b][4 * g + i] : -INFINITY;
-            }
-          }
-        }
-      }
-      float top = s[0][0];
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[b][i]);
-      top = fmaxf(top, other_half(top));
-      if (__any(top > m)) {
-        const float m_new = fmaxf(m, top), mc_new = m_new == -INFINITY ? 0.0f : m_new * c;
-        const float f = m == -INFINITY ? 0.0f : exp2_fast(m_c - mc_new);
-        m = m_new;
-        m_c = mc_new;
-        l *= f;
-#pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[dt][i] *= f;
-      }
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[b][i] = exp2_fast(fmaf(s[b][i], c, kLift<T> - m_c));
-          l += s[b][i];
-        }
-        contract<T, DP>(o, s_v, 32 * b, s[b], kMask && odd, seen[b]);
-      }
+    if (t + 1 < t1) {
+      ks.fetch(a, (t + 1) * KT, len);
+      vs.fetch(a, (t + 1) * KT, len);
+    }
+    if (row0 < a.rows) {
+      if ((t + 1) * KT <= len)
+        multiply(t, s_k, s_v, odd, std::false_type());
+      else
+        multiply(t, s_k, s_v, odd, std::true_type());
+    }
+    if constexpr (kBuffers == 2)
+      at ^= 2 * kTile;
+    else
+      __syncthreads();
+  }
+  float l = run.l + other_half(run.l);
+  const int64_t part = (int64_t(w.batch * a.kv_heads + w.kv_head) * a.splits + w.split) * a.rows;
+  if constexpr (kFew) {
+    // rows by waves in LDS, then a thread per (row, four elements)
+    constexpr int kWide = L::kOut * 32 + 4;
+    float* s_o = reinterpret_cast<float*>(s_tile);
+    if (valid) {
+      store_column<L::kOut>(s_o + (wave * 32 + lane % 32) * kWide, run.o, 1.0f, L::kOut * 32);
+      if (h == 0) s_ml[wave * 32 + lane] = make_float2(l == 0.0f ? -INFINITY : run.m_c, l);
     }
     __syncthreads();
+    for (uint32_t e = tid; e < a.rows * (L::kOut * 8); e += kAttnThreads) {
+      const uint32_t r = e / (L::kOut * 8), d = e % (L::kOut * 8) * 4;
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kAttnWaves; ++k) top = fmaxf(top, s_ml[k * 32 + r].x);
+      float sum = 0.0f, v[4] = {};
+#pragma unroll
+      for (int k = 0; k < kAttnWaves; ++k) {
+        const float2 ml = s_ml[k * 32 + r];
+        if (ml.x == -INFINITY) continue;
+        const float f = exp2_fast(ml.x - top);
+        sum = fmaf(ml.y, f, sum);
+        const Vec<float, 4> x = *reinterpret_cast<const Vec<float, 4>*>(s_o + (k * 32 + r) * kWide + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaf(x[i], f, v[i]);
+      }
+      if (int(d) >= dim) continue;
+      if (a.splits > 1) {
+        store_f32<4>(a.part + (part + r) * dim + d, dim - int(d), v);
+        if (d == 0) reinterpret_cast<float2*>(a.part_ml)[part + r] = make_float2(top, sum);
+        continue;
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] *= inv;
+      uint32_t qr, hd;
+      row_of(a, w.kv_head, r, &qr, &hd);
+      T* out = static_cast<T*>(a.out) + int64_t(w.batch) * a.os[0] + int64_t(qr) * a.os[1] + int64_t(hd) * a.os[2];
+      store_f32<4>(out + d, dim - int(d), v);
+      if (a.lse && d == 0)
+        a.lse[(int64_t(w.batch) * a.heads + hd) * a.queries + qr] =
+            sum == 0.0f ? -INFINITY : (top - kLift<T> + log2f(sum)) * kLn2;
+    }
+    return;
   }
   if (!valid) return;
-  l += other_half(l);
   if (a.splits > 1) {
-    const int64_t at = (int64_t(w.batch * a.kv_heads + w.kv_head) * a.splits + w.split) * a.rows + row;
-    store_column<float, DP>(a.part + at * dim, o, 1.0f, dim);
-    if (h == 0) reinterpret_cast<float2*>(a.part_ml)[at] = make_float2(l == 0.0f ? -INFINITY : m_c, l);
+    store_column<L::kOut>(a.part + (part + row) * dim, run.o, 1.0f, dim);
+    if (h == 0) reinterpret_cast<float2*>(a.part_ml)[part + row] = make_float2(l == 0.0f ? -INFINITY : run.m_c, l);
     return;
   }
   T* out = static_cast<T*>(a.out) + int64_t(w.batch) * a.os[0] + int64_t(query) * a.os[1] + int64_t(head) * a.os[2];
-  store_column<T, DP>(out, o, l == 0.0f ? 0.0f : 1.0f / l, dim);
+  store_column<L::kOut>(out, run.o, l == 0.0f ? 0.0f : 1.0f / l, dim);
   if (a.lse && h == 0)
-    a.lse[(int64_t(w.batch) * a.heads + head) * a.queries + query] = l == 0.0f ? -INFINITY : (m_c - kLift<T> + log2f(l)) * kLn2;
+    a.lse[(int64_t(w.batch) * a.heads + head) * a.queries + query] =
+        l == 0.0f ? -INFINITY : (run.m_c - kLift<T> + log2f(l)) * kLn2;
 }
 
-// Joins the parts of rows whose keys were split: a thread per (row, element).
+// Joins the parts of rows whose keys were split: a wave per row, its halves taking every other part (four elements a
+// lane).
 template <typename T>
 __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs a) {
-  const uint64_t id = uint64_t(blockIdx.x) * kAttnThreads + threadIdx.x;
-  const uint64_t rows = uint64_t(a.batch) * a.kv_heads * a.rows;
-  if (id >= rows * a.dim) return;
-  const uint32_t d = uint32_t(id % a.dim);
-  const uint64_t at = id / a.dim, group = at / a.rows;
+  const uint64_t at = uint64_t(blockIdx.x) * kAttnWaves + (threadIdx.x >> 6), group = at / a.rows;
+  if (at >= uint64_t(a.batch) * a.kv_heads * a.rows) return;
   const uint32_t row = uint32_t(at % a.rows), kv_head = uint32_t(group % a.kv_heads), b = uint32_t(group / a.kv_heads);
+  const int lane = threadIdx.x & 63, dim = int(a.dim), d = (lane & 31) * 4;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + group * a.splits * a.rows + row;
   const float* part = a.part + (group * a.splits * a.rows + row) * a.dim + d;
   float top = -INFINITY;
-  for (uint32_t s = 0; s < a.splits; ++s) top = fmaxf(top, ml[uint64_t(s) * a.rows].x);
-  float l = 0.0f, o = 0.0f;
-  for (uint32_t s = 0; s < a.splits; ++s) {
+  for (uint32_t s = lane; s < a.splits; s += 64) top = fmaxf(top, ml[uint64_t(s) * a.rows].x);
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
+  float l = 0.0f, o[4] = {};
+#pragma unroll 4
+  for (uint32_t s = lane >> 5; s < a.splits; s += 2) {
     const float2 v = ml[uint64_t(s) * a.rows];
-    if (v.x == -INFINITY) continue;
-    const float f = exp2_fast(v.x - top);
+    const float f = v.x == -INFINITY ? 0.0f : exp2_fast(v.x - top);
+    float x[4] = {};
+    if (d < dim && v.x != -INFINITY) load_f32<4>(part + uint64_t(s) * a.rows * a.dim, dim - d, x);
     l = fmaf(v.y, f, l);
-    o = fmaf(part[uint64_t(s) * a.rows * a.dim], f, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = fmaf(x[i], f, o[i]);
   }
+  l += other_half(l);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] += other_half(o[i]);
+  if (lane >= 32 || d >= dim) return;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] *= inv;
   uint32_t query, head;
   row_of(a, kv_head, row, &query, &head);
   T* out = static_cast<T*>(a.out) + int64_t(b) * a.os[0] + int64_t(query) * a.os[1] + int64_t(head) * a.os[2];
-  out[d] = T(l == 0.0f ? 0.0f : o / l);
+  store_f32<4>(out + d, dim - d, o);
   if (a.lse && d == 0)
-    a.lse[(int64_t(b) * a.heads + head) * a.queries + query] = l == 0.0f ? -INFINITY : (top - kLift<T> + log2f(l)) * kLn2;
+    a.lse[(int64_t(b) * a.heads + head) * a.queries + query] =
+        l == 0.0f ? -INFINITY : (top - kLift<T> + log2f(l)) * kLn2;
 }
 
 }  // namespace
@@ -228,6 +291,7 @@ gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, c
   a->keys = d->keys;
   a->dim = d->head_dim;
   a->scale = d->scale;
+  a->whole = d->head_dim % (16 / eb) == 0;
   a->share.set(d->heads / d->kv_heads);
   a->rows = d->queries * (d->heads / d->kv_heads);
   for (int i = 0; i < 3; ++i) {
@@ -263,9 +327,10 @@ extern "C" gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, co
   if ((st = enter(ctx))) return st;
   a.out = o;
   a.lse = lse;
-  const uint32_t key_tile = d->dtype == GSR_F32 ? 32 : 64;
-  const dim3 grid = attention_grid(&a, (a.rows + kAttnRows - 1) / kAttnRows,
-                                   (uint64_t(a.keys) + key_tile - 1) / key_tile, 1024);
+  const bool few = a.rows <= 32;
+  const uint32_t key_tile = few ? 128 : (d->dtype != GSR_F32 && d->head_dim <= 64 ? 64 : 32);
+  const dim3 grid = attention_grid(&a, few ? 1 : (a.rows + kAttnRows - 1) / kAttnRows,
+                                   (uint64_t(a.keys) + key_tile - 1) / key_tile, few ? 512 : 1024);
   if (a.splits > 1) {
     const size_t parts = size_t(a.batch) * a.kv_heads * a.splits * a.rows;
     if ((st = grow(ctx, ctx->arena.feat_part, parts * (a.dim + 2) * sizeof(float)))) return st;
@@ -274,14 +339,18 @@ extern "C" gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, co
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   timing_mark(ctx, GSR_STAGE_ATTENTION_FORWARD, s, false);
-  attention_by_kind(d->dtype, a.dim, mask != nullptr && a.keys, [&](auto t, auto dp, auto masked) {
+  attention_by_kind(d->dtype, a.dim, mask != nullptr && a.keys, [&](auto t, auto dk, auto masked) {
     using T = decltype(t);
-    hipLaunchKernelGGL((k_attn_fwd<T, decltype(dp)::value, decltype(masked)::value>), grid, dim3(kAttnThreads), 0, s,
-                       a);
+    constexpr int DK = decltype(dk)::value;
+    constexpr bool kMask = decltype(masked)::value;
+    if (few)
+      hipLaunchKernelGGL((k_attn_fwd<T, DK, kMask, true>), grid, dim3(kAttnThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_attn_fwd<T, DK, kMask, false>), grid, dim3(kAttnThreads), 0, s, a);
     if (a.splits > 1) {
-      const uint64_t n = uint64_t(a.batch) * a.kv_heads * a.rows * a.dim;
-      hipLaunchKernelGGL((k_attn_join<T>), dim3(uint32_t((n + kAttnThreads - 1) / kAttnThreads)), dim3(kAttnThreads),
-                         0, s, a);
+      const uint64_t n = uint64_t(a.batch) * a.kv_heads * a.rows;
+      hipLaunchKernelGGL((k_attn_join<T>), dim3(uint32_t((n + kAttnWaves - 1) / kAttnWaves)), dim3(kAttnThreads), 0,
+                         s, a);
     }
   });
   timing_mark(ctx, GSR_STAGE_ATTENTION_FORWARD, s, true);
