@@ -56,7 +56,7 @@ template <typename T, int DK, bool kMask>
 __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, DK>;
   constexpr int KT = 32, kTile = KT * L::kRowBytes;
-  __shared__ __attribute__((aligned(16))) char s_tile[4 * kTile];
+  __shared__ __attribute__((aligned(16))) char s_tile[6 * kTile];
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim);
@@ -98,11 +98,14 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
   const uint32_t len = keys_of(a, w.batch), tiles = (len + KT - 1) / KT;
   const uint32_t t0 = uint32_t(uint64_t(tiles) * w.split / a.splits);
   const uint32_t t1 = uint32_t(uint64_t(tiles) * (w.split + 1) / a.splits);
-  Stream<T, DK, KT> ks, vs;
-  ks.base = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(w.kv_head) * a.ks[2];
-  vs.base = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(w.kv_head) * a.vs[2];
-  ks.stride = a.ks[1];
-  vs.stride = a.vs[1];
+  const T* kb = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(w.kv_head) * a.ks[2];
+  const T* vb = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(w.kv_head) * a.vs[2];
+  using Copy = Copier<T, DK, KT>;
+  auto start = [&](uint32_t t, char* s) {
+    const uint32_t key0 = t * KT;
+    Copy::start(s, len - key0, dim, a.aligned_kv, [&](int r) { return kb + int64_t(key0 + r) * a.ks[1]; });
+    Copy::start(s + kTile, len - key0, dim, a.aligned_kv, [&](int r) { return vb + int64_t(key0 + r) * a.vs[1]; });
+  };
 
   const float c = a.scale * kLog2e, delta_s = delta * a.scale;
   f32x16 acc[L::kOut];
@@ -129,31 +132,27 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
     range.fit(s, acc);
     contract<T, DK>(acc, s_k, 0, s, kMask && odd, seen);
   };
-  if (t0 < t1) {
-    ks.fetch(a, t0 * KT, len);
-    vs.fetch(a, t0 * KT, len);
-  }
+  clear_tiles<T, DK>(s_tile, 6 * kTile, dim);
+  __syncthreads();
+  if (t0 < t1) start(t0, s_tile);
+  if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
   int at = 0;
   for (uint32_t t = t0; t < t1; ++t) {
-    char *s_k = s_tile + at, *s_v = s_k + kTile;
-    ks.put(s_k);
-    vs.put(s_v);
-    bool odd = false;
-    if constexpr (kMask)
-      odd = __syncthreads_or(ks.nonfinite());
+    const char *s_k = s_tile + at, *s_v = s_k + kTile;
+    if (t + 1 < t1 && (t + 2) * KT <= len)
+      tile_barrier<2 * Copy::kSteps>();
     else
-      __syncthreads();
-    if (t + 1 < t1) {
-      ks.fetch(a, (t + 1) * KT, len);
-      vs.fetch(a, (t + 1) * KT, len);
-    }
+      tile_barrier<0>();
+    if (t + 2 < t1) start(t + 2, s_tile + (at >= 2 * kTile ? at - 2 * kTile : at + 4 * kTile));
+    bool odd = false;
+    if constexpr (kMask) odd = __syncthreads_or(scan_nonfinite<T, kTile>(s_k));
     if (row0 < a.rows) {
       if ((t + 1) * KT <= len)
         multiply(t, s_k, s_v, odd, std::false_type());
       else
         multiply(t, s_k, s_v, odd, std::true_type());
     }
-    at ^= 2 * kTile;
+    at = at == 4 * kTile ? 0 : at + 2 * kTile;
   }
   if (!valid) return;
   if (a.splits > 1) {
@@ -170,10 +169,10 @@ template <typename T, int DK, bool kMask>
 __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, DK>;
   constexpr int QT = 32, kTile = QT * L::kRowBytes;
-  __shared__ __attribute__((aligned(16))) char s_tile[4 * kTile];
-  __shared__ __attribute__((aligned(16))) float s_lse[2][QT];
-  __shared__ __attribute__((aligned(16))) float s_delta[2][QT];
-  __shared__ int64_t s_mask[2][kMask ? QT : 1];
+  __shared__ __attribute__((aligned(16))) char s_tile[6 * kTile];
+  __shared__ __attribute__((aligned(16))) float s_lse[3][QT];
+  __shared__ __attribute__((aligned(16))) float s_delta[3][QT];
+  __shared__ int64_t s_mask[3][kMask ? QT : 1];
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim);
@@ -200,49 +199,38 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
   // with one query head to a key head, the rows are the queries, a constant stride apart
   const bool plain = a.share.d == 1;
   const int64_t stat0 = int64_t(w.batch) * a.heads * a.queries;
-  Stream<T, DK, QT> qs, ds;
-  qs.base = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0] + (plain ? int64_t(w.kv_head) * a.qs[2] : 0);
-  ds.base = static_cast<const T*>(a.dout) + int64_t(w.batch) * a.dos[0] + (plain ? int64_t(w.kv_head) * a.dos[2] : 0);
-  qs.stride = a.qs[1];
-  ds.stride = a.dos[1];
-  float lse = -INFINITY, delta = 0.0f;       // of row tid of the tile (the first QT threads)
-  float row_lse[Stream<T, DK, QT>::kLoads];  // of the rows this thread copies
+  const T* qb = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0] + (plain ? int64_t(w.kv_head) * a.qs[2] : 0);
+  const T* db = static_cast<const T*>(a.dout) + int64_t(w.batch) * a.dos[0] +
+                (plain ? int64_t(w.kv_head) * a.dos[2] : 0);
+  using Copy = Copier<T, DK, QT>;
+  float lse = -INFINITY, delta = 0.0f;  // of row tid of the newest tile (the first QT threads)
   int64_t mask_at = 0;
-  auto stat_of = [&](uint32_t row) {
-    uint32_t query, head;
-    row_of(a, w.kv_head, row, &query, &head);
-    return stat0 + int64_t(head) * a.queries + query;
-  };
-  auto fetch = [&](uint32_t t) {
-    if (plain) {
-      qs.fetch(a, t * QT, a.rows);
-      ds.fetch(a, t * QT, a.rows);
-    } else {
-      qs.fetch_rows(a, w.kv_head, t * QT, a.qs);
-      ds.fetch_rows(a, w.kv_head, t * QT, a.dos);
-    }
-    if constexpr (kMask) {
-#pragma unroll
-      for (int i = 0; i < qs.kLoads; ++i) {
-        const uint32_t row = t * QT + qs.row() + i * qs.kPass;
-        row_lse[i] = row < a.rows ? a.lse[stat_of(row)] : -INFINITY;
-      }
-    }
+  auto start = [&](uint32_t t, char* s) {
+    const uint32_t row0 = t * QT;
     if (tid < QT) {
-      const uint32_t row = t * QT + tid;
       lse = -INFINITY;
       delta = 0.0f;
-      mask_at = 0;
-      if (row < a.rows) {
-        const int64_t at = stat_of(row);
+      if (row0 + tid < a.rows) {
+        uint32_t query, head;
+        row_of(a, w.kv_head, row0 + tid, &query, &head);
+        const int64_t at = stat0 + int64_t(head) * a.queries + query;
         lse = a.lse[at];
         delta = a.delta[at];
-        if constexpr (kMask) {
-          uint32_t query, head;
-          row_of(a, w.kv_head, row, &query, &head);
-          mask_at = int64_t(head) * a.ms[1] + int64_t(query) * a.ms[2];
-        }
+        if constexpr (kMask) mask_at = int64_t(head) * a.ms[1] + int64_t(query) * a.ms[2];
       }
+    }
+    if (plain) {
+      Copy::start(s, a.rows - row0, dim, a.aligned_rows, [&](int r) { return qb + int64_t(row0 + r) * a.qs[1]; });
+      Copy::start(s + kTile, a.rows - row0, dim, a.aligned_rows,
+                  [&](int r) { return db + int64_t(row0 + r) * a.dos[1]; });
+    } else {
+      auto row_at = [&](const T* base, const int64_t* st, int r) {
+        uint32_t query, head;
+        row_of(a, w.kv_head, row0 + r, &query, &head);
+        return base + int64_t(query) * st[1] + int64_t(head) * st[2];
+      };
+      Copy::start(s, a.rows - row0, dim, a.aligned_rows, [&](int r) { return row_at(qb, a.qs, r); });
+      Copy::start(s + kTile, a.rows - row0, dim, a.aligned_rows, [&](int r) { return row_at(db, a.dos, r); });
     }
   };
 
@@ -253,30 +241,40 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
 #pragma unroll
   for (int dt = 0; dt < L::kOut; ++dt) dk[dt] = dv[dt] = f32x16{};
   Ranged<T, DK> range;
-  if (t0 < t1) fetch(t0);
-  int buf = 0;
-  for (uint32_t t = t0; t < t1; ++t) {
-    char *s_q = s_tile + buf * 2 * kTile, *s_d = s_q + kTile;
-    if constexpr (kMask) {
-      // a row that saw no key is taken as zeros, whatever it holds
-#pragma unroll
-      for (int i = 0; i < qs.kLoads; ++i)
-        if (row_lse[i] == -INFINITY) qs.reg[i] = ds.reg[i] = u32x4{0, 0, 0, 0};
-    }
-    qs.put(s_q);
-    ds.put(s_d);
+  // the newest tile's statistics to LDS, beside its rows; a row that saw no key or does not exist gets p = 0
+  auto put_stats = [&](int buf) {
     if (tid < QT) {
-      // -inf becomes +inf: p = 0 for a row that saw no key or does not exist
       s_lse[buf][tid] = lse == -INFINITY ? -INFINITY : kLiftBack<T> - lse * kLog2e;
       s_delta[buf][tid] = lse == -INFINITY ? 0.0f : -delta * scale;
       if constexpr (kMask) s_mask[buf][tid] = mask_at;
     }
-    bool odd = false;
-    if constexpr (kMask)
-      odd = __syncthreads_or(qs.nonfinite() || ds.nonfinite());
+  };
+  clear_tiles<T, DK>(s_tile, 6 * kTile, dim);
+  __syncthreads();
+  if (t0 < t1) {
+    start(t0, s_tile);
+    put_stats(0);
+  }
+  if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
+  int buf = 0;
+  for (uint32_t t = t0; t < t1; ++t) {
+    char *s_q = s_tile + buf * 2 * kTile, *s_d = s_q + kTile;
+    const int next = buf == 2 ? 0 : buf + 1;
+    if (t + 1 < t1) put_stats(next);
+    if (t + 1 < t1 && (t + 2) * QT <= a.rows)
+      tile_barrier<2 * Copy::kSteps>();
     else
+      tile_barrier<0>();
+    bool odd = false;
+    if constexpr (kMask) {
+      // a row that saw no key is taken as zeros, whatever it holds
+      for (int e = tid; e < QT * L::kChunks; e += kAttnThreads)
+        if (s_lse[buf][e / L::kChunks] == -INFINITY)
+          reinterpret_cast<u32x4*>(s_q)[e] = reinterpret_cast<u32x4*>(s_d)[e] = u32x4{0, 0, 0, 0};
       __syncthreads();
-    if (t + 1 < t1) fetch(t + 1);
+      odd = __syncthreads_or(scan_nonfinite<T, 2 * kTile>(s_q));
+    }
+    if (t + 2 < t1) start(t + 2, s_tile + (next == 2 ? 0 : next + 1) * 2 * kTile);
     if (key0 < len) {
       f32x16 s = {}, dp = {};
 #pragma unroll
@@ -305,7 +303,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
       range.fit(dp, dk);
       contract<T, DK>(dk, s_q, 0, dp, kMask && odd, seen);
     }
-    buf ^= 1;
+    buf = next;
   }
   if (key >= a.keys) return;
   if (!valid) {  // past the length: zeros
@@ -370,7 +368,7 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
   static const char* who = "gsr_cross_attention_backward";
   if (!ctx) return GSR_EINVAL;
   AttnArgs a;
-  gsr_status st = attention_args(ctx, d, q, k, v, kv_lengths, mask, o, who, &a);
+  gsr_status st = attention_args(ctx, d, q, k, v, kv_lengths, mask, o, dout, who, &a);
   if (st) return st;
   const size_t eb = elem_bytes(d->dtype);
   const bool has_q = d->batch && d->queries, has_k = d->batch && d->keys;

@@ -74,7 +74,7 @@ struct AttnArgs {
   uint32_t rows;   // queries * (heads / kv_heads): the rows that meet one key head
   uint32_t tiles;  // workgroups across rows (keys in the key gradient)
   uint32_t splits, works, per_xcd;
-  bool whole;      // a row is a whole number of 16-byte chunks
+  bool aligned_kv, aligned_rows;  // keys and values (queries and gradients) lie in whole, aligned 16-byte chunks
   float scale;
   FastDiv share;   // row -> query; the rest is the head within its group
   int64_t qs[3], ks[3], vs[3], os[3], ms[3], dos[3], dqs[3], dks[3], dvs[3];
@@ -201,66 +201,70 @@ __device__ __forceinline__ bool any_nonfinite(u32x4 c) {
   return bad;
 }
 
-// Copies tiles of R rows, a constant stride apart, to LDS through registers: thread (row, chunk) = (tid / kCols,
-// tid % kCols) takes kLoads rows.
+// Copies tiles of R rows to LDS, 1 KiB a wave at a time: thread (row, slot) = (tid / kChunks, tid % kChunks) of every
+// kPass rows, the slot holding the chunk that the permutation puts there.
 template <typename T, int DK, int R>
-struct Stream {
+struct Copier {
   using L = Tile<T, DK>;
-  static constexpr int kCols = L::kUsed <= 4 ? 4 : (L::kUsed <= 8 ? 8 : (L::kUsed <= 16 ? 16 : 32));
-  static constexpr int kPass = kAttnThreads / kCols;
-  static constexpr int kLoads = (R + kPass - 1) / kPass;
-  const T* base;
-  int64_t stride;
-  u32x4 reg[kLoads];
+  static constexpr int kPass = kAttnThreads / L::kChunks;
+  static constexpr int kSteps = (R + kPass - 1) / kPass;
+  static constexpr int kBytes = R * L::kRowBytes;
 
-  __device__ static __forceinline__ int row() { return int(threadIdx.x) / kCols; }
-  __device__ static __forceinline__ int chunk() { return int(threadIdx.x) % kCols; }
+  __device__ static __forceinline__ int row(int i) { return int(threadIdx.x) / L::kChunks + i * kPass; }
+  __device__ static __forceinline__ int col(int i) {
+    return ((int(threadIdx.x) % L::kChunks) ^ L::swizzle(row(i))) * L::kPer;
+  }
 
-  // Rows first .. of the tile, those from `end` on as zeros.
-  __device__ __forceinline__ void fetch(const AttnArgs& a, uint32_t first, uint32_t end) {
-    const int c = chunk() * L::kPer, dim = int(a.dim);
-    const T* p = base + int64_t(first + row()) * stride + c;
-    const bool full = first + R <= end && R % kPass == 0 && a.whole;
+  // Starts the copies of tile rows 0 .. from the addresses at(row), those at or past `rows` as zeros. The chunks travel
+  // from memory to LDS by themselves (direct); the caller waits for kSteps of them. Otherwise, or where a chunk ends
+  // past the row, they pass through registers.
+  template <typename F>
+  __device__ static __forceinline__ void start(char* tile, uint32_t rows, int dim, bool direct, F at) {
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = row() + i * kPass;
-      reg[i] = u32x4{0, 0, 0, 0};
-      if (full) {
-        if (c < dim) __builtin_memcpy(&reg[i], p + i * kPass * stride, 16);
-      } else if (c < dim && r < R && first + r < end) {
-        reg[i] = load_chunk(p - c + i * kPass * stride, c, dim);
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = row(i), c = col(i);
+      if (kSteps * kPass != R && r >= R) continue;
+      if (direct) {
+        if (rows >= R || r < int(rows)) {
+          if (L::kRow == DK && dim == DK) {
+            load_lds(at(r) + c, tile + (i * kPass * L::kRowBytes + wave * 1024));
+          } else if (c < dim) {
+            load_lds(at(r) + c, tile + (i * kPass * L::kRowBytes + wave * 1024));
+          }
+        } else {
+          *reinterpret_cast<u32x4*>(tile + (i * kPass * L::kRowBytes + int(threadIdx.x) * 16)) = u32x4{0, 0, 0, 0};
+        }
+      } else {
+        u32x4 v = {0, 0, 0, 0};
+        if (r < int(rows) && c < dim) v = load_chunk(at(r), c, dim);
+        *reinterpret_cast<u32x4*>(tile + (i * kPass * L::kRowBytes + int(threadIdx.x) * 16)) = v;
       }
     }
   }
-  // The same of packed rows first .. of a key head, `base` and the strides those of a batch entry.
-  __device__ __forceinline__ void fetch_rows(const AttnArgs& a, uint32_t kv_head, uint32_t first, const int64_t* st) {
-    const int c = chunk() * L::kPer, dim = int(a.dim);
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = row() + i * kPass;
-      reg[i] = u32x4{0, 0, 0, 0};
-      if (c < dim && r < R && first + r < a.rows) {
-        uint32_t query, head;
-        row_of(a, kv_head, first + r, &query, &head);
-        reg[i] = load_chunk(base + int64_t(query) * st[1] + int64_t(head) * st[2], c, dim);
-      }
-    }
-  }
-  __device__ __forceinline__ void put(char* s) const {
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = row() + i * kPass;
-      if ((R % kPass == 0 || r < R) && (kCols == L::kUsed || chunk() < L::kUsed))
-        *reinterpret_cast<u32x4*>(s + L::at(r, chunk())) = reg[i];
-    }
-  }
-  __device__ __forceinline__ bool nonfinite() const {
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) bad |= any_nonfinite<T>(reg[i]);
-    return bad;
+  __device__ static __forceinline__ void load_lds(const T* p, char* s) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p,
+                                     (__attribute__((address_space(3))) void*)s, 16, 0, 0);
   }
 };
+
+// The barrier of a tile: this wave's copies but the newest kPending have landed, its LDS accesses are done, and so are
+// every other wave's. kPending > 0 needs that many copies started after the awaited ones, which a whole tile has and a
+// tile that ends early may not have.
+template <int kPending>
+__device__ __forceinline__ void tile_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kPending) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Clears the chunks past the head dimension, which no copy writes.
+template <typename T, int DK>
+__device__ __forceinline__ void clear_tiles(char* s, int bytes, int dim) {
+  if (dim < Tile<T, DK>::kRow)
+    for (int e = int(threadIdx.x) * 16; e < bytes; e += kAttnThreads * 16)
+      *reinterpret_cast<u32x4*>(s + e) = u32x4{0, 0, 0, 0};
+}
 
 // An operand fragment straight from a row in memory.
 template <typename T>
@@ -292,6 +296,17 @@ __device__ __forceinline__ Vec<T, 8> to_frag(const f32x16& p, int s) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) f[j] = T(p[8 * s + j]);
   return f;
+}
+
+// Whether a tile holds a non-finite element (the part this thread looks at).
+template <typename T, int kBytes>
+__device__ __forceinline__ bool scan_nonfinite(const char* tile) {
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < kBytes; e += kAttnThreads * 16)
+    if (kBytes % (kAttnThreads * 16) == 0 || e + int(threadIdx.x) * 16 < kBytes)
+      bad |= any_nonfinite<T>(*reinterpret_cast<const u32x4*>(tile + e + int(threadIdx.x) * 16));
+  return bad;
 }
 
 // acc[dt] += (transposed tile rows) * (block p), over the block's 32 rows, which are tile rows r0 ..
@@ -378,8 +393,8 @@ __device__ __forceinline__ uint32_t visible(const uint8_t* mask, uint32_t key0, 
 // Host side (attention_fwd.hip): checks the descriptor and the inputs both directions share and fills the arguments.
 // *nothing is set when there is no query or no element to write.
 gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, const void* k, const void* v,
-                          const int32_t* kv_lengths, const uint8_t* mask, const void* o, const char* who,
-                          AttnArgs* a);
+                          const int32_t* kv_lengths, const uint8_t* mask, const void* o, const void* dout,
+                          const char* who, AttnArgs* a);
 
 // Fills tiles, splits and the grid of a launch: `tiles` workgroups per key head, split over `steps` tiles of the
 // streamed side when they alone do not fill the compute units.

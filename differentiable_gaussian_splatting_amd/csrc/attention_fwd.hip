@@ -2,8 +2,9 @@
 // the softmax (in base 2: exp(scale s) = 2^(c s), c = scale log2 e).
 //
 // A workgroup holds 128 rows (query, head of one key head's group: heads that share keys share the tiles), 32 to a
-// wave, and streams tiles of keys and values through LDS, double buffered: a tile's loads are in flight while the one
-// before it is multiplied, and one barrier a tile suffices. Scores are computed transposed (keys down, queries
+// wave, and streams tiles of keys and values through three LDS buffers: the copies of the next two tiles, which go from
+// memory to LDS without passing registers, are in flight while a tile is multiplied, and one barrier a tile suffices.
+// Scores are computed transposed (keys down, queries
 // across), so that a query's maximum and sum are a lane's own registers plus one exchange between the wave's halves.
 // With at most 32 rows (a served token) the waves take 32 keys each of a tile of 128 instead, and their results are
 // joined in LDS. With few rows and many keys, the keys are split over workgroups and k_attn_join adds the parts in
@@ -69,7 +70,7 @@ template <typename T, int DK, bool kMask, bool kFew>
 __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64) ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   using L = Tile<T, DK>;
   constexpr int KT = kFew ? 128 : kKeyTile<T, DK>, kBlocks = kFew ? 1 : KT / 32;
-  constexpr int kTile = KT * L::kRowBytes, kBuffers = kFew ? 1 : 2;
+  constexpr int kTile = KT * L::kRowBytes, kBuffers = !kFew ? 3 : (kTile <= (32 << 10) ? 2 : 1);
   constexpr int kJoin = kFew ? kAttnWaves * 32 * (L::kOut * 32 + 4) * 4 : 0;  // the waves' outputs
   constexpr int kBytes = 2 * kBuffers * kTile > kJoin ? 2 * kBuffers * kTile : kJoin;
   __shared__ __attribute__((aligned(16))) char s_tile[kBytes];
@@ -97,11 +98,14 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
   const uint32_t len = keys_of(a, w.batch), tiles = (len + KT - 1) / KT;
   const uint32_t t0 = uint32_t(uint64_t(tiles) * w.split / a.splits);
   const uint32_t t1 = uint32_t(uint64_t(tiles) * (w.split + 1) / a.splits);
-  Stream<T, DK, KT> ks, vs;
-  ks.base = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(w.kv_head) * a.ks[2];
-  vs.base = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(w.kv_head) * a.vs[2];
-  ks.stride = a.ks[1];
-  vs.stride = a.vs[1];
+  const T* kb = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(w.kv_head) * a.ks[2];
+  const T* vb = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(w.kv_head) * a.vs[2];
+  using Copy = Copier<T, DK, KT>;
+  auto start = [&](uint32_t t, char* s) {
+    const uint32_t key0 = t * KT;
+    Copy::start(s, len - key0, dim, a.aligned_kv, [&](int r) { return kb + int64_t(key0 + r) * a.ks[1]; });
+    Copy::start(s + kTile, len - key0, dim, a.aligned_kv, [&](int r) { return vb + int64_t(key0 + r) * a.vs[1]; });
+  };
 
   const float c = a.scale * kLog2e;
   const int r0 = kFew ? wave * 32 : 0;  // the tile rows of this wave's keys
@@ -127,35 +131,34 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
     }
     run.template add<kBlocks>(s, c, s_v, r0, kMask && odd, seen);
   };
-  if (t0 < t1) {
-    ks.fetch(a, t0 * KT, len);
-    vs.fetch(a, t0 * KT, len);
-  }
-  int at = 0;
+  clear_tiles<T, DK>(s_tile, 2 * kBuffers * kTile, dim);
+  __syncthreads();
+  constexpr int kAhead = kBuffers - 1;  // tiles in flight while one is multiplied
+  if (t0 < t1) start(t0, s_tile);
+  if (kAhead == 2 && t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
+  int buf = 0;
   for (uint32_t t = t0; t < t1; ++t) {
-    char *s_k = s_tile + at, *s_v = s_k + kTile;
-    ks.put(s_k);
-    vs.put(s_v);
-    bool odd = false;
-    if constexpr (kMask)
-      odd = __syncthreads_or(vs.nonfinite());
+    const char *s_k = s_tile + buf * 2 * kTile, *s_v = s_k + kTile;
+    if (kAhead == 2 && t + 1 < t1 && (t + 2) * KT <= len)
+      tile_barrier<2 * Copy::kSteps>();
     else
-      __syncthreads();
-    if (t + 1 < t1) {
-      ks.fetch(a, (t + 1) * KT, len);
-      vs.fetch(a, (t + 1) * KT, len);
-    }
+      tile_barrier<0>();
+    if (kAhead > 0 && t + kAhead < t1) start(t + kAhead, s_tile + (buf == 0 ? kAhead : buf - 1) * 2 * kTile);
+    bool odd = false;
+    if constexpr (kMask) odd = __syncthreads_or(scan_nonfinite<T, kTile>(s_v));
     if (row0 < a.rows) {
       if ((t + 1) * KT <= len)
         multiply(t, s_k, s_v, odd, std::false_type());
       else
         multiply(t, s_k, s_v, odd, std::true_type());
     }
-    if constexpr (kBuffers == 2)
-      at ^= 2 * kTile;
-    else
-      __syncthreads();
+    buf = buf == kAhead ? 0 : buf + 1;
+    if (kAhead == 0 && t + 1 < t1) {
+      tile_barrier<0>();
+      start(t + 1, s_tile);
+    }
   }
+  if constexpr (kFew) __syncthreads();  // the tiles' memory takes the waves' outputs
   float l = run.l + other_half(run.l);
   const int64_t part = (int64_t(w.batch * a.kv_heads + w.kv_head) * a.splits + w.split) * a.rows;
   if constexpr (kFew) {
@@ -259,8 +262,8 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs a) {
 }  // namespace
 
 gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, const void* k, const void* v,
-                          const int32_t* kv_lengths, const uint8_t* mask, const void* o, const char* who,
-                          AttnArgs* a) {
+                          const int32_t* kv_lengths, const uint8_t* mask, const void* o, const void* dout,
+                          const char* who, AttnArgs* a) {
   if (!d) return fail(ctx, GSR_EINVAL, "%s: null descriptor", who);
   if (d->dtype > GSR_BF16) return fail(ctx, GSR_EINVAL, "%s: unknown dtype %u", who, d->dtype);
   if (d->kv_heads == 0 || d->heads == 0 || d->heads % d->kv_heads)
@@ -291,7 +294,12 @@ gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, c
   a->keys = d->keys;
   a->dim = d->head_dim;
   a->scale = d->scale;
-  a->whole = d->head_dim % (16 / eb) == 0;
+  auto aligned = [&](const void* p, const int64_t* st) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (st[0] * int64_t(eb)) % 16 == 0 &&
+           (st[1] * int64_t(eb)) % 16 == 0 && (st[2] * int64_t(eb)) % 16 == 0 && d->head_dim * eb % 16 == 0;
+  };
+  a->aligned_kv = aligned(k, d->k_stride) && aligned(v, d->v_stride);
+  a->aligned_rows = aligned(q, d->q_stride) && aligned(dout, d->do_stride);
   a->share.set(d->heads / d->kv_heads);
   a->rows = d->queries * (d->heads / d->kv_heads);
   for (int i = 0; i < 3; ++i) {
@@ -318,7 +326,7 @@ extern "C" gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, co
   static const char* who = "gsr_cross_attention_forward";
   if (!ctx) return GSR_EINVAL;
   AttnArgs a;
-  gsr_status st = attention_args(ctx, d, q, k, v, kv_lengths, mask, o, who, &a);
+  gsr_status st = attention_args(ctx, d, q, k, v, kv_lengths, mask, o, nullptr, who, &a);
   if (st) return st;
   if (misaligned(lse, 4)) return fail(ctx, GSR_EINVAL, "%s: a pointer is not aligned to its element", who);
   if (!distinct({{d->o_stride[0], d->batch}, {d->o_stride[1], d->queries}, {d->o_stride[2], d->heads}}, d->head_dim))
@@ -330,7 +338,7 @@ extern "C" gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, co
   const bool few = a.rows <= 32;
   const uint32_t key_tile = few ? 128 : (d->dtype != GSR_F32 && d->head_dim <= 64 ? 64 : 32);
   const dim3 grid = attention_grid(&a, few ? 1 : (a.rows + kAttnRows - 1) / kAttnRows,
-                                   (uint64_t(a.keys) + key_tile - 1) / key_tile, few ? 512 : 1024);
+                                   (uint64_t(a.keys) + key_tile - 1) / key_tile, 512);
   if (a.splits > 1) {
     const size_t parts = size_t(a.batch) * a.kv_heads * a.splits * a.rows;
     if ((st = grow(ctx, ctx->arena.feat_part, parts * (a.dim + 2) * sizeof(float)))) return st;
