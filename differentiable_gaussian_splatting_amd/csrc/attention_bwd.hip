@@ -18,6 +18,10 @@ namespace {
 // wave's operands and sums.
 template <typename T, int DK, bool kMask>
 constexpr int kWavesPerSimd = sizeof(T) == 2 && DK <= 96 && !(kMask && DK > 64) ? 2 : 1;
+// 32-row blocks of a streamed tile: two give the matrix cores one block's products while the other's exponentials are
+// taken (D = 128, where one wave has a SIMD to itself).
+template <typename T, bool kMask>
+constexpr int kStreamBlocks = sizeof(T) == 2 && !kMask ? 2 : 1;
 template <typename T, int DK, bool kMask>
 constexpr int kWavesPerSimdKeys = sizeof(T) == 2 && DK <= 96 && !(kMask && DK > 32) ? 2 : 1;
 
@@ -55,11 +59,11 @@ struct Ranged {
 template <typename T, int DK, bool kMask>
 __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, DK>;
-  constexpr int KT = 32, kTile = KT * L::kRowBytes;
+  constexpr int kBlocks = kStreamBlocks<T, kMask>, KT = 32 * kBlocks, kTile = KT * L::kRowBytes;
   __shared__ __attribute__((aligned(16))) char s_tile[6 * kTile];
   AttnWork w;
   if (!w.set(a)) return;
-  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim);
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim), dim_in = int(a.dim_in);
   const uint32_t row0 = w.tile * kAttnRows + (tid >> 6) * 32, row = row0 + (lane & 31);
   const bool valid = row < a.rows;
   uint32_t query = 0, head = 0;
@@ -82,9 +86,9 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
                       int64_t(head) * a.os[2];
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) {
-        qf[kk] = load_frag(qr, kk, dim);
-        df[kk] = load_frag(dr, kk, dim);
-        const Vec<T, 8> of = load_frag(orow, kk, dim);
+        qf[kk] = load_frag(qr, kk, dim_in);
+        df[kk] = load_frag(dr, kk, dim_in);
+        const Vec<T, 8> of = load_frag(orow, kk, dim_in);
 #pragma unroll
         for (int j = 0; j < 8; ++j) delta = fmaf(float(df[kk][j]), float(of[j]), delta);
       }
@@ -103,8 +107,8 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
   using Copy = Copier<T, DK, KT>;
   auto start = [&](uint32_t t, char* s) {
     const uint32_t key0 = t * KT;
-    Copy::start(s, len - key0, dim, a.aligned_kv, [&](int r) { return kb + int64_t(key0 + r) * a.ks[1]; });
-    Copy::start(s + kTile, len - key0, dim, a.aligned_kv, [&](int r) { return vb + int64_t(key0 + r) * a.vs[1]; });
+    Copy::start(s, len - key0, dim_in, [&](int r) { return kb + int64_t(key0 + r) * a.ks[1]; });
+    Copy::start(s + kTile, len - key0, dim_in, [&](int r) { return vb + int64_t(key0 + r) * a.vs[1]; });
   };
 
   const float c = a.scale * kLog2e, delta_s = delta * a.scale;
@@ -113,26 +117,34 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
   for (int dt = 0; dt < L::kOut; ++dt) acc[dt] = f32x16{};
   Ranged<T, DK> range;
   auto multiply = [&](uint32_t t, const char* s_k, const char* s_v, bool odd, auto edge) {
-    f32x16 s = {}, dp = {};
+    f32x16 s[kBlocks], dp[kBlocks];
 #pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) s = mma(L::frag(s_k, 0, kk), qf[kk], s);
+    for (int b = 0; b < kBlocks; ++b) {
+      s[b] = dp[b] = f32x16{};
 #pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) dp = mma(L::frag(s_v, 0, kk), df[kk], dp);
-    uint32_t seen = 0;
-    if constexpr (kMask || decltype(edge)::value) {
-      seen = visible<kMask>(mask, t * KT, len);
+      for (int kk = 0; kk < DK / 16; ++kk) s[b] = mma(L::frag(s_k, 32 * b, kk), qf[kk], s[b]);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[i] = (seen >> i) & 1 ? s[i] : -INFINITY;
-        dp[i] = (seen >> i) & 1 ? dp[i] : 0.0f;
-      }
+      for (int kk = 0; kk < DK / 16; ++kk) dp[b] = mma(L::frag(s_v, 32 * b, kk), df[kk], dp[b]);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = exp2_fast(fmaf(s[i], c, -lse2)) * fmaf(dp[i], a.scale, -delta_s);
-    range.fit(s, acc);
-    contract<T, DK>(acc, s_k, 0, s, kMask && odd, seen);
+    for (int b = 0; b < kBlocks; ++b) {
+      uint32_t seen = 0;
+      if constexpr (kMask || decltype(edge)::value) {
+        seen = visible<kMask>(mask, t * KT + 32 * b, len);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[b][i] = (seen >> i) & 1 ? s[b][i] : -INFINITY;
+          dp[b][i] = (seen >> i) & 1 ? dp[b][i] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        s[b][i] = exp2_fast(fmaf(s[b][i], c, -lse2)) * fmaf(dp[b][i], a.scale, -delta_s);
+      range.fit(s[b], acc);
+      contract<T, DK>(acc, s_k, 32 * b, s[b], kMask && odd, seen);
+    }
   };
-  clear_tiles<T, DK>(s_tile, 6 * kTile, dim);
+  clear_tiles<T, DK>(s_tile, 6 * kTile, dim_in);
   __syncthreads();
   if (t0 < t1) start(t0, s_tile);
   if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
@@ -168,14 +180,14 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
 template <typename T, int DK, bool kMask>
 __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, DK>;
-  constexpr int QT = 32, kTile = QT * L::kRowBytes;
+  constexpr int kBlocks = kStreamBlocks<T, kMask>, QT = 32 * kBlocks, kTile = QT * L::kRowBytes;
   __shared__ __attribute__((aligned(16))) char s_tile[6 * kTile];
   __shared__ __attribute__((aligned(16))) float s_lse[3][QT];
   __shared__ __attribute__((aligned(16))) float s_delta[3][QT];
   __shared__ int64_t s_mask[3][kMask ? QT : 1];
   AttnWork w;
   if (!w.set(a)) return;
-  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim);
+  const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim), dim_in = int(a.dim_in);
   const uint32_t key0 = w.tile * kAttnRows + (tid >> 6) * 32, key = key0 + (lane & 31);
   const uint32_t len = keys_of(a, w.batch);
   const bool valid = key < len;
@@ -189,8 +201,8 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
                   int64_t(w.kv_head) * a.vs[2];
 #pragma unroll
     for (int kk = 0; kk < DK / 16; ++kk) {
-      kf[kk] = load_frag(kr, kk, dim);
-      vf[kk] = load_frag(vr, kk, dim);
+      kf[kk] = load_frag(kr, kk, dim_in);
+      vf[kk] = load_frag(vr, kk, dim_in);
     }
   }
   const uint32_t tiles = w.tile * kAttnRows < len ? (a.rows + QT - 1) / QT : 0;  // no visible key: nothing to sum
@@ -220,8 +232,8 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
       }
     }
     if (plain) {
-      Copy::start(s, a.rows - row0, dim, a.aligned_rows, [&](int r) { return qb + int64_t(row0 + r) * a.qs[1]; });
-      Copy::start(s + kTile, a.rows - row0, dim, a.aligned_rows,
+      Copy::start(s, a.rows - row0, dim_in, [&](int r) { return qb + int64_t(row0 + r) * a.qs[1]; });
+      Copy::start(s + kTile, a.rows - row0, dim_in,
                   [&](int r) { return db + int64_t(row0 + r) * a.dos[1]; });
     } else {
       auto row_at = [&](const T* base, const int64_t* st, int r) {
@@ -229,8 +241,8 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
         row_of(a, w.kv_head, row0 + r, &query, &head);
         return base + int64_t(query) * st[1] + int64_t(head) * st[2];
       };
-      Copy::start(s, a.rows - row0, dim, a.aligned_rows, [&](int r) { return row_at(qb, a.qs, r); });
-      Copy::start(s + kTile, a.rows - row0, dim, a.aligned_rows, [&](int r) { return row_at(db, a.dos, r); });
+      Copy::start(s, a.rows - row0, dim_in, [&](int r) { return row_at(qb, a.qs, r); });
+      Copy::start(s + kTile, a.rows - row0, dim_in, [&](int r) { return row_at(db, a.dos, r); });
     }
   };
 
@@ -249,7 +261,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
       if constexpr (kMask) s_mask[buf][tid] = mask_at;
     }
   };
-  clear_tiles<T, DK>(s_tile, 6 * kTile, dim);
+  clear_tiles<T, DK>(s_tile, 6 * kTile, dim_in);
   __syncthreads();
   if (t0 < t1) {
     start(t0, s_tile);
@@ -276,32 +288,40 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
     }
     if (t + 2 < t1) start(t + 2, s_tile + (next == 2 ? 0 : next + 1) * 2 * kTile);
     if (key0 < len) {
-      f32x16 s = {}, dp = {};
+      f32x16 s[kBlocks], dp[kBlocks];
 #pragma unroll
-      for (int kk = 0; kk < DK / 16; ++kk) s = mma(L::frag(s_q, 0, kk), kf[kk], s);
+      for (int b = 0; b < kBlocks; ++b) {
+        s[b] = dp[b] = f32x16{};
 #pragma unroll
-      for (int kk = 0; kk < DK / 16; ++kk) dp = mma(L::frag(s_d, 0, kk), vf[kk], dp);
-      uint32_t seen = 0;
+        for (int kk = 0; kk < DK / 16; ++kk) s[b] = mma(L::frag(s_q, 32 * b, kk), kf[kk], s[b]);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const Vec<float, 4> ls = *reinterpret_cast<const Vec<float, 4>*>(&s_lse[buf][8 * g + 4 * h]);
-        const Vec<float, 4> dl = *reinterpret_cast<const Vec<float, 4>*>(&s_delta[buf][8 * g + 4 * h]);
+        for (int kk = 0; kk < DK / 16; ++kk) dp[b] = mma(L::frag(s_d, 32 * b, kk), vf[kk], dp[b]);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = 4 * g + i;
-          s[e] = exp2_fast(fmaf(s[e], c, ls[i]));
-          dp[e] = s[e] * fmaf(dp[e], scale, dl[i]);
-          if constexpr (kMask) {
-            const bool vis = valid && ls[i] != -INFINITY && mask[s_mask[buf][8 * g + 4 * h + i]] != 0;
-            seen |= uint32_t(vis) << e;
-            s[e] = vis ? s[e] : 0.0f;
-            dp[e] = vis ? dp[e] : 0.0f;
+      for (int b = 0; b < kBlocks; ++b) {
+        uint32_t seen = 0;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int r = 32 * b + 8 * g + 4 * h;
+          const Vec<float, 4> ls = *reinterpret_cast<const Vec<float, 4>*>(&s_lse[buf][r]);
+          const Vec<float, 4> dl = *reinterpret_cast<const Vec<float, 4>*>(&s_delta[buf][r]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = 4 * g + i;
+            s[b][e] = exp2_fast(fmaf(s[b][e], c, ls[i]));
+            dp[b][e] = s[b][e] * fmaf(dp[b][e], scale, dl[i]);
+            if constexpr (kMask) {
+              const bool vis = valid && ls[i] != -INFINITY && mask[s_mask[buf][r + i]] != 0;
+              seen |= uint32_t(vis) << e;
+              s[b][e] = vis ? s[b][e] : 0.0f;
+              dp[b][e] = vis ? dp[b][e] : 0.0f;
+            }
           }
         }
+        contract<T, DK>(dv, s_d, 32 * b, s[b], kMask && odd, seen);
+        range.fit(dp[b], dk);
+        contract<T, DK>(dk, s_q, 32 * b, dp[b], kMask && odd, seen);
       }
-      contract<T, DK>(dv, s_d, 0, s, kMask && odd, seen);
-      range.fit(dp, dk);
-      contract<T, DK>(dk, s_q, 0, dp, kMask && odd, seen);
     }
     buf = next;
   }
@@ -392,19 +412,31 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  // one scratch buffer: do.o of every row, then the parts of whichever kernel splits (one after the other)
+  // one scratch buffer: copies of inputs, do.o of every row, then the parts of whichever kernel splits (in turn)
   AttnArgs b = a;
-  const dim3 grid_q = attention_grid(&a, (a.rows + kAttnRows - 1) / kAttnRows, (uint64_t(a.keys) + 31) / 32, 512);
-  const dim3 grid_k = attention_grid(&b, (b.keys + kAttnRows - 1) / kAttnRows, (uint64_t(b.rows) + 31) / 32, 512);
+  const uint32_t streamed = d->dtype != GSR_F32 && !mask ? 64 : 32;  // keys or rows of a streamed tile
+  const dim3 grid_q = attention_grid(&a, (a.rows + kAttnRows - 1) / kAttnRows, (uint64_t(a.keys) + streamed - 1) / streamed, 512);
+  const dim3 grid_k = attention_grid(&b, (b.keys + kAttnRows - 1) / kAttnRows, (uint64_t(b.rows) + streamed - 1) / streamed, 512);
   const size_t groups = size_t(a.batch) * a.kv_heads, deltas = (groups * a.rows + 3) / 4 * 4;
   size_t parts = 0;
   if (a.splits > 1) parts = groups * a.splits * a.rows * a.dim;
   if (b.splits > 1) parts = std::max(parts, 2 * groups * b.splits * b.keys * b.dim);
-  if ((st = grow(ctx, ctx->arena.feat_part, (deltas + parts) * sizeof(float)))) return st;
-  a.delta = b.delta = static_cast<float*>(ctx->arena.feat_part.ptr);
-  a.part = b.part = a.delta + deltas;
+  const auto inputs = {AttnInput{&a.q, a.qs, a.queries, a.heads},      AttnInput{&a.k, a.ks, a.keys, a.kv_heads},
+                       AttnInput{&a.v, a.vs, a.keys, a.kv_heads},      AttnInput{&a.o, a.os, a.queries, a.heads},
+                       AttnInput{&a.dout, a.dos, a.queries, a.heads}};
+  const size_t packed = attention_pack_bytes(a, d->dtype, inputs);
+  if ((st = grow(ctx, ctx->arena.feat_part, packed + (deltas + parts) * sizeof(float)))) return st;
+  a.delta = reinterpret_cast<float*>(static_cast<char*>(ctx->arena.feat_part.ptr) + packed);
+  a.part = a.delta + deltas;
   hipStream_t s = static_cast<hipStream_t>(stream);
   timing_mark(ctx, GSR_STAGE_ATTENTION_BACKWARD, s, false);
+  attention_pack(&a, d->dtype, inputs, ctx->arena.feat_part.ptr, s);
+  const uint32_t tiles = b.tiles, splits = b.splits, works = b.works, per_xcd = b.per_xcd;
+  b = a;
+  b.tiles = tiles;
+  b.splits = splits;
+  b.works = works;
+  b.per_xcd = per_xcd;
   attention_by_kind(d->dtype, a.dim, mask != nullptr && a.keys, [&](auto t, auto dk_, auto masked) {
     using T = decltype(t);
     constexpr int DK = decltype(dk_)::value;

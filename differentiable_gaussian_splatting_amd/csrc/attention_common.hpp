@@ -74,7 +74,7 @@ struct AttnArgs {
   uint32_t rows;   // queries * (heads / kv_heads): the rows that meet one key head
   uint32_t tiles;  // workgroups across rows (keys in the key gradient)
   uint32_t splits, works, per_xcd;
-  bool aligned_kv, aligned_rows;  // keys and values (queries and gradients) lie in whole, aligned 16-byte chunks
+  uint32_t dim_in;  // elements of a row of q, k, v, o and do: dim, or dim padded with zeros to whole 16-byte chunks
   float scale;
   FastDiv share;   // row -> query; the rest is the head within its group
   int64_t qs[3], ks[3], vs[3], os[3], ms[3], dos[3], dqs[3], dks[3], dvs[3];
@@ -165,22 +165,6 @@ struct Tile {
   }
 };
 
-// One 16-byte chunk of a row: elements col .. of `dim`, zeros beyond.
-template <typename T>
-__device__ __forceinline__ u32x4 load_chunk(const T* row, int col, int dim) {
-  constexpr int kPer = 16 / int(sizeof(T));
-  u32x4 r = {0, 0, 0, 0};
-  if (col + kPer <= dim) {
-    __builtin_memcpy(&r, row + col, 16);
-  } else {
-    Vec<T, kPer> e;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) e[i] = col + i < dim ? row[col + i] : T(0.0f);
-    r = __builtin_bit_cast(u32x4, e);
-  }
-  return r;
-}
-
 template <typename T>
 __device__ __forceinline__ bool finite_bits(T x) {
   if constexpr (sizeof(T) == 4)
@@ -216,30 +200,20 @@ struct Copier {
   }
 
   // Starts the copies of tile rows 0 .. from the addresses at(row), those at or past `rows` as zeros. The chunks travel
-  // from memory to LDS by themselves (direct); the caller waits for kSteps of them. Otherwise, or where a chunk ends
-  // past the row, they pass through registers.
+  // from memory to LDS by themselves: every wave that has rows starts kSteps of them for a whole tile, and the caller
+  // waits.
   template <typename F>
-  __device__ static __forceinline__ void start(char* tile, uint32_t rows, int dim, bool direct, F at) {
+  __device__ static __forceinline__ void start(char* tile, uint32_t rows, int dim, F at) {
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int r = row(i), c = col(i);
       if (kSteps * kPass != R && r >= R) continue;
-      if (direct) {
-        if (rows >= R || r < int(rows)) {
-          if (L::kRow == DK && dim == DK) {
-            load_lds(at(r) + c, tile + (i * kPass * L::kRowBytes + wave * 1024));
-          } else if (c < dim) {
-            load_lds(at(r) + c, tile + (i * kPass * L::kRowBytes + wave * 1024));
-          }
-        } else {
-          *reinterpret_cast<u32x4*>(tile + (i * kPass * L::kRowBytes + int(threadIdx.x) * 16)) = u32x4{0, 0, 0, 0};
-        }
-      } else {
-        u32x4 v = {0, 0, 0, 0};
-        if (r < int(rows) && c < dim) v = load_chunk(at(r), c, dim);
-        *reinterpret_cast<u32x4*>(tile + (i * kPass * L::kRowBytes + int(threadIdx.x) * 16)) = v;
-      }
+      if (c >= dim) continue;
+      if (rows >= R || r < int(rows))
+        load_lds(at(r) + c, tile + (i * kPass * L::kRowBytes + wave * 1024));
+      else
+        *reinterpret_cast<u32x4*>(tile + (i * kPass * L::kRowBytes + int(threadIdx.x) * 16)) = u32x4{0, 0, 0, 0};
     }
   }
   __device__ static __forceinline__ void load_lds(const T* p, char* s) {
@@ -266,16 +240,19 @@ __device__ __forceinline__ void clear_tiles(char* s, int bytes, int dim) {
       *reinterpret_cast<u32x4*>(s + e) = u32x4{0, 0, 0, 0};
 }
 
-// An operand fragment straight from a row in memory.
+// An operand fragment straight from a row in memory, zeros from `dim` (a whole number of chunks) on.
 template <typename T>
 __device__ __forceinline__ Vec<T, 8> load_frag(const T* row, int kk, int dim) {
   const int col = 16 * kk + 8 * int((threadIdx.x & 63) >> 5);
   Vec<T, 8> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = T(0.0f);
   if constexpr (sizeof(T) == 2) {
-    f = __builtin_bit_cast(Vec<T, 8>, load_chunk(row, col, dim));
+    if (col < dim) f = *reinterpret_cast<const Vec<T, 8>*>(row + col);
   } else {
-    const Vec<T, 4> a = __builtin_bit_cast(Vec<T, 4>, load_chunk(row, col, dim));
-    const Vec<T, 4> b = __builtin_bit_cast(Vec<T, 4>, load_chunk(row, col + 4, dim));
+    Vec<T, 4> a = {}, b = {};
+    if (col < dim) a = *reinterpret_cast<const Vec<T, 4>*>(row + col);
+    if (col + 4 < dim) b = *reinterpret_cast<const Vec<T, 4>*>(row + col + 4);
     f = Vec<T, 8>{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
   }
   return f;
@@ -391,10 +368,22 @@ __device__ __forceinline__ uint32_t visible(const uint8_t* mask, uint32_t key0, 
 }
 
 // Host side (attention_fwd.hip): checks the descriptor and the inputs both directions share and fills the arguments.
-// *nothing is set when there is no query or no element to write.
 gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, const void* k, const void* v,
                           const int32_t* kv_lengths, const uint8_t* mask, const void* o, const void* dout,
                           const char* who, AttnArgs* a);
+
+// An input of the kernels: its tensor and strides in the arguments, and the tokens and heads it has.
+struct AttnInput {
+  const void** p;
+  int64_t* stride;
+  uint32_t tokens, heads;
+};
+
+// The kernels read rows in aligned 16-byte chunks. Inputs that do not lie so (a head dimension of no whole number of
+// chunks, odd strides, a shifted pointer) are first copied, each row padded with zeros, to `scratch`: attention_pack
+// queues the copies and points the arguments at them, attention_pack_bytes says how much they take.
+size_t attention_pack_bytes(const AttnArgs& a, uint32_t dtype, std::initializer_list<AttnInput> in);
+void attention_pack(AttnArgs* a, uint32_t dtype, std::initializer_list<AttnInput> in, void* scratch, hipStream_t s);
 
 // Fills tiles, splits and the grid of a launch: `tiles` workgroups per key head, split over `steps` tiles of the
 // streamed side when they alone do not fill the compute units.

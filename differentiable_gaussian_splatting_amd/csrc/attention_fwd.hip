@@ -77,7 +77,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
   __shared__ float2 s_ml[kFew ? kAttnWaves * 32 : 1];
   AttnWork w;
   if (!w.set(a)) return;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, dim = int(a.dim);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, dim = int(a.dim), dim_in = int(a.dim_in);
   const uint32_t row0 = kFew ? 0 : w.tile * kAttnRows + wave * 32;
   const uint32_t row = row0 + (lane & 31);
   const bool valid = row < a.rows;
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
     const T* qr = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0] + int64_t(query) * a.qs[1] +
                   int64_t(head) * a.qs[2];
 #pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) qf[kk] = load_frag(qr, kk, dim);
+    for (int kk = 0; kk < DK / 16; ++kk) qf[kk] = load_frag(qr, kk, dim_in);
   }
   const uint8_t* mask = nullptr;
   if (kMask && valid)
@@ -103,8 +103,8 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
   using Copy = Copier<T, DK, KT>;
   auto start = [&](uint32_t t, char* s) {
     const uint32_t key0 = t * KT;
-    Copy::start(s, len - key0, dim, a.aligned_kv, [&](int r) { return kb + int64_t(key0 + r) * a.ks[1]; });
-    Copy::start(s + kTile, len - key0, dim, a.aligned_kv, [&](int r) { return vb + int64_t(key0 + r) * a.vs[1]; });
+    Copy::start(s, len - key0, dim_in, [&](int r) { return kb + int64_t(key0 + r) * a.ks[1]; });
+    Copy::start(s + kTile, len - key0, dim_in, [&](int r) { return vb + int64_t(key0 + r) * a.vs[1]; });
   };
 
   const float c = a.scale * kLog2e;
@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
     }
     run.template add<kBlocks>(s, c, s_v, r0, kMask && odd, seen);
   };
-  clear_tiles<T, DK>(s_tile, 2 * kBuffers * kTile, dim);
+  clear_tiles<T, DK>(s_tile, 2 * kBuffers * kTile, dim_in);
   __syncthreads();
   constexpr int kAhead = kBuffers - 1;  // tiles in flight while one is multiplied
   if (t0 < t1) start(t0, s_tile);
@@ -294,12 +294,6 @@ gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, c
   a->keys = d->keys;
   a->dim = d->head_dim;
   a->scale = d->scale;
-  auto aligned = [&](const void* p, const int64_t* st) {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (st[0] * int64_t(eb)) % 16 == 0 &&
-           (st[1] * int64_t(eb)) % 16 == 0 && (st[2] * int64_t(eb)) % 16 == 0 && d->head_dim * eb % 16 == 0;
-  };
-  a->aligned_kv = aligned(k, d->k_stride) && aligned(v, d->v_stride);
-  a->aligned_rows = aligned(q, d->q_stride) && aligned(dout, d->do_stride);
   a->share.set(d->heads / d->kv_heads);
   a->rows = d->queries * (d->heads / d->kv_heads);
   for (int i = 0; i < 3; ++i) {
@@ -314,6 +308,70 @@ gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, c
     a->dvs[i] = d->dv_stride[i];
   }
   return GSR_OK;
+}
+
+namespace {
+
+// Rows of one input, [batch][tokens][heads] of dim elements, to adjacent rows of dim_in: a thread per 16-byte chunk.
+template <typename T>
+__global__ __launch_bounds__(kAttnThreads) void k_attn_pack(const T* __restrict__ x, int64_t s0, int64_t s1,
+                                                            int64_t s2, uint32_t tokens, uint32_t heads, uint32_t dim,
+                                                            uint64_t chunks, uint32_t per_row, T* __restrict__ out) {
+  constexpr int kPer = 16 / int(sizeof(T));
+  const uint64_t id = uint64_t(blockIdx.x) * kAttnThreads + threadIdx.x;
+  if (id >= chunks) return;
+  const uint32_t c = uint32_t(id % per_row) * kPer;
+  const uint64_t row = id / per_row, token = row / heads;
+  const T* p = x + int64_t(token / tokens) * s0 + int64_t(token % tokens) * s1 + int64_t(row % heads) * s2 + c;
+  Vec<T, kPer> v;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = c + i < dim ? p[i] : T(0.0f);
+  reinterpret_cast<Vec<T, kPer>*>(out)[id] = v;
+}
+
+bool lies_in_chunks(const AttnArgs& a, size_t eb, const AttnInput& in) {
+  if (a.dim * eb % 16 || reinterpret_cast<uintptr_t>(*in.p) % 16) return false;
+  for (int i = 0; i < 3; ++i)
+    if (in.stride[i] * int64_t(eb) % 16) return false;
+  return true;
+}
+
+}  // namespace
+
+size_t attention_pack_bytes(const AttnArgs& a, uint32_t dtype, std::initializer_list<AttnInput> in) {
+  const size_t eb = elem_bytes(dtype), row = (a.dim * eb + 15) / 16 * 16;
+  size_t total = 0;
+  for (const AttnInput& t : in)
+    if (!lies_in_chunks(a, eb, t)) total += size_t(a.batch) * t.tokens * t.heads * row;
+  return total;
+}
+
+void attention_pack(AttnArgs* a, uint32_t dtype, std::initializer_list<AttnInput> in, void* scratch, hipStream_t s) {
+  const size_t eb = elem_bytes(dtype), row = (a->dim * eb + 15) / 16 * 16;
+  char* to = static_cast<char*>(scratch);
+  a->dim_in = uint32_t(row / eb);
+  for (const AttnInput& t : in) {
+    if (lies_in_chunks(*a, eb, t)) continue;
+    const uint64_t chunks = uint64_t(a->batch) * t.tokens * t.heads * (row / 16);
+    if (chunks) {
+      auto launch = [&](auto e) {
+        using T = decltype(e);
+        hipLaunchKernelGGL((k_attn_pack<T>), dim3(uint32_t((chunks + kAttnThreads - 1) / kAttnThreads)),
+                           dim3(kAttnThreads), 0, s, static_cast<const T*>(*t.p), t.stride[0], t.stride[1],
+                           t.stride[2], t.tokens, t.heads, a->dim, chunks, uint32_t(row / 16),
+                           reinterpret_cast<T*>(to));
+      };
+      if (eb == 4)
+        launch(float());
+      else
+        launch(_Float16());  // any two bytes
+    }
+    *t.p = to;
+    t.stride[2] = int64_t(row / eb);
+    t.stride[1] = t.stride[2] * t.heads;
+    t.stride[0] = t.stride[1] * t.tokens;
+    to += chunks * 16;
+  }
 }
 
 }  // namespace gsr
@@ -339,14 +397,16 @@ extern "C" gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, co
   const uint32_t key_tile = few ? 128 : (d->dtype != GSR_F32 && d->head_dim <= 64 ? 64 : 32);
   const dim3 grid = attention_grid(&a, few ? 1 : (a.rows + kAttnRows - 1) / kAttnRows,
                                    (uint64_t(a.keys) + key_tile - 1) / key_tile, 512);
-  if (a.splits > 1) {
-    const size_t parts = size_t(a.batch) * a.kv_heads * a.splits * a.rows;
-    if ((st = grow(ctx, ctx->arena.feat_part, parts * (a.dim + 2) * sizeof(float)))) return st;
-    a.part_ml = static_cast<float*>(ctx->arena.feat_part.ptr);
-    a.part = a.part_ml + parts * 2;
-  }
+  const auto inputs = {AttnInput{&a.q, a.qs, a.queries, a.heads}, AttnInput{&a.k, a.ks, a.keys, a.kv_heads},
+                       AttnInput{&a.v, a.vs, a.keys, a.kv_heads}};
+  const size_t packed = attention_pack_bytes(a, d->dtype, inputs);
+  const size_t parts = a.splits > 1 ? size_t(a.batch) * a.kv_heads * a.splits * a.rows : 0;
+  if ((st = grow(ctx, ctx->arena.feat_part, packed + parts * (a.dim + 2) * sizeof(float)))) return st;
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(ctx->arena.feat_part.ptr) + packed);
+  a.part = a.part_ml + parts * 2;
   hipStream_t s = static_cast<hipStream_t>(stream);
   timing_mark(ctx, GSR_STAGE_ATTENTION_FORWARD, s, false);
+  attention_pack(&a, d->dtype, inputs, ctx->arena.feat_part.ptr, s);
   attention_by_kind(d->dtype, a.dim, mask != nullptr && a.keys, [&](auto t, auto dk, auto masked) {
     using T = decltype(t);
     constexpr int DK = decltype(dk)::value;
