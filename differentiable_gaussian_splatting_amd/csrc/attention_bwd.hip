@@ -61,6 +61,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
   using L = Tile<T, DK>;
   constexpr int kBlocks = kStreamBlocks<T, kMask>, KT = 32 * kBlocks, kTile = KT * L::kRowBytes;
   __shared__ __attribute__((aligned(16))) char s_tile[6 * kTile];
+  __shared__ int s_odd[3];
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim), dim_in = int(a.dim_in);
@@ -116,6 +117,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
 #pragma unroll
   for (int dt = 0; dt < L::kOut; ++dt) acc[dt] = f32x16{};
   Ranged<T, DK> range;
+  uint32_t words[kBlocks][4], seen[kBlocks] = {};  // the mask of the tile that comes next; what this one shows
   auto multiply = [&](uint32_t t, const char* s_k, const char* s_v, bool odd, auto edge) {
     f32x16 s[kBlocks], dp[kBlocks];
 #pragma unroll
@@ -128,36 +130,48 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
     }
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
-      uint32_t seen = 0;
       if constexpr (kMask || decltype(edge)::value) {
-        seen = visible<kMask>(mask, t * KT + 32 * b, len);
+        if constexpr (!kMask) seen[b] = visible<false>(nullptr, t * KT + 32 * b, len);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[b][i] = (seen >> i) & 1 ? s[b][i] : -INFINITY;
-          dp[b][i] = (seen >> i) & 1 ? dp[b][i] : 0.0f;
+          s[b][i] = (seen[b] >> i) & 1 ? s[b][i] : -INFINITY;
+          dp[b][i] = (seen[b] >> i) & 1 ? dp[b][i] : 0.0f;
         }
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         s[b][i] = exp2_fast(fmaf(s[b][i], c, -lse2)) * fmaf(dp[b][i], a.scale, -delta_s);
       range.fit(s[b], acc);
-      contract<T, DK>(acc, s_k, 32 * b, s[b], kMask && odd, seen);
+      contract<T, DK>(acc, s_k, 32 * b, s[b], kMask && odd, seen[b]);
     }
   };
+  if (tid < 3) s_odd[tid] = 0;
+  if (kMask && t0 < t1) {
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) mask_words(mask, t0 * KT + 32 * b, len, words[b]);
+  }
   clear_tiles<T, DK>(s_tile, 6 * kTile, dim_in);
   __syncthreads();
   if (t0 < t1) start(t0, s_tile);
   if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
   int at = 0;
   for (uint32_t t = t0; t < t1; ++t) {
-    const char *s_k = s_tile + at, *s_v = s_k + kTile;
+    char *s_k = s_tile + at, *s_v = s_k + kTile;
     if (t + 1 < t1 && (t + 2) * KT <= len)
       tile_barrier<2 * Copy::kSteps>();
     else
       tile_barrier<0>();
+    if constexpr (kMask) {  // before the copies start, so that waiting for these loads does not wait for those
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        seen[b] = visible<true>(words[b], 0, 0);
+        mask_words(t + 1 < t1 ? mask : nullptr, (t + 1) * KT + 32 * b, len, words[b]);
+      }
+    }
     if (t + 2 < t1) start(t + 2, s_tile + (at >= 2 * kTile ? at - 2 * kTile : at + 4 * kTile));
     bool odd = false;
-    if constexpr (kMask) odd = __syncthreads_or(scan_nonfinite<T, kTile>(s_k));
+    if constexpr (kMask)
+      odd = tile_nonfinite<T, DK, KT>(s_k, t - t0, s_odd, [](int) { return true; });
     if (row0 < a.rows) {
       if ((t + 1) * KT <= len)
         multiply(t, s_k, s_v, odd, std::false_type());
@@ -185,6 +199,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
   __shared__ __attribute__((aligned(16))) float s_lse[3][QT];
   __shared__ __attribute__((aligned(16))) float s_delta[3][QT];
   __shared__ int64_t s_mask[3][kMask ? QT : 1];
+  __shared__ int s_odd[3];
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim), dim_in = int(a.dim_in);
@@ -261,11 +276,27 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
       if constexpr (kMask) s_mask[buf][tid] = mask_at;
     }
   };
+  // the mask bytes of a tile, one row each of this lane's 16 values of a block, a tile ahead
+  uint8_t seen_row[kMask ? kBlocks * 16 : 1];
+  auto fetch_mask = [&](uint32_t t, int buf) {
+    if constexpr (kMask) {
+#pragma unroll
+      for (int e = 0; e < kBlocks * 16; ++e) {
+        const int r = 32 * (e / 16) + 8 * (e % 16 / 4) + 4 * h + e % 4;
+        seen_row[e] = valid && t * QT + r < a.rows ? mask[s_mask[buf][r]] : uint8_t(0);
+      }
+    }
+  };
   clear_tiles<T, DK>(s_tile, 6 * kTile, dim_in);
+  if (tid < 3) s_odd[tid] = 0;
   __syncthreads();
   if (t0 < t1) {
     start(t0, s_tile);
     put_stats(0);
+    if constexpr (kMask) {
+      lds_barrier();
+      fetch_mask(t0, 0);
+    }
   }
   if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
   int buf = 0;
@@ -277,15 +308,15 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
       tile_barrier<2 * Copy::kSteps>();
     else
       tile_barrier<0>();
-    bool odd = false;
-    if constexpr (kMask) {
-      // a row that saw no key is taken as zeros, whatever it holds
-      for (int e = tid; e < QT * L::kChunks; e += kAttnThreads)
-        if (s_lse[buf][e / L::kChunks] == -INFINITY)
-          reinterpret_cast<u32x4*>(s_q)[e] = reinterpret_cast<u32x4*>(s_d)[e] = u32x4{0, 0, 0, 0};
-      __syncthreads();
-      odd = __syncthreads_or(scan_nonfinite<T, 2 * kTile>(s_q));
+    uint32_t seen[kBlocks] = {};
+    if constexpr (kMask) {  // the next tile's bytes before the copies start, as above
+#pragma unroll
+      for (int e = 0; e < kBlocks * 16; ++e) seen[e / 16] |= uint32_t(seen_row[e] != 0) << (e % 16);
+      if (t + 1 < t1) fetch_mask(t + 1, next);
     }
+    bool odd = false;
+    if constexpr (kMask)  // a row that saw no key is taken as zeros, whatever it holds
+      odd = tile_nonfinite<T, DK, 2 * QT>(s_q, t - t0, s_odd, [&](int r) { return s_lse[buf][r % QT] != -INFINITY; });
     if (t + 2 < t1) start(t + 2, s_tile + (next == 2 ? 0 : next + 1) * 2 * kTile);
     if (key0 < len) {
       f32x16 s[kBlocks], dp[kBlocks];
@@ -299,7 +330,6 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
       }
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        uint32_t seen = 0;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int r = 32 * b + 8 * g + 4 * h;
@@ -311,16 +341,15 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
             s[b][e] = exp2_fast(fmaf(s[b][e], c, ls[i]));
             dp[b][e] = s[b][e] * fmaf(dp[b][e], scale, dl[i]);
             if constexpr (kMask) {
-              const bool vis = valid && ls[i] != -INFINITY && mask[s_mask[buf][r + i]] != 0;
-              seen |= uint32_t(vis) << e;
+              const bool vis = (seen[b] >> e) & 1;
               s[b][e] = vis ? s[b][e] : 0.0f;
               dp[b][e] = vis ? dp[b][e] : 0.0f;
             }
           }
         }
-        contract<T, DK>(dv, s_d, 32 * b, s[b], kMask && odd, seen);
+        contract<T, DK>(dv, s_d, 32 * b, s[b], kMask && odd, seen[b]);
         range.fit(dp[b], dk);
-        contract<T, DK>(dk, s_q, 32 * b, dp[b], kMask && odd, seen);
+        contract<T, DK>(dk, s_q, 32 * b, dp[b], kMask && odd, seen[b]);
       }
     }
     buf = next;
@@ -415,8 +444,11 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
   // one scratch buffer: copies of inputs, do.o of every row, then the parts of whichever kernel splits (in turn)
   AttnArgs b = a;
   const uint32_t streamed = d->dtype != GSR_F32 && !mask ? 64 : 32;  // keys or rows of a streamed tile
-  const dim3 grid_q = attention_grid(&a, (a.rows + kAttnRows - 1) / kAttnRows, (uint64_t(a.keys) + streamed - 1) / streamed, 512);
-  const dim3 grid_k = attention_grid(&b, (b.keys + kAttnRows - 1) / kAttnRows, (uint64_t(b.rows) + streamed - 1) / streamed, 512);
+  const uint32_t slots = d->dtype != GSR_F32 && a.dim <= 64 ? 512 : 256, cost = d->dtype == GSR_F32 ? 1 : 4;
+  const dim3 grid_q = attention_grid(&a, (a.rows + kAttnRows - 1) / kAttnRows,
+                                     (uint64_t(a.keys) + streamed - 1) / streamed, slots, cost);
+  const dim3 grid_k = attention_grid(&b, (b.keys + kAttnRows - 1) / kAttnRows,
+                                     (uint64_t(b.rows) + streamed - 1) / streamed, slots, 2 * cost);
   const size_t groups = size_t(a.batch) * a.kv_heads, deltas = (groups * a.rows + 3) / 4 * 4;
   size_t parts = 0;
   if (a.splits > 1) parts = groups * a.splits * a.rows * a.dim;

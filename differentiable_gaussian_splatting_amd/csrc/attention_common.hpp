@@ -275,15 +275,31 @@ __device__ __forceinline__ Vec<T, 8> to_frag(const f32x16& p, int s) {
   return f;
 }
 
-// Whether a tile holds a non-finite element (the part this thread looks at).
-template <typename T, int kBytes>
-__device__ __forceinline__ bool scan_nonfinite(const char* tile) {
+// A barrier for LDS alone: copies from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Whether a tile holds a non-finite element, to every thread; keep(row) false makes that row zeros first. s_odd[3] is
+// cleared at the start; turn counts the tiles.
+template <typename T, int DK, int kRows, typename F>
+__device__ __forceinline__ bool tile_nonfinite(char* tile, uint32_t turn, int* s_odd, F keep) {
+  using L = Tile<T, DK>;
   bool bad = false;
 #pragma unroll
-  for (int e = 0; e < kBytes; e += kAttnThreads * 16)
-    if (kBytes % (kAttnThreads * 16) == 0 || e + int(threadIdx.x) * 16 < kBytes)
-      bad |= any_nonfinite<T>(*reinterpret_cast<const u32x4*>(tile + e + int(threadIdx.x) * 16));
-  return bad;
+  for (int e = int(threadIdx.x); e < kRows * L::kChunks; e += kAttnThreads) {
+    u32x4* p = reinterpret_cast<u32x4*>(tile) + e;
+    if (!keep(e / L::kChunks))
+      *p = u32x4{0, 0, 0, 0};
+    else
+      bad |= any_nonfinite<T>(*p);
+  }
+  if (bad) s_odd[turn % 3] = 1;
+  if (threadIdx.x == 0) s_odd[(turn + 1) % 3] = 0;
+  lds_barrier();
+  return s_odd[turn % 3] != 0;
 }
 
 // acc[dt] += (transposed tile rows) * (block p), over the block's 32 rows, which are tile rows r0 ..
@@ -339,31 +355,34 @@ __device__ __forceinline__ void store_column(T* row, const f32x16* acc, float f,
     }
 }
 
-// The visible ones of the 32 keys from `key0` on, as this lane's 16 values of the block see them. `mask` is the row's
-// (null: a row beyond the last sees nothing).
-template <bool kMask>
-__device__ __forceinline__ uint32_t visible(const uint8_t* mask, uint32_t key0, uint32_t len) {
+// The mask bytes of the 32 keys from `key0` on, as this lane's 16 values of the block see them: four adjacent keys a
+// word. `mask` is the row's (null: a row beyond the last sees nothing); keys past `len` are not read.
+__device__ __forceinline__ void mask_words(const uint8_t* mask, uint32_t key0, uint32_t len, uint32_t* words) {
   const uint32_t h = (threadIdx.x & 63) >> 5;
-  uint32_t seen = 0;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const uint32_t key = key0 + 8 * g + 4 * h;
-    uint32_t bytes = 0x01010101u;
-    if constexpr (kMask) {
-      bytes = 0;
-      if (mask) {
-        if (key + 4 <= len) {
-          __builtin_memcpy(&bytes, mask + key, 4);
-        } else {
-          for (uint32_t i = 0; i < 4; ++i)
-            if (key + i < len) bytes |= uint32_t(mask[key + i]) << (8 * i);
-        }
+    words[g] = 0;
+    if (mask && key < len) {
+      if (key + 4 <= len) {
+        __builtin_memcpy(&words[g], mask + key, 4);
+      } else {
+        for (uint32_t i = 0; i < 4 && key + i < len; ++i) words[g] |= uint32_t(mask[key + i]) << (8 * i);
       }
     }
+  }
+}
+
+// Bit i: value i of the block of keys from `key0` on is visible, by its mask words (kMask) and the length.
+template <bool kMask>
+__device__ __forceinline__ uint32_t visible(const uint32_t* words, uint32_t key0, uint32_t len) {
+  const uint32_t h = (threadIdx.x & 63) >> 5;
+  uint32_t seen = 0;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      seen |= uint32_t(key + i < len && ((bytes >> (8 * i)) & 0xffu) != 0) << (4 * g + i);
-  }
+      seen |= uint32_t(kMask ? ((words[g] >> (8 * i)) & 0xffu) != 0 : key0 + 8 * g + 4 * h + i < len) << (4 * g + i);
   return seen;
 }
 
@@ -385,12 +404,22 @@ struct AttnInput {
 size_t attention_pack_bytes(const AttnArgs& a, uint32_t dtype, std::initializer_list<AttnInput> in);
 void attention_pack(AttnArgs* a, uint32_t dtype, std::initializer_list<AttnInput> in, void* scratch, hipStream_t s);
 
-// Fills tiles, splits and the grid of a launch: `tiles` workgroups per key head, split over `steps` tiles of the
-// streamed side when they alone do not fill the compute units.
-inline dim3 attention_grid(AttnArgs* a, uint32_t tiles, uint64_t steps, uint32_t want) {
+// Fills tiles, splits and the grid of a launch: `tiles` workgroups per key head, each streaming `steps` tiles, `slots`
+// workgroups at once on the card. The stream is split so that the last round is full: the time goes as rounds *
+// (steps of a part + cost), cost the steps that writing and adding a part take.
+inline dim3 attention_grid(AttnArgs* a, uint32_t tiles, uint64_t steps, uint32_t slots, uint32_t cost) {
   const uint64_t base = uint64_t(tiles) * a->kv_heads * a->batch;
   a->tiles = tiles;
-  a->splits = uint32_t(std::max<uint64_t>(1, std::min<uint64_t>(steps, want / std::max<uint64_t>(1, base))));
+  a->splits = 1;
+  uint64_t best = ~uint64_t(0);
+  for (uint64_t n = 1; base && n <= std::max<uint64_t>(1, std::min<uint64_t>(steps, 4 * slots / base + 4)); ++n) {
+    const uint64_t rounds = (base * n + slots - 1) / slots, t = rounds * ((steps + n - 1) / n + (n > 1 ? cost : 0));
+    if (t < best) {
+      best = t;
+      a->splits = uint32_t(n);
+    }
+    if (base >= 8 * slots) break;  // an unfull last round is little of eight
+  }
   a->works = uint32_t(base * a->splits);
   a->per_xcd = (a->works + kFeatXcds - 1) / kFeatXcds;
   return dim3(a->per_xcd * kFeatXcds);

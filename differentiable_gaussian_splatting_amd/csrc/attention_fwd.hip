@@ -75,6 +75,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
   constexpr int kBytes = 2 * kBuffers * kTile > kJoin ? 2 * kBuffers * kTile : kJoin;
   __shared__ __attribute__((aligned(16))) char s_tile[kBytes];
   __shared__ float2 s_ml[kFew ? kAttnWaves * 32 : 1];
+  __shared__ int s_odd[3];
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, dim = int(a.dim), dim_in = int(a.dim_in);
@@ -112,6 +113,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
   Running<T, DK> run;
 #pragma unroll
   for (int dt = 0; dt < L::kOut; ++dt) run.o[dt] = f32x16{};
+  uint32_t words[kBlocks][4], seen[kBlocks] = {};  // the mask of the tile that comes next; what this one shows
   auto multiply = [&](uint32_t t, const char* s_k, const char* s_v, bool odd, auto edge) {
     f32x16 s[kBlocks];
 #pragma unroll
@@ -120,11 +122,10 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) s[b] = mma(L::frag(s_k, r0 + 32 * b, kk), qf[kk], s[b]);
     }
-    uint32_t seen[kBlocks] = {};
     if constexpr (kMask || decltype(edge)::value) {
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        seen[b] = visible<kMask>(mask, t * KT + r0 + 32 * b, len);
+        if constexpr (!kMask) seen[b] = visible<false>(nullptr, t * KT + r0 + 32 * b, len);
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[b][i] = (seen[b] >> i) & 1 ? s[b][i] : -INFINITY;
       }
@@ -132,20 +133,32 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
     run.template add<kBlocks>(s, c, s_v, r0, kMask && odd, seen);
   };
   clear_tiles<T, DK>(s_tile, 2 * kBuffers * kTile, dim_in);
+  if (tid < 3) s_odd[tid] = 0;
+  if (kMask && t0 < t1) {
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b) mask_words(mask, t0 * KT + r0 + 32 * b, len, words[b]);
+  }
   __syncthreads();
   constexpr int kAhead = kBuffers - 1;  // tiles in flight while one is multiplied
   if (t0 < t1) start(t0, s_tile);
   if (kAhead == 2 && t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
   int buf = 0;
   for (uint32_t t = t0; t < t1; ++t) {
-    const char *s_k = s_tile + buf * 2 * kTile, *s_v = s_k + kTile;
+    char *s_k = s_tile + buf * 2 * kTile, *s_v = s_k + kTile;
     if (kAhead == 2 && t + 1 < t1 && (t + 2) * KT <= len)
       tile_barrier<2 * Copy::kSteps>();
     else
       tile_barrier<0>();
+    if constexpr (kMask) {  // before the copies start, so that waiting for these loads does not wait for those
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+        seen[b] = visible<true>(words[b], 0, 0);
+        mask_words(t + 1 < t1 ? mask : nullptr, (t + 1) * KT + r0 + 32 * b, len, words[b]);
+      }
+    }
     if (kAhead > 0 && t + kAhead < t1) start(t + kAhead, s_tile + (buf == 0 ? kAhead : buf - 1) * 2 * kTile);
     bool odd = false;
-    if constexpr (kMask) odd = __syncthreads_or(scan_nonfinite<T, kTile>(s_v));
+    if constexpr (kMask) odd = tile_nonfinite<T, DK, KT>(s_v, t - t0, s_odd, [](int) { return true; });
     if (row0 < a.rows) {
       if ((t + 1) * KT <= len)
         multiply(t, s_k, s_v, odd, std::false_type());
@@ -396,7 +409,7 @@ extern "C" gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, co
   const bool few = a.rows <= 32;
   const uint32_t key_tile = few ? 128 : (d->dtype != GSR_F32 && d->head_dim <= 64 ? 64 : 32);
   const dim3 grid = attention_grid(&a, few ? 1 : (a.rows + kAttnRows - 1) / kAttnRows,
-                                   (uint64_t(a.keys) + key_tile - 1) / key_tile, 512);
+                                   (uint64_t(a.keys) + key_tile - 1) / key_tile, few ? 256 : 512, 4);
   const auto inputs = {AttnInput{&a.q, a.qs, a.queries, a.heads}, AttnInput{&a.k, a.ks, a.keys, a.kv_heads},
                        AttnInput{&a.v, a.vs, a.keys, a.kv_heads}};
   const size_t packed = attention_pack_bytes(a, d->dtype, inputs);
