@@ -444,7 +444,7 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
   // one scratch buffer: copies of inputs, do.o of every row, then the parts of whichever kernel splits (in turn)
   AttnArgs b = a;
   const uint32_t streamed = d->dtype != GSR_F32 && !mask ? 64 : 32;  // keys or rows of a streamed tile
-  const uint32_t slots = d->dtype != GSR_F32 && a.dim <= 64 ? 512 : 256, cost = d->dtype == GSR_F32 ? 1 : 4;
+  const uint32_t slots = d->dtype != GSR_F32 && a.dim <= 64 ? 512 : 256, cost = 1;
   const dim3 grid_q = attention_grid(&a, (a.rows + kAttnRows - 1) / kAttnRows,
                                      (uint64_t(a.keys) + streamed - 1) / streamed, slots, cost);
   const dim3 grid_k = attention_grid(&b, (b.keys + kAttnRows - 1) / kAttnRows,

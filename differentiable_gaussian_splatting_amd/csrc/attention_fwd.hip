@@ -409,7 +409,8 @@ extern "C" gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, co
   const bool few = a.rows <= 32;
   const uint32_t key_tile = few ? 128 : (d->dtype != GSR_F32 && d->head_dim <= 64 ? 64 : 32);
   const dim3 grid = attention_grid(&a, few ? 1 : (a.rows + kAttnRows - 1) / kAttnRows,
-                                   (uint64_t(a.keys) + key_tile - 1) / key_tile, few ? 256 : 512, 4);
+                                   (uint64_t(a.keys) + key_tile - 1) / key_tile, few ? 256 : 512,
+                                   few ? 1 : (d->dtype == GSR_F32 ? 2 : 16));
   const auto inputs = {AttnInput{&a.q, a.qs, a.queries, a.heads}, AttnInput{&a.k, a.ks, a.keys, a.kv_heads},
                        AttnInput{&a.v, a.vs, a.keys, a.kv_heads}};
   const size_t packed = attention_pack_bytes(a, d->dtype, inputs);

@@ -2,7 +2,10 @@
 //
 // A thread owns V adjacent channels (16 bytes) and walks pixels, so a wave reads whole pixel rows whatever the group
 // width is (a group's channels alone are a short strip of each row). Sums are therefore kept per channel and joined
-// to groups afterwards:
+// to groups afterwards.
+//
+// Where a workgroup's registers hold all pixels of an image over a set of whole groups, one launch reads each feature
+// once (k_gn_small, k_gn_small_back: the small maps, whose time is launches). Otherwise:
 //   k_gn_stats     per (image, chunk of pixels, channel): mean and sum of squared deviations
 //   k_gn_finish    per (image, group): mean and rstd from the chunks' channel statistics
 //   k_gn_apply     y = act((x - mean) rstd gamma + beta)
@@ -156,31 +159,46 @@ __global__ __launch_bounds__(kThreads) void k_gn_stats(GnShape g, const T* __res
   }
 }
 
+// f(chunk, channel within the group, entry) over the chunks and channels of one (image, group), eight loads in flight.
+// Threads take (channel, part of the chunks), so that a wave reads along channels.
+template <typename F>
+__device__ __forceinline__ void for_parts(const GnShape& g, uint32_t img, uint32_t grp,
+                                          const float2* __restrict__ part, F f) {
+  const uint32_t width = min(g.cpg, uint32_t(kThreads)), lanes = kThreads / width;
+  const uint32_t tc = threadIdx.x % width, tk = threadIdx.x / width;
+  if (tk >= lanes) return;
+  for (uint32_t c = tc; c < g.cpg; c += width) {
+    const float2* base = part + int64_t(img) * g.chunks * g.channels + grp * g.cpg + c;
+    for (uint32_t k0 = tk; k0 < g.chunks; k0 += 8 * lanes) {
+      float2 v[8];
+#pragma unroll
+      for (uint32_t i = 0; i < 8; ++i)
+        if (k0 + i * lanes < g.chunks) v[i] = base[int64_t(k0 + i * lanes) * g.channels];
+#pragma unroll
+      for (uint32_t i = 0; i < 8; ++i)
+        if (k0 + i * lanes < g.chunks) f(k0 + i * lanes, c, v[i]);
+    }
+  }
+}
+
 // Mean and rstd of one (image, group) from its chunks' channel statistics: the weighted mean of the means, then
 // M2 = sum M2_i + n_i (mean_i - mean)^2.
 __global__ __launch_bounds__(kThreads) void k_gn_finish(GnShape g, const float2* __restrict__ part,
                                                         float2* __restrict__ stats) {
   __shared__ float s[kThreads];
   const uint32_t grp = blockIdx.x, img = blockIdx.y;
-  const float2* base = part + int64_t(img) * g.chunks * g.channels + grp * g.cpg;
-  const uint32_t n = g.chunks * g.cpg;
-  const float last = float(g.pixels - (g.chunks - 1) * g.chunk);
+  const float last = float(g.pixels - (g.chunks - 1) * g.chunk), full = float(g.chunk);
   const float total = float(g.pixels) * float(g.cpg);
+  const float w_full = full / total, w_last = last / total;
   float m = 0.0f;
-  for (uint32_t e = threadIdx.x; e < n; e += kThreads) {
-    const uint32_t k = e / g.cpg;
-    const float w = k + 1 == g.chunks ? last : float(g.chunk);
-    m = fmaf(w / total, base[int64_t(k) * g.channels + (e - k * g.cpg)].x, m);
-  }
+  for_parts(g, img, grp, part,
+            [&](uint32_t k, uint32_t, float2 v) { m = fmaf(k + 1 == g.chunks ? w_last : w_full, v.x, m); });
   const float mean = block_sum(m, s);
   float q = 0.0f;
-  for (uint32_t e = threadIdx.x; e < n; e += kThreads) {
-    const uint32_t k = e / g.cpg;
-    const float w = k + 1 == g.chunks ? last : float(g.chunk);
-    const float2 v = base[int64_t(k) * g.channels + (e - k * g.cpg)];
+  for_parts(g, img, grp, part, [&](uint32_t k, uint32_t, float2 v) {
     const float d = v.x - mean;
-    q += fmaf(w * d, d, v.y);
-  }
+    q += fmaf((k + 1 == g.chunks ? last : full) * d, d, v.y);
+  });
   const float var = block_sum(q, s) / total;
   if (threadIdx.x == 0) stats[img * g.groups + grp] = make_float2(mean, 1.0f / sqrtf(var + g.eps));
 }
@@ -221,8 +239,20 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GnShape g, const T* __res
   const uint32_t p0 = blockIdx.x * g.chunk, p1 = min(g.pixels, p0 + g.chunk);
   const T* xb = x + int64_t(blockIdx.y) * xi + c0;
   T* yb = y + int64_t(blockIdx.y) * yi + c0;
-#pragma unroll 4
-  for (uint32_t p = p0 + row; p < p1; p += g.rows) {
+  constexpr int kAtOnce = 4;  // loads in flight before the first store (y may be x, so the compiler keeps their order)
+  uint32_t p = p0 + row;
+  for (; p + (kAtOnce - 1) * g.rows < p1; p += kAtOnce * g.rows) {
+    float f[kAtOnce][V];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) load_f32<V>(xb + int64_t(p + k * g.rows) * xp, n_c, f[k]);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[k][i] = act_value<ACT>(fmaf(f[k][i] - ch.mean[i], ch.rstd[i], ch.beta[i]));
+      store_f32<V>(yb + int64_t(p + k * g.rows) * yp, n_c, f[k]);
+    }
+  }
+  for (; p < p1; p += g.rows) {
     float f[V];
     load_f32<V>(xb + int64_t(p) * xp, n_c, f);
 #pragma unroll
@@ -275,7 +305,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums(GnShape g, const T* __rest
   }
 }
 
-// One workgroup per (image, group): threads take (channel, part of the chunks), so that a wave reads along channels.
+// One workgroup per (image, group).
 __global__ __launch_bounds__(kThreads) void k_gn_sums_join(GnShape g, const float2* __restrict__ part,
                                                            const float* __restrict__ gamma,
                                                            float2* __restrict__ chan, float2* __restrict__ group) {
@@ -285,20 +315,28 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums_join(GnShape g, const floa
   const uint32_t tc = threadIdx.x % width, tk = threadIdx.x / width;
   float ga = 0.0f, gb = 0.0f;
   for (uint32_t c0 = 0; c0 < g.cpg; c0 += width) {
+    const bool live = c0 + tc < g.cpg;
     const uint32_t c = grp * g.cpg + c0 + tc;
     float a = 0.0f, b = 0.0f;
-    if (tk < lanes && c0 + tc < g.cpg) {
-      for (uint32_t k = tk; k < g.chunks; k += lanes) {
-        const float2 v = part[(int64_t(img) * g.chunks + k) * g.channels + c];
-        a += v.x;
-        b += v.y;
+    if (tk < lanes && live) {
+      const float2* base = part + int64_t(img) * g.chunks * g.channels + c;
+      for (uint32_t k0 = tk; k0 < g.chunks; k0 += 8 * lanes) {
+        float2 v[8];
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i)
+          v[i] = k0 + i * lanes < g.chunks ? base[int64_t(k0 + i * lanes) * g.channels] : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+          a += v[i].x;
+          b += v[i].y;
+        }
       }
     }
     __syncthreads();
     sa[threadIdx.x] = a;
     sb[threadIdx.x] = b;
     __syncthreads();
-    if (tk == 0 && c0 + tc < g.cpg) {
+    if (tk == 0 && live) {
       for (uint32_t k = 1; k < lanes; ++k) {
         a += sa[k * width + tc];
         b += sb[k * width + tc];
@@ -356,19 +394,260 @@ __global__ __launch_bounds__(kThreads) void k_gn_dx(GnShape g, const T* __restri
   const T* xb = x + int64_t(blockIdx.y) * xi + c0;
   const T* db = dy + int64_t(blockIdx.y) * di + c0;
   T* ob = dx + int64_t(blockIdx.y) * oi + c0;
-#pragma unroll 2
-  for (uint32_t p = p0 + row; p < p1; p += g.rows) {
-    float f[V], d[V];
-    load_f32<V>(xb + int64_t(p) * xp, n_c, f);
-    load_f32<V>(db + int64_t(p) * dp, n_c, d);
+  auto gradient = [&](const float* f, float* d) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const float xh = (f[i] - ch.mean[i]) * ch.rstd[i];
       const float dz = d[i] * act_slope<ACT>(fmaf(xh, ch.gamma[i], ch.beta[i]));
       d[i] = ch.rstd[i] * (fmaf(dz, ch.gamma[i], -m1[i]) - xh * m2[i]);
     }
+  };
+  uint32_t p = p0 + row;
+  for (; p + g.rows < p1; p += 2 * g.rows) {  // two pixels' loads in flight before the first store
+    float f[2][V], d[2][V];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      load_f32<V>(xb + int64_t(p + k * g.rows) * xp, n_c, f[k]);
+      load_f32<V>(db + int64_t(p + k * g.rows) * dp, n_c, d[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      gradient(f[k], d[k]);
+      store_f32<V>(ob + int64_t(p + k * g.rows) * op, n_c, d[k]);
+    }
+  }
+  if (p < p1) {
+    float f[V], d[V];
+    load_f32<V>(xb + int64_t(p) * xp, n_c, f);
+    load_f32<V>(db + int64_t(p) * dp, n_c, d);
+    gradient(f, d);
     store_f32<V>(ob + int64_t(p) * op, n_c, d);
   }
+}
+
+// ---- one launch: all pixels of an image over a set of whole groups in a workgroup's registers
+
+constexpr int kSmallThreads = 1024, kHoldForward = 8, kHoldBackward = 4;  // vectors of an input a thread holds
+
+struct GnSet {
+  uint32_t groups, channels;  // of a full set; the last may have fewer
+  uint32_t cols, rows;        // threads across the set's channels and across pixels
+};
+
+// Totals over the workgroup's pixels of every channel (s_chan) from each thread's V values.
+// s_part: [kSmallThreads][V], s_sub: [kSmallThreads].
+template <int V>
+__device__ __forceinline__ void channel_totals(const GnSet& t, bool live, const float* v, float (*s_part)[V],
+                                               float* s_sub, float* s_chan) {
+  const uint32_t wide = t.cols * V, subs = max(1u, min(8u, kSmallThreads / wide));
+  __syncthreads();
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) s_part[threadIdx.x][i] = v[i];
+  }
+  __syncthreads();
+  for (uint32_t e = threadIdx.x; e < subs * wide; e += kSmallThreads) {
+    const uint32_t ch = e % wide, sub = e / wide;
+    float sum = 0.0f;
+    for (uint32_t r = sub; r < t.rows; r += subs) sum += s_part[r * t.cols + ch / V][ch % V];
+    if (subs > 1)
+      s_sub[e] = sum;
+    else
+      s_chan[ch] = sum;
+  }
+  __syncthreads();
+  if (subs > 1 && threadIdx.x < wide) {
+    float sum = 0.0f;
+    for (uint32_t k = 0; k < subs; ++k) sum += s_sub[k * wide + threadIdx.x];
+    s_chan[threadIdx.x] = sum;
+  }
+  __syncthreads();
+}
+
+// Sums over each group's channels of s_chan (times gamma, if given): a wave per group.
+__device__ __forceinline__ void group_totals(uint32_t groups, uint32_t cpg, const float* s_chan, const float* gamma,
+                                             float* s_group) {
+  const uint32_t lane = threadIdx.x & 63;
+  for (uint32_t g = threadIdx.x >> 6; g < groups; g += kSmallThreads / 64) {
+    float sum = 0.0f;
+    for (uint32_t c = lane; c < cpg; c += 64) sum = fmaf(s_chan[g * cpg + c], gamma ? gamma[g * cpg + c] : 1.0f, sum);
+#pragma unroll
+    for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
+    if (lane == 0) s_group[g] = sum;
+  }
+  __syncthreads();
+}
+
+// Shared memory of a set, at most kSmallThreads channels and as many groups.
+template <int V>
+struct SmallShared {
+  float part[kSmallThreads][V];
+  float sub[kSmallThreads], chan[2][kSmallThreads], group[2][kSmallThreads];
+};
+
+template <typename T, int V, int kHold>
+struct Held {
+  Vec<T, V> v[kHold];
+  __device__ __forceinline__ void load(const T* base, int64_t stride, uint32_t row, uint32_t rows, uint32_t pixels,
+                                       int n) {
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+      const uint32_t p = row + k * rows;
+      if (p >= pixels) continue;
+      if (n >= V) {
+        __builtin_memcpy(&v[k], base + int64_t(p) * stride, sizeof v[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] = i < n ? base[int64_t(p) * stride + i] : T(0.0f);
+      }
+    }
+  }
+};
+
+template <typename T, int ACT, int V>
+__global__ __launch_bounds__(kSmallThreads) void k_gn_small(GnShape g, GnSet t, const T* x, int64_t xi, int64_t xp,
+                                                            const float* __restrict__ gamma,
+                                                            const float* __restrict__ beta,
+                                                            float2* __restrict__ stats, T* y, int64_t yi,
+                                                            int64_t yp) {
+  constexpr int kHold = kHoldForward;
+  __shared__ SmallShared<V> s;
+  const uint32_t grp0 = blockIdx.x * t.groups, groups = min(t.groups, g.groups - grp0), c_set = grp0 * g.cpg;
+  const uint32_t col = threadIdx.x % t.cols, row = threadIdx.x / t.cols;
+  const int n_c = int(groups * g.cpg) - int(col * V);
+  const bool live = row < t.rows && n_c > 0;
+  Held<T, V, kHold> f;
+  if (live) f.load(x + int64_t(blockIdx.y) * xi + c_set + col * V, xp, row, t.rows, g.pixels, n_c);
+  float v[V], mean[V], scale[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    v[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k)
+      if (live && row + k * t.rows < g.pixels) v[i] += float(f.v[k][i]);
+  }
+  const float total = float(g.pixels) * float(g.cpg);
+  channel_totals<V>(t, row < t.rows, v, s.part, s.sub, s.chan[0]);
+  group_totals(groups, g.cpg, s.chan[0], nullptr, s.group[0]);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    mean[i] = i < n_c ? s.group[0][(col * V + i) / g.cpg] / total : 0.0f;
+    v[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+      const float d = live && row + k * t.rows < g.pixels && i < n_c ? float(f.v[k][i]) - mean[i] : 0.0f;
+      v[i] = fmaf(d, d, v[i]);
+    }
+  }
+  channel_totals<V>(t, row < t.rows, v, s.part, s.sub, s.chan[0]);
+  group_totals(groups, g.cpg, s.chan[0], nullptr, s.group[1]);
+  for (uint32_t k = threadIdx.x; k < groups; k += kSmallThreads)
+    stats[blockIdx.y * g.groups + grp0 + k] =
+        make_float2(s.group[0][k] / total, 1.0f / sqrtf(s.group[1][k] / total + g.eps));
+  if (!live) return;
+  float shift[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t c = c_set + col * V + i;
+    scale[i] = i < n_c ? 1.0f / sqrtf(s.group[1][(col * V + i) / g.cpg] / total + g.eps) : 0.0f;
+    if (i < n_c && gamma) scale[i] *= gamma[c];
+    shift[i] = i < n_c && beta ? beta[c] : 0.0f;
+  }
+  T* yb = y + int64_t(blockIdx.y) * yi + c_set + col * V;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    const uint32_t p = row + k * t.rows;
+    if (p >= g.pixels) break;
+    float o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = act_value<ACT>(fmaf(float(f.v[k][i]) - mean[i], scale[i], shift[i]));
+    store_f32<V>(yb + int64_t(p) * yp, n_c, o);
+  }
+}
+
+template <typename T, int ACT, int V>
+__global__ __launch_bounds__(kSmallThreads) void k_gn_small_back(
+    GnShape g, GnSet t, const T* __restrict__ x, int64_t xi, int64_t xp, const float* __restrict__ gamma,
+    const float* __restrict__ beta, const float2* __restrict__ stats, const T* dy, int64_t di, int64_t dp, T* dx,
+    int64_t oi, int64_t op, float* __restrict__ dgamma, float* __restrict__ dbeta, float2* __restrict__ chan) {
+  constexpr int kHold = kHoldBackward;
+  __shared__ SmallShared<V> s;
+  const uint32_t grp0 = blockIdx.x * t.groups, groups = min(t.groups, g.groups - grp0), c_set = grp0 * g.cpg;
+  const uint32_t col = threadIdx.x % t.cols, row = threadIdx.x / t.cols;
+  const int n_c = int(groups * g.cpg) - int(col * V);
+  const bool live = row < t.rows && n_c > 0;
+  Held<T, V, kHold> f, d;
+  Channel<V> ch;
+  float a[V], b[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) a[i] = b[i] = 0.0f;
+  if (live) {
+    f.load(x + int64_t(blockIdx.y) * xi + c_set + col * V, xp, row, t.rows, g.pixels, n_c);
+    d.load(dy + int64_t(blockIdx.y) * di + c_set + col * V, dp, row, t.rows, g.pixels, n_c);
+    ch.load(g, blockIdx.y, c_set + col * V, n_c, stats, gamma, beta);
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+      if (row + k * t.rows >= g.pixels) break;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float xh = (float(f.v[k][i]) - ch.mean[i]) * ch.rstd[i];
+        const float dz = float(d.v[k][i]) * act_slope<ACT>(fmaf(xh, ch.gamma[i], ch.beta[i]));
+        a[i] += dz;
+        b[i] = fmaf(dz, xh, b[i]);
+      }
+    }
+  }
+  channel_totals<V>(t, row < t.rows, a, s.part, s.sub, s.chan[0]);
+  channel_totals<V>(t, row < t.rows, b, s.part, s.sub, s.chan[1]);
+  group_totals(groups, g.cpg, s.chan[0], gamma ? gamma + c_set : nullptr, s.group[0]);
+  group_totals(groups, g.cpg, s.chan[1], gamma ? gamma + c_set : nullptr, s.group[1]);
+  const bool alone = g.images == 1;
+  for (uint32_t c = threadIdx.x; c < groups * g.cpg; c += kSmallThreads) {
+    if (!alone) chan[int64_t(blockIdx.y) * g.channels + c_set + c] = make_float2(s.chan[0][c], s.chan[1][c]);
+    if (alone && dbeta) dbeta[c_set + c] = s.chan[0][c];
+    if (alone && dgamma) dgamma[c_set + c] = s.chan[1][c];
+  }
+  if (live && dx) {
+    const float inv = 1.0f / (float(g.pixels) * float(g.cpg));
+    float m1[V], m2[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t k = i < n_c ? (col * V + i) / g.cpg : 0;
+      m1[i] = s.group[0][k] * inv;
+      m2[i] = s.group[1][k] * inv;
+    }
+    T* ob = dx + int64_t(blockIdx.y) * oi + c_set + col * V;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+      const uint32_t p = row + k * t.rows;
+      if (p >= g.pixels) break;
+      float o[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float xh = (float(f.v[k][i]) - ch.mean[i]) * ch.rstd[i];
+        const float dz = float(d.v[k][i]) * act_slope<ACT>(fmaf(xh, ch.gamma[i], ch.beta[i]));
+        o[i] = ch.rstd[i] * (fmaf(dz, ch.gamma[i], -m1[i]) - xh * m2[i]);
+      }
+      store_f32<V>(ob + int64_t(p) * op, n_c, o);
+    }
+  }
+}
+
+// dgamma and dbeta from the images' channel sums, in order. (A last-workgroup-done counter inside k_gn_small_back saves
+// this launch of 3 us, but its fences across the dies cost 15 us.)
+__global__ void k_gn_images(uint32_t images, uint32_t channels, const float2* __restrict__ chan,
+                            float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  const uint32_t c = blockIdx.x * blockDim.x + threadIdx.x;
+  if (c >= channels) return;
+  float a = 0.0f, b = 0.0f;
+#pragma unroll 8
+  for (uint32_t n = 0; n < images; ++n) {
+    const float2 v = chan[int64_t(n) * channels + c];
+    a += v.x;
+    b += v.y;
+  }
+  if (dbeta) dbeta[c] = a;
+  if (dgamma) dgamma[c] = b;
 }
 
 // dgamma and dbeta when no pixel is there to sum.
@@ -420,6 +699,28 @@ GnShape shape_of(const gsr_group_norm* d) {
   return g;
 }
 
+// The set of groups whose pixels a workgroup of the one-launch form holds, `hold` vectors of `*v` elements a thread, or
+// false. Up to 1 MB of features, where time is latency, one group a workgroup and two elements a thread: most workgroups,
+// shortest chains of work (a 3 x 323 x 90 float16 map: 11 us a launch with 128-byte strips on six workgroups). Above,
+// the fewest groups that make a 128-byte strip of a row (64 if those do not fit; narrower strips waste the cache lines
+// they touch), if that gives the compute units enough workgroups.
+bool small_set(const GnShape& g, uint32_t dtype, uint32_t hold, GnSet* t, uint32_t* v) {
+  const uint32_t eb = dtype == GSR_F32 ? 4 : 2;
+  const bool tiny = uint64_t(g.images) * g.pixels * g.channels * eb <= (1u << 20);
+  *v = tiny ? 2 : 16 / eb;
+  for (uint32_t n = tiny ? 1 : std::min<uint32_t>(g.groups, (128 / eb + g.cpg - 1) / g.cpg); n >= 1; --n) {
+    t->groups = n;
+    t->channels = n * g.cpg;
+    t->cols = (t->channels + *v - 1) / *v;
+    if (t->cols * *v > kSmallThreads) continue;
+    if (!tiny && t->channels * eb < 64 && n < g.groups) return false;
+    t->rows = kSmallThreads / t->cols;
+    const uint64_t sets = (g.groups + n - 1) / n;
+    if (uint64_t(t->rows) * hold >= g.pixels) return tiny || sets * g.images >= 128;
+  }
+  return false;
+}
+
 dim3 grid_of(const GnShape& g, uint32_t dtype) {
   const uint32_t v = dtype == GSR_F32 ? 4 : 8;
   const uint32_t vecs = (g.channels + v - 1) / v;
@@ -464,6 +765,26 @@ extern "C" gsr_status gsr_group_norm_forward(gsr_ctx* ctx, void* stream, const g
   if ((st = check_out(ctx, d, d->y_stride, who, "y"))) return st;
   if ((st = enter(ctx))) return st;
   const GnShape g = shape_of(d);
+  GnSet set;
+  uint32_t vec;
+  if (small_set(g, d->dtype, kHoldForward, &set, &vec)) {
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    timing_mark(ctx, GSR_STAGE_GROUP_NORM_FORWARD, s, false);
+    by_kind(d, [&](auto t, auto a) {
+      using T = decltype(t);
+      auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((g.groups + set.groups - 1) / set.groups, g.images), dim3(kSmallThreads), 0, s,
+                           g, set, static_cast<const T*>(x), d->x_stride[0], d->x_stride[1], gamma, beta,
+                           reinterpret_cast<float2*>(stats), static_cast<T*>(y), d->y_stride[0], d->y_stride[1]);
+      };
+      if (vec == 2)
+        launch(k_gn_small<T, decltype(a)::value, 2>);
+      else
+        launch(k_gn_small<T, decltype(a)::value, 16 / int(sizeof(T))>);
+    });
+    timing_mark(ctx, GSR_STAGE_GROUP_NORM_FORWARD, s, true);
+    return check_launch(ctx, who);
+  }
   if ((st = grow(ctx, ctx->arena.feat_part, size_t(g.images) * g.chunks * g.channels * sizeof(float2)))) return st;
   float2* part = static_cast<float2*>(ctx->arena.feat_part.ptr);
   float2* out = reinterpret_cast<float2*>(stats);
@@ -513,7 +834,29 @@ extern "C" gsr_status gsr_group_norm_backward(gsr_ctx* ctx, void* stream, const 
   float2* chan = part + n_part;
   float2* group = chan + n_chan;
   const float2* in = reinterpret_cast<const float2*>(stats);
+  GnSet set;
   timing_mark(ctx, GSR_STAGE_GROUP_NORM_BACKWARD, s, false);
+  uint32_t vec;
+  if (small_set(g, d->dtype, kHoldBackward, &set, &vec)) {
+    by_kind(d, [&](auto t, auto a) {
+      using T = decltype(t);
+      auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3((g.groups + set.groups - 1) / set.groups, g.images), dim3(kSmallThreads), 0, s,
+                           g, set, static_cast<const T*>(x), d->x_stride[0], d->x_stride[1], gamma, beta, in,
+                           static_cast<const T*>(dy), d->dy_stride[0], d->dy_stride[1], static_cast<T*>(dx),
+                           d->dx_stride[0], d->dx_stride[1], dgamma, dbeta, chan);
+      };
+      if (vec == 2)
+        launch(k_gn_small_back<T, decltype(a)::value, 2>);
+      else
+        launch(k_gn_small_back<T, decltype(a)::value, 16 / int(sizeof(T))>);
+    });
+    if (g.images > 1 && (dgamma || dbeta))
+      hipLaunchKernelGGL(k_gn_images, dim3((g.channels + 63) / 64), dim3(64), 0, s, g.images, g.channels, chan, dgamma,
+                         dbeta);
+    timing_mark(ctx, GSR_STAGE_GROUP_NORM_BACKWARD, s, true);
+    return check_launch(ctx, who);
+  }
   by_kind(d, [&](auto t, auto a) {
     using T = decltype(t);
     const T *xt = static_cast<const T*>(x), *dt = static_cast<const T*>(dy);

@@ -14,6 +14,7 @@ namespace gsr {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAtOnce = 4;  // wide loads in flight before the first store (x may be out, so the compiler keeps their order)
 
 struct RotaryArgs {
   uint64_t items;  // tokens of all batch entries * units per token
@@ -59,10 +60,7 @@ __global__ __launch_bounds__(kThreads) void k_rotary_interleaved(RotaryArgs a, c
   const uint32_t h0 = blockIdx.y * a.heads_per_thread, h1 = min(a.heads, h0 + a.heads_per_thread);
   const T* xp = x + int64_t(b) * a.x_stride[0] + int64_t(t) * a.x_stride[1] + e0;
   T* op = out + int64_t(b) * a.out_stride[0] + int64_t(t) * a.out_stride[1] + e0;
-#pragma unroll 4
-  for (uint32_t h = h0; h < h1; ++h) {
-    float f[V];
-    load_f32<V>(xp + int64_t(h) * a.x_stride[2], n, f);
+  auto turned = [&](float* f) {
 #pragma unroll
     for (int i = 0; i < V / 2; ++i) {
       const float u = f[2 * i], v = f[2 * i + 1];
@@ -71,6 +69,21 @@ __global__ __launch_bounds__(kThreads) void k_rotary_interleaved(RotaryArgs a, c
         f[2 * i + 1] = fmaf(u, s[i], v * c[i]);
       }
     }
+  };
+  uint32_t h = h0;
+  for (; h + kAtOnce <= h1; h += kAtOnce) {
+    float f[kAtOnce][V];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) load_f32<V>(xp + int64_t(h + k) * a.x_stride[2], n, f[k]);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) turned(f[k]);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) store_f32<V>(op + int64_t(h + k) * a.out_stride[2], n, f[k]);
+  }
+  for (; h < h1; ++h) {
+    float f[V];
+    load_f32<V>(xp + int64_t(h) * a.x_stride[2], n, f);
+    turned(f);
     store_f32<V>(op + int64_t(h) * a.out_stride[2], n, f);
   }
 }
@@ -109,17 +122,36 @@ __global__ __launch_bounds__(kThreads) void k_rotary_halves(RotaryArgs a, const 
     c[i] = s[i] = 0.0f;
     if (i < n) turn(a, pos, e0 + i, back, &c[i], &s[i]);
   }
-#pragma unroll 2
-  for (uint32_t h = h0; h < h1; ++h) {
-    float u[V], v[V];
-    load_f32<V>(xp + int64_t(h) * a.x_stride[2] + e0, n, u);
-    load_f32<V>(xp + int64_t(h) * a.x_stride[2] + e0 + a.pairs, n, v);
+  auto turned = [&](float* u, float* v) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const float w = fmaf(u[i], c[i], -(v[i] * s[i]));
       v[i] = fmaf(u[i], s[i], v[i] * c[i]);
       u[i] = w;
     }
+  };
+  constexpr int kPairsAtOnce = kAtOnce / 2;
+  uint32_t h = h0;
+  for (; h + kPairsAtOnce <= h1; h += kPairsAtOnce) {
+    float u[kPairsAtOnce][V], v[kPairsAtOnce][V];
+#pragma unroll
+    for (int k = 0; k < kPairsAtOnce; ++k) {
+      load_f32<V>(xp + int64_t(h + k) * a.x_stride[2] + e0, n, u[k]);
+      load_f32<V>(xp + int64_t(h + k) * a.x_stride[2] + e0 + a.pairs, n, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kPairsAtOnce; ++k) turned(u[k], v[k]);
+#pragma unroll
+    for (int k = 0; k < kPairsAtOnce; ++k) {
+      store_f32<V>(op + int64_t(h + k) * a.out_stride[2] + e0, n, u[k]);
+      store_f32<V>(op + int64_t(h + k) * a.out_stride[2] + e0 + a.pairs, n, v[k]);
+    }
+  }
+  for (; h < h1; ++h) {
+    float u[V], v[V];
+    load_f32<V>(xp + int64_t(h) * a.x_stride[2] + e0, n, u);
+    load_f32<V>(xp + int64_t(h) * a.x_stride[2] + e0 + a.pairs, n, v);
+    turned(u, v);
     store_f32<V>(op + int64_t(h) * a.out_stride[2] + e0, n, u);
     store_f32<V>(op + int64_t(h) * a.out_stride[2] + e0 + a.pairs, n, v);
   }

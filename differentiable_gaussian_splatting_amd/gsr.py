@@ -466,6 +466,17 @@ def gsr_loss_l1_ssim(ctx: Context, out_rgba: torch.Tensor, target: torch.Tensor,
 _DTYPES = {torch.float32: GSR_F32, torch.float16: GSR_F16, torch.bfloat16: GSR_BF16}
 
 
+def _stream_on(ctx, stream):
+    """The given stream, or torch's current one on the context's device (its handle, without a Stream object: a third
+    of a small call's host time)."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(ctx.device.index)
+
+
+def _like(x):
+    """A contiguous empty tensor like x."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _need_feature(t, name, device, dtype=None, shape=None):
     """A strided feature tensor: on the device, of a supported (or the given) dtype, its last dimension adjacent."""
     if not isinstance(t, torch.Tensor):
@@ -523,14 +534,14 @@ def gsr_group_norm_forward(ctx: Context, x: torch.Tensor, gamma: torch.Tensor | 
     float32 [C] or None). Returns (y like x, stats float32 [N, groups, 2] = (mean, rstd))."""
     d = _group_norm_desc(ctx, x, gamma, beta, groups, eps, activation)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = _like(x)
     if stats is None:
         stats = torch.empty((x.shape[0], groups, 2), dtype=torch.float32, device=x.device)
     _need_feature(y, "y", ctx.device, x.dtype, x.shape)
     _need(stats, "stats", (torch.float32,), x.shape[0] * groups * 2, ctx.device)
     d.y_stride[:] = _image_strides(y, "y")
-    ctx.check(load().gsr_group_norm_forward(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(x), _ptr(gamma),
-                                            _ptr(beta), _ptr(y), _ptr(stats)), "gsr_group_norm_forward")
+    ctx.check(load().gsr_group_norm_forward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(x),
+                                            _ptr(gamma), _ptr(beta), _ptr(y), _ptr(stats)), "gsr_group_norm_forward")
     return y, stats
 
 
@@ -544,7 +555,7 @@ def gsr_group_norm_backward(ctx: Context, x: torch.Tensor, gamma: torch.Tensor |
     _need(stats, "stats", (torch.float32,), x.shape[0] * groups * 2, dev)
     _need_feature(dy, "dy", dev, x.dtype, x.shape)
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dx = _like(x)
     if dgamma is None:
         dgamma = torch.empty(C, dtype=torch.float32, device=dev)
     if dbeta is None:
@@ -554,8 +565,9 @@ def gsr_group_norm_backward(ctx: Context, x: torch.Tensor, gamma: torch.Tensor |
     _need(dbeta, "dbeta", (torch.float32,), C, dev)
     d.dy_stride[:] = _image_strides(dy, "dy")
     d.dx_stride[:] = _image_strides(dx, "dx")
-    ctx.check(load().gsr_group_norm_backward(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(x), _ptr(gamma),
-                                             _ptr(beta), _ptr(stats), _ptr(dy), _ptr(dx), _ptr(dgamma), _ptr(dbeta)),
+    ctx.check(load().gsr_group_norm_backward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(x),
+                                             _ptr(gamma), _ptr(beta), _ptr(stats), _ptr(dy), _ptr(dx), _ptr(dgamma),
+                                             _ptr(dbeta)),
               "gsr_group_norm_backward")
     return dx, dgamma, dbeta
 
@@ -574,7 +586,7 @@ def _rotary(ctx, x, positions, axis_pairs, base, layout, out, stream, name):
         raise ValueError(f"positions must be float32 [{B} or 1, {T}, {axes}]")
     _need(positions, "positions", (torch.float32,), None, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = _like(x)
     _need_feature(out, "out", dev, x.dtype, x.shape)
     d = gsr_rotary(_DTYPES[x.dtype], B, T, H, D, layout, axes)
     d.axis_pairs[:axes] = axis_pairs
@@ -582,7 +594,7 @@ def _rotary(ctx, x, positions, axis_pairs, base, layout, out, stream, name):
     d.x_stride[:] = x.stride()[:3]
     d.out_stride[:] = out.stride()[:3]
     d.position_stride = T * axes if positions.shape[0] == B else 0
-    ctx.check(getattr(load(), name)(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(x), _ptr(positions),
+    ctx.check(getattr(load(), name)(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(x), _ptr(positions),
                                     _ptr(out)), name)
     return out
 
@@ -639,14 +651,15 @@ def gsr_cross_attention_forward(ctx: Context, q: torch.Tensor, k: torch.Tensor, 
     d = _attention_desc(ctx, q, k, v, scale, kv_lengths, mask)
     B, Tq, H, _ = q.shape
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _like(q)
     if lse is None:
         lse = torch.empty((B, H, Tq), dtype=torch.float32, device=q.device)
     _need_feature(out, "out", ctx.device, q.dtype, q.shape)
     _need(lse, "lse", (torch.float32,), B * H * Tq, ctx.device)
     d.o_stride[:] = out.stride()[:3]
-    ctx.check(load().gsr_cross_attention_forward(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(q), _ptr(k),
-                                                 _ptr(v), _ptr(kv_lengths), _ptr(mask), _ptr(out), _ptr(lse)),
+    ctx.check(load().gsr_cross_attention_forward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(q),
+                                                 _ptr(k), _ptr(v), _ptr(kv_lengths), _ptr(mask), _ptr(out),
+                                                 _ptr(lse)),
               "gsr_cross_attention_forward")
     return out, lse
 
@@ -664,18 +677,18 @@ def gsr_cross_attention_backward(ctx: Context, q: torch.Tensor, k: torch.Tensor,
     _need_feature(dout, "dout", dev, q.dtype, q.shape)
     _need(lse, "lse", (torch.float32,), B * H * Tq, dev)
     if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        dq = _like(q)
     if dk is None:
-        dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        dk = _like(k)
     if dv is None:
-        dv = torch.empty(v.shape, dtype=q.dtype, device=dev)
+        dv = _like(v)
     for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
         _need_feature(t, name, dev, q.dtype, like.shape)
     for field, t in (("o_stride", out), ("do_stride", dout), ("dq_stride", dq), ("dk_stride", dk),
                      ("dv_stride", dv)):
         getattr(d, field)[:] = t.stride()[:3]
-    ctx.check(load().gsr_cross_attention_backward(ctx.handle, _stream(stream), ctypes.byref(d), _ptr(q), _ptr(k),
-                                                  _ptr(v), _ptr(kv_lengths), _ptr(mask), _ptr(out), _ptr(lse),
-                                                  _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv)),
+    ctx.check(load().gsr_cross_attention_backward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(q),
+                                                  _ptr(k), _ptr(v), _ptr(kv_lengths), _ptr(mask), _ptr(out),
+                                                  _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv)),
               "gsr_cross_attention_backward")
     return dq, dk, dv

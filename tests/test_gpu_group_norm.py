@@ -130,10 +130,11 @@ def test_strided_and_in_place(ctx):
     assert all(torch.equal(yb[i], y[0]) for i in range(3))
 
 
-def test_repeats_on_another_stream(ctx):
+@pytest.mark.parametrize("n,p", [(2, 5000), (9, 40)], ids=str)  # several launches; one
+def test_repeats_on_another_stream(ctx, n, p):
     from differentiable_gaussian_splatting_amd import gsr
-    banner("group norm on another stream, repeated")
-    x, dy = features(3, 2, 5000, 48, torch.float16).cuda(), normal(4, (2, 5000, 48), torch.float16).cuda()
+    banner(f"group norm on another stream, repeated, {n} x {p}")
+    x, dy = features(3, n, p, 48, torch.float16).cuda(), normal(4, (n, p, 48), torch.float16).cuda()
     y, st = gsr.gsr_group_norm_forward(ctx, x, None, None, 6, 1e-5, 1)
     ref = gsr.gsr_group_norm_backward(ctx, x, None, None, 6, st, dy, 1)
     torch.cuda.synchronize()
@@ -145,10 +146,11 @@ def test_repeats_on_another_stream(ctx):
         assert torch.equal(y, y2) and torch.equal(st, st2) and all(torch.equal(a, b) for a, b in zip(ref, got))
 
 
-def test_graph_replays(ctx):
+@pytest.mark.parametrize("n,p", [(2, 3000), (9, 40)], ids=str)
+def test_graph_replays(ctx, n, p):
     from differentiable_gaussian_splatting_amd import gsr
-    banner("group norm in a graph")
-    x, dy = features(3, 2, 3000, 48, torch.float32).cuda(), normal(4, (2, 3000, 48)).cuda()
+    banner(f"group norm in a graph, {n} x {p}")
+    x, dy = features(3, n, p, 48, torch.float32).cuda(), normal(4, (n, p, 48)).cuda()
     y, st = gsr.gsr_group_norm_forward(ctx, x, None, None, 6, 1e-5, 1)
     ref = (y, st) + gsr.gsr_group_norm_backward(ctx, x, None, None, 6, st, dy, 1)
     ref = [t.clone() for t in ref]
