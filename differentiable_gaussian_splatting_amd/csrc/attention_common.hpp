@@ -52,18 +52,6 @@ __device__ __forceinline__ float other_half(float v) {
   return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
-// n / d by multiplication, for n < 2^31.
-struct FastDiv {
-  uint32_t m, s, d;
-  void set(uint32_t by) {
-    d = by;
-    s = 0;
-    while ((uint64_t(1) << s) < by) ++s;
-    m = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << s) - by)) / by + 1);
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
-};
-
 struct AttnArgs {
   const void *q, *k, *v, *o, *dout;
   void *out, *dq, *dk, *dv;

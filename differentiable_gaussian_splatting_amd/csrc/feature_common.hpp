@@ -18,6 +18,18 @@ constexpr uint32_t kFeatXcds = 8;  // accelerator dies; workgroups are dealt to 
 template <typename T, int N>
 using Vec = T __attribute__((ext_vector_type(N)));
 
+// n / d by multiplication, for n < 2^31.
+struct FastDiv {
+  uint32_t m, s, d;
+  void set(uint32_t by) {
+    d = by;
+    s = 0;
+    while ((uint64_t(1) << s) < by) ++s;
+    m = uint32_t(((uint64_t(1) << 32) * ((uint64_t(1) << s) - by)) / by + 1);
+  }
+  __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
+
 // N adjacent elements as floats in one load of any alignment (global memory takes unaligned wide accesses; 16-byte
 // aligned ones touch the fewest cache lines), or the first `n` of them, the rest 0.
 template <int N, typename T>

@@ -1,6 +1,7 @@
 // Rotary positions with several axes: each pair of a head's elements is turned by an angle set by the token's position
-// on the pair's axis. One read and one write of the features; the sine and cosine of a (token, pair) are shared by all
-// heads, so a thread keeps them for its pairs and walks the heads.
+// on the pair's axis. One read and one write of the features. A workgroup takes a few whole tokens: it computes their
+// sines and cosines once, in LDS, and streams every head of them past, adjacent threads on adjacent 16 bytes; the first
+// loads are in flight while the angles are computed.
 //
 // The angle p base^(-i / n) is kept in turns: with f = base^(-i / n) / (2 pi) as a sum hi + lo of two floats (rounded
 // from a double on the host), p hi splits into its rounded product t and the exact remainder fma(p, hi, -t), so the
@@ -14,146 +15,107 @@ namespace gsr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAtOnce = 4;  // wide loads in flight before the first store (x may be out, so the compiler keeps their order)
 
 struct RotaryArgs {
-  uint64_t items;  // tokens of all batch entries * units per token
-  uint32_t tokens, heads, head_dim, units, pairs, axes, heads_per_thread;
+  uint32_t all_tokens;  // of all batch entries
+  uint32_t heads, head_dim, pairs, axes;
+  uint32_t group;       // tokens of a workgroup
+  uint32_t turning;     // units of a head that turn (split halves)
+  FastDiv units, head_div, pair_div, token_div;
   int64_t x_stride[3], out_stride[3], pos_stride;
   uint8_t axis[GSR_ROTARY_MAX_PAIRS];
   float hi[GSR_ROTARY_MAX_PAIRS], lo[GSR_ROTARY_MAX_PAIRS];
 };
 
-__device__ __forceinline__ void turn(const RotaryArgs& a, const float* pos, uint32_t pair, bool back, float* c,
-                                     float* s) {
+// The cosine and sine of pair `pair` at the token's positions `pos`.
+__device__ __forceinline__ float2 turn(const RotaryArgs& a, const float* pos, uint32_t pair, bool back) {
   const float p = pos[a.axis[pair]], hi = a.hi[pair];
   const float t = p * hi;
   const float r = (t - rintf(t)) + fmaf(p, a.lo[pair], fmaf(p, hi, -t));
   float sn, cs;
   sincospif(2.0f * r, &sn, &cs);
-  *c = cs;
-  *s = back ? -sn : sn;
+  return make_float2(cs, back ? -sn : sn);
 }
 
-// Interleaved pairs: a unit is V adjacent elements (V / 2 pairs).
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_rotary_interleaved(RotaryArgs a, const T* x,
-                                                                 const float* __restrict__ positions, T* out,
-                                                                 bool back) {
-  constexpr int V = 16 / sizeof(T);
-  const uint64_t id = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (id >= a.items) return;
-  const uint32_t unit = uint32_t(id % a.units);
-  const uint64_t tok = id / a.units;
-  const uint64_t b = tok / a.tokens, t = tok % a.tokens;
-  const float* pos = positions + int64_t(b) * a.pos_stride + int64_t(t) * a.axes;
-  const uint32_t e0 = unit * V;
-  const int n = int(a.head_dim) - int(e0);
-  float c[V / 2], s[V / 2];
+constexpr uint32_t kAngles = 2048;  // (token, pair) angles a workgroup keeps
+
+// A unit is V adjacent elements: V / 2 interleaved pairs, or with split halves V pairs (two loads, V elements apart by
+// the pairs) and, after those, V elements of the rest, which are copied.
+template <typename T, bool kHalves>
+__global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs a, const T* x, const float* __restrict__ positions,
+                                                     T* out, bool back) {
+  constexpr int V = 16 / sizeof(T), kAtOnce = kHalves ? 2 : 4;
+  __shared__ float2 s_turn[kAngles];
+  const uint32_t tok0 = blockIdx.x * a.group, group = min(a.group, a.all_tokens - tok0);
+  const uint32_t items = group * a.heads * a.units.d;
+  struct Item {
+    const T* from;
+    T* to;
+    uint32_t token, e0;  // within the group; first element (or pair, of a turning unit of split halves)
+    int n;               // elements (pairs) of the unit; <= 0: none
+    bool turns;
+    float u[V], v[kHalves ? V : 1];
+  };
+  auto load = [&](uint32_t e, Item& it) {
+    it.n = 0;
+    if (e >= items) return;
+    const uint32_t th = a.units.div(e), unit = e - th * a.units.d;
+    it.token = a.head_div.div(th);
+    const uint32_t head = th - it.token * a.heads;
+    const uint32_t tok = tok0 + it.token, b = a.token_div.div(tok), t = tok - b * a.token_div.d;
+    it.turns = !kHalves || unit < a.turning;
+    it.e0 = kHalves && !it.turns ? 2 * a.pairs + (unit - a.turning) * V : unit * V;
+    it.n = int(kHalves && it.turns ? a.pairs : a.head_dim) - int(it.e0);
+    it.from = x + int64_t(b) * a.x_stride[0] + int64_t(t) * a.x_stride[1] + int64_t(head) * a.x_stride[2] + it.e0;
+    it.to = out + int64_t(b) * a.out_stride[0] + int64_t(t) * a.out_stride[1] + int64_t(head) * a.out_stride[2] + it.e0;
+    load_f32<V>(it.from, it.n, it.u);
+    if constexpr (kHalves)
+      if (it.turns) load_f32<V>(it.from + a.pairs, it.n, it.v);
+  };
+  auto finish = [&](Item& it) {
+    if (it.n <= 0) return;
+    const float2* cs = s_turn + it.token * a.pairs;
+    if constexpr (kHalves) {
+      if (it.turns) {
 #pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    const uint32_t pair = e0 / 2 + i;
-    c[i] = 1.0f;
-    s[i] = 0.0f;
-    if (pair < a.pairs) turn(a, pos, pair, back, &c[i], &s[i]);
-  }
-  const uint32_t h0 = blockIdx.y * a.heads_per_thread, h1 = min(a.heads, h0 + a.heads_per_thread);
-  const T* xp = x + int64_t(b) * a.x_stride[0] + int64_t(t) * a.x_stride[1] + e0;
-  T* op = out + int64_t(b) * a.out_stride[0] + int64_t(t) * a.out_stride[1] + e0;
-  auto turned = [&](float* f) {
+        for (int i = 0; i < V; ++i) {
+          const float2 r = i < it.n ? cs[it.e0 + i] : make_float2(1.0f, 0.0f);
+          const float w = fmaf(it.u[i], r.x, -(it.v[i] * r.y));
+          it.v[i] = fmaf(it.u[i], r.y, it.v[i] * r.x);
+          it.u[i] = w;
+        }
+        store_f32<V>(it.to + a.pairs, it.n, it.v);
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const float u = f[2 * i], v = f[2 * i + 1];
-      if (e0 / 2 + i < a.pairs) {
-        f[2 * i] = fmaf(u, c[i], -(v * s[i]));
-        f[2 * i + 1] = fmaf(u, s[i], v * c[i]);
+      for (int i = 0; i < V / 2; ++i) {
+        const uint32_t pair = it.e0 / 2 + i;
+        if (pair >= a.pairs) break;
+        const float2 r = cs[pair];
+        const float u = it.u[2 * i], v = it.u[2 * i + 1];
+        it.u[2 * i] = fmaf(u, r.x, -(v * r.y));
+        it.u[2 * i + 1] = fmaf(u, r.y, v * r.x);
       }
     }
+    store_f32<V>(it.to, it.n, it.u);
   };
-  uint32_t h = h0;
-  for (; h + kAtOnce <= h1; h += kAtOnce) {
-    float f[kAtOnce][V];
+  Item it[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) load_f32<V>(xp + int64_t(h + k) * a.x_stride[2], n, f[k]);
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) turned(f[k]);
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) store_f32<V>(op + int64_t(h + k) * a.out_stride[2], n, f[k]);
+  for (int k = 0; k < kAtOnce; ++k) load(threadIdx.x + k * kThreads, it[k]);
+  for (uint32_t e = threadIdx.x; e < group * a.pairs; e += kThreads) {
+    const uint32_t token = a.pair_div.div(e), pair = e - token * a.pairs;
+    const uint32_t tok = tok0 + token, b = a.token_div.div(tok), t = tok - b * a.token_div.d;
+    s_turn[e] = turn(a, positions + int64_t(b) * a.pos_stride + int64_t(t) * a.axes, pair, back);
   }
-  for (; h < h1; ++h) {
-    float f[V];
-    load_f32<V>(xp + int64_t(h) * a.x_stride[2], n, f);
-    turned(f);
-    store_f32<V>(op + int64_t(h) * a.out_stride[2], n, f);
-  }
-}
-
-// Split halves: a unit is V adjacent pairs, elements (i ..) and (i + pairs ..); the units after them copy V elements
-// of the rest each.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_rotary_halves(RotaryArgs a, const T* x,
-                                                            const float* __restrict__ positions, T* out, bool back) {
-  constexpr int V = 16 / sizeof(T);
-  const uint64_t id = uint64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (id >= a.items) return;
-  const uint32_t unit = uint32_t(id % a.units);
-  const uint64_t tok = id / a.units;
-  const uint64_t b = tok / a.tokens, t = tok % a.tokens;
-  const float* pos = positions + int64_t(b) * a.pos_stride + int64_t(t) * a.axes;
-  const uint32_t turning = (a.pairs + V - 1) / V;
-  const uint32_t h0 = blockIdx.y * a.heads_per_thread, h1 = min(a.heads, h0 + a.heads_per_thread);
-  const T* xp = x + int64_t(b) * a.x_stride[0] + int64_t(t) * a.x_stride[1];
-  T* op = out + int64_t(b) * a.out_stride[0] + int64_t(t) * a.out_stride[1];
-  if (unit >= turning) {
-    const uint32_t e0 = 2 * a.pairs + (unit - turning) * V;
-    const int n = int(a.head_dim) - int(e0);
-    for (uint32_t h = h0; h < h1; ++h) {
-      float f[V];
-      load_f32<V>(xp + int64_t(h) * a.x_stride[2] + e0, n, f);
-      store_f32<V>(op + int64_t(h) * a.out_stride[2] + e0, n, f);
+  __syncthreads();
+  for (uint32_t e0 = threadIdx.x; e0 < items; e0 += kAtOnce * kThreads) {
+    // all of a batch is loaded before any of it is stored: x may be out, and the compiler keeps their order
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) finish(it[k]);
+    if (e0 + kAtOnce * kThreads < items) {
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) load(e0 + (kAtOnce + k) * kThreads, it[k]);
     }
-    return;
-  }
-  const uint32_t e0 = unit * V;
-  const int n = int(a.pairs) - int(e0);
-  float c[V], s[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    c[i] = s[i] = 0.0f;
-    if (i < n) turn(a, pos, e0 + i, back, &c[i], &s[i]);
-  }
-  auto turned = [&](float* u, float* v) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float w = fmaf(u[i], c[i], -(v[i] * s[i]));
-      v[i] = fmaf(u[i], s[i], v[i] * c[i]);
-      u[i] = w;
-    }
-  };
-  constexpr int kPairsAtOnce = kAtOnce / 2;
-  uint32_t h = h0;
-  for (; h + kPairsAtOnce <= h1; h += kPairsAtOnce) {
-    float u[kPairsAtOnce][V], v[kPairsAtOnce][V];
-#pragma unroll
-    for (int k = 0; k < kPairsAtOnce; ++k) {
-      load_f32<V>(xp + int64_t(h + k) * a.x_stride[2] + e0, n, u[k]);
-      load_f32<V>(xp + int64_t(h + k) * a.x_stride[2] + e0 + a.pairs, n, v[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kPairsAtOnce; ++k) turned(u[k], v[k]);
-#pragma unroll
-    for (int k = 0; k < kPairsAtOnce; ++k) {
-      store_f32<V>(op + int64_t(h + k) * a.out_stride[2] + e0, n, u[k]);
-      store_f32<V>(op + int64_t(h + k) * a.out_stride[2] + e0 + a.pairs, n, v[k]);
-    }
-  }
-  for (; h < h1; ++h) {
-    float u[V], v[V];
-    load_f32<V>(xp + int64_t(h) * a.x_stride[2] + e0, n, u);
-    load_f32<V>(xp + int64_t(h) * a.x_stride[2] + e0 + a.pairs, n, v);
-    turned(u, v);
-    store_f32<V>(op + int64_t(h) * a.out_stride[2] + e0, n, u);
-    store_f32<V>(op + int64_t(h) * a.out_stride[2] + e0 + a.pairs, n, v);
   }
 }
 
@@ -186,7 +148,8 @@ gsr_status rotary(gsr_ctx* ctx, void* stream, const gsr_rotary* d, const void* x
   gsr_status st = enter(ctx);
   if (st) return st;
   RotaryArgs a{};
-  a.tokens = d->tokens;
+  a.all_tokens = d->batch * d->tokens;
+  a.token_div.set(d->tokens);
   a.heads = d->heads;
   a.head_dim = d->head_dim;
   a.pairs = uint32_t(pairs);
@@ -205,26 +168,26 @@ gsr_status rotary(gsr_ctx* ctx, void* stream, const gsr_rotary* d, const void* x
       a.lo[at] = float(f - double(a.hi[at]));
     }
   const uint32_t v = d->dtype == GSR_F32 ? 4 : 8;
-  if (d->layout == GSR_ROTARY_INTERLEAVED)
-    a.units = (d->head_dim + v - 1) / v;
-  else
-    a.units = (a.pairs + v - 1) / v + (d->head_dim - 2 * a.pairs + v - 1) / v;
-  a.items = uint64_t(d->batch) * d->tokens * a.units;
-  // a thread takes several heads (sharing their sines) once the tokens alone fill the compute units
-  a.heads_per_thread = 1;
-  while (a.heads_per_thread < d->heads && a.items * (d->heads / (2 * a.heads_per_thread)) >= (1u << 19))
-    a.heads_per_thread *= 2;
-  const dim3 grid(uint32_t((a.items + kThreads - 1) / kThreads),
-                  (d->heads + a.heads_per_thread - 1) / a.heads_per_thread);
+  const bool halves = d->layout == GSR_ROTARY_HALVES;
+  a.turning = (a.pairs + v - 1) / v;
+  const uint32_t units = halves ? a.turning + (d->head_dim - 2 * a.pairs + v - 1) / v : (d->head_dim + v - 1) / v;
+  a.units.set(units);
+  a.head_div.set(d->heads);
+  a.pair_div.set(std::max(1u, a.pairs));
+  // whole tokens of about 2048 units a workgroup, at most kAngles angles; fewer where that leaves compute units idle
+  const uint64_t per_token = uint64_t(units) * d->heads;
+  uint64_t group = std::max<uint64_t>(1, std::min<uint64_t>(2048 / per_token, kAngles / std::max(1u, a.pairs)));
+  group = std::min(group, std::max<uint64_t>(1, a.all_tokens / 1024));
+  a.group = uint32_t(group);
+  const dim3 grid(uint32_t((uint64_t(a.all_tokens) + group - 1) / group));
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto launch = [&](auto t) {
     using T = decltype(t);
     const T* xt = static_cast<const T*>(x);
-    if (d->layout == GSR_ROTARY_INTERLEAVED)
-      hipLaunchKernelGGL((k_rotary_interleaved<T>), grid, dim3(kThreads), 0, s, a, xt, positions,
-                         static_cast<T*>(out), back);
+    if (halves)
+      hipLaunchKernelGGL((k_rotary<T, true>), grid, dim3(kThreads), 0, s, a, xt, positions, static_cast<T*>(out), back);
     else
-      hipLaunchKernelGGL((k_rotary_halves<T>), grid, dim3(kThreads), 0, s, a, xt, positions, static_cast<T*>(out),
+      hipLaunchKernelGGL((k_rotary<T, false>), grid, dim3(kThreads), 0, s, a, xt, positions, static_cast<T*>(out),
                          back);
   };
   timing_mark(ctx, GSR_STAGE_ROTARY, s, false);
