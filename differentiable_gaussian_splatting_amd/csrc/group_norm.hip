@@ -52,17 +52,19 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.0f;
 }
 
-// Sum over the workgroup, in a fixed order; every thread gets it. `s` holds kThreads floats.
+constexpr int kJoinThreads = 1024;  // one workgroup joins the chunks of an (image, group): most loads in flight
+
+// Sum over the workgroup, in a fixed order; every thread gets it. `s` holds kJoinThreads / 64 floats.
 __device__ __forceinline__ float block_sum(float v, float* s) {
-  const int t = threadIdx.x;
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) v += __shfl_xor(v, k);
   __syncthreads();
-  s[t] = v;
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
-  for (int h = kThreads / 2; h > 0; h >>= 1) {
-    if (t < h) s[t] += s[t + h];
-    __syncthreads();
-  }
-  return s[0];
+  float sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kJoinThreads / 64; ++k) sum += s[k];
+  return sum;
 }
 
 // Adds two running values of every thread over the threads of its channel column (the rows), leaving the totals in
@@ -164,7 +166,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_stats(GnShape g, const T* __res
 template <typename F>
 __device__ __forceinline__ void for_parts(const GnShape& g, uint32_t img, uint32_t grp,
                                           const float2* __restrict__ part, F f) {
-  const uint32_t width = min(g.cpg, uint32_t(kThreads)), lanes = kThreads / width;
+  const uint32_t width = min(g.cpg, uint32_t(kJoinThreads)), lanes = kJoinThreads / width;
   const uint32_t tc = threadIdx.x % width, tk = threadIdx.x / width;
   if (tk >= lanes) return;
   for (uint32_t c = tc; c < g.cpg; c += width) {
@@ -183,9 +185,9 @@ __device__ __forceinline__ void for_parts(const GnShape& g, uint32_t img, uint32
 
 // Mean and rstd of one (image, group) from its chunks' channel statistics: the weighted mean of the means, then
 // M2 = sum M2_i + n_i (mean_i - mean)^2.
-__global__ __launch_bounds__(kThreads) void k_gn_finish(GnShape g, const float2* __restrict__ part,
+__global__ __launch_bounds__(kJoinThreads) void k_gn_finish(GnShape g, const float2* __restrict__ part,
                                                         float2* __restrict__ stats) {
-  __shared__ float s[kThreads];
+  __shared__ float s[kJoinThreads / 64];
   const uint32_t grp = blockIdx.x, img = blockIdx.y;
   const float last = float(g.pixels - (g.chunks - 1) * g.chunk), full = float(g.chunk);
   const float total = float(g.pixels) * float(g.cpg);
@@ -306,12 +308,12 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums(GnShape g, const T* __rest
 }
 
 // One workgroup per (image, group).
-__global__ __launch_bounds__(kThreads) void k_gn_sums_join(GnShape g, const float2* __restrict__ part,
+__global__ __launch_bounds__(kJoinThreads) void k_gn_sums_join(GnShape g, const float2* __restrict__ part,
                                                            const float* __restrict__ gamma,
                                                            float2* __restrict__ chan, float2* __restrict__ group) {
-  __shared__ float sa[kThreads], sb[kThreads];
+  __shared__ float sa[kJoinThreads], sb[kJoinThreads], s[kJoinThreads / 64];
   const uint32_t grp = blockIdx.x, img = blockIdx.y;
-  const uint32_t width = min(g.cpg, uint32_t(kThreads)), lanes = kThreads / width;
+  const uint32_t width = min(g.cpg, uint32_t(kJoinThreads)), lanes = kJoinThreads / width;
   const uint32_t tc = threadIdx.x % width, tk = threadIdx.x / width;
   float ga = 0.0f, gb = 0.0f;
   for (uint32_t c0 = 0; c0 < g.cpg; c0 += width) {
@@ -336,19 +338,25 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums_join(GnShape g, const floa
     sa[threadIdx.x] = a;
     sb[threadIdx.x] = b;
     __syncthreads();
-    if (tk == 0 && live) {
-      for (uint32_t k = 1; k < lanes; ++k) {
-        a += sa[k * width + tc];
-        b += sb[k * width + tc];
+    // the parts of a channel, halving (a fixed order)
+    for (uint32_t half = lanes > 1 ? 1u << (31 - __clz(lanes - 1)) : 0; half > 0; half >>= 1) {
+      if (tk < half && tk + half < lanes) {
+        sa[threadIdx.x] += sa[threadIdx.x + half * width];
+        sb[threadIdx.x] += sb[threadIdx.x + half * width];
       }
+      __syncthreads();
+    }
+    if (tk == 0 && live) {
+      a = sa[threadIdx.x];
+      b = sb[threadIdx.x];
       chan[int64_t(img) * g.channels + c] = make_float2(a, b);
       const float gm = gamma ? gamma[c] : 1.0f;
       ga = fmaf(a, gm, ga);
       gb = fmaf(b, gm, gb);
     }
   }
-  ga = block_sum(ga, sa);
-  gb = block_sum(gb, sa);
+  ga = block_sum(ga, s);
+  gb = block_sum(gb, s);
   if (threadIdx.x == 0) {
     const float m = float(g.pixels) * float(g.cpg);
     group[img * g.groups + grp] = make_float2(ga / m, gb / m);
@@ -795,7 +803,7 @@ extern "C" gsr_status gsr_group_norm_forward(gsr_ctx* ctx, void* stream, const g
     const T* xt = static_cast<const T*>(x);
     hipLaunchKernelGGL((k_gn_stats<T>), grid_of(g, d->dtype), dim3(kThreads), 0, s, g, xt, d->x_stride[0],
                        d->x_stride[1], part);
-    hipLaunchKernelGGL(k_gn_finish, dim3(g.groups, g.images), dim3(kThreads), 0, s, g, part, out);
+    hipLaunchKernelGGL(k_gn_finish, dim3(g.groups, g.images), dim3(kJoinThreads), 0, s, g, part, out);
     hipLaunchKernelGGL((k_gn_apply<T, decltype(a)::value>), grid_of(g, d->dtype), dim3(kThreads), 0, s, g, xt, d->x_stride[0],
                        d->x_stride[1], gamma, beta, out, static_cast<T*>(y), d->y_stride[0], d->y_stride[1]);
   });
@@ -862,7 +870,7 @@ extern "C" gsr_status gsr_group_norm_backward(gsr_ctx* ctx, void* stream, const 
     const T *xt = static_cast<const T*>(x), *dt = static_cast<const T*>(dy);
     hipLaunchKernelGGL((k_gn_sums<T, decltype(a)::value>), grid_of(g, d->dtype), dim3(kThreads), 0, s, g, xt, d->x_stride[0],
                        d->x_stride[1], gamma, beta, in, dt, d->dy_stride[0], d->dy_stride[1], part);
-    hipLaunchKernelGGL(k_gn_sums_join, dim3(g.groups, g.images), dim3(kThreads), 0, s, g, part, gamma, chan, group);
+    hipLaunchKernelGGL(k_gn_sums_join, dim3(g.groups, g.images), dim3(kJoinThreads), 0, s, g, part, gamma, chan, group);
     dim3 grid = grid_of(g, d->dtype);
     if (!dx) grid.x = grid.y = 1;
     hipLaunchKernelGGL((k_gn_dx<T, decltype(a)::value>), grid, dim3(kThreads), 0, s, g, xt, d->x_stride[0], d->x_stride[1], gamma, beta,
