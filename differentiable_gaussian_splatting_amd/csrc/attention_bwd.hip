@@ -17,13 +17,14 @@ namespace {
 // Waves that share a SIMD, so that one multiplies while another computes exponentials: two where 256 registers hold a
 // wave's operands and sums.
 template <typename T, int DK, bool kMask>
-constexpr int kWavesPerSimd = sizeof(T) == 2 && DK <= 96 && !(kMask && DK > 64) ? 2 : 1;
+constexpr int kWavesPerSimd = DK <= 64 || (sizeof(T) == 2 && DK <= 96 && !kMask) ? 2 : 1;
 // 32-row blocks of a streamed tile: two give the matrix cores one block's products while the other's exponentials are
 // taken (D = 128, where one wave has a SIMD to itself).
 template <typename T, bool kMask>
 constexpr int kStreamBlocks = sizeof(T) == 2 && !kMask ? 2 : 1;
 template <typename T, int DK, bool kMask>
-constexpr int kWavesPerSimdKeys = sizeof(T) == 2 && DK <= 96 && !(kMask && DK > 32) ? 2 : 1;
+constexpr int kWavesPerSimdKeys =
+    sizeof(T) == 2 ? (DK <= 64 || (DK <= 96 && !kMask) ? 2 : 1) : (DK <= 32 || (DK <= 48 && !kMask) ? 2 : 1);
 
 // float16 values of ds, whose size follows the loss's scale, are kept in range by a power of two per column of the
 // accumulator (a query's dq, a key's dk): set from the first block that has a value, lowered when a later block would
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
   using L = Tile<T, DK>;
   constexpr int kBlocks = kStreamBlocks<T, kMask>, KT = 32 * kBlocks, kTile = KT * L::kRowBytes;
   __shared__ __attribute__((aligned(16))) char s_tile[6 * kTile];
-  __shared__ int s_odd[3];
+  __shared__ BadBits<T, DK, kMask ? KT : 1> s_bad;
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim), dim_in = int(a.dim_in);
@@ -70,33 +71,6 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
   uint32_t query = 0, head = 0;
   if (valid) row_of(a, w.kv_head, row, &query, &head);
   const int64_t stat = (int64_t(w.batch) * a.heads + head) * a.queries + query;
-  Vec<T, 8> qf[DK / 16], df[DK / 16];
-#pragma unroll
-  for (int kk = 0; kk < DK / 16; ++kk) qf[kk] = df[kk] = zero_frag<T>();
-  // a row that saw no key (lse = -inf) has p = 0 everywhere; whatever its gradient holds is not looked at
-  float lse2 = INFINITY, delta = 0.0f;
-  if (valid) {
-    const float lse = a.lse[stat];
-    if (lse != -INFINITY) {
-      lse2 = lse * kLog2e;
-      const T* qr = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0] + int64_t(query) * a.qs[1] +
-                    int64_t(head) * a.qs[2];
-      const T* dr = static_cast<const T*>(a.dout) + int64_t(w.batch) * a.dos[0] + int64_t(query) * a.dos[1] +
-                    int64_t(head) * a.dos[2];
-      const T* orow = static_cast<const T*>(a.o) + int64_t(w.batch) * a.os[0] + int64_t(query) * a.os[1] +
-                      int64_t(head) * a.os[2];
-#pragma unroll
-      for (int kk = 0; kk < DK / 16; ++kk) {
-        qf[kk] = load_frag(qr, kk, dim_in);
-        df[kk] = load_frag(dr, kk, dim_in);
-        const Vec<T, 8> of = load_frag(orow, kk, dim_in);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) delta = fmaf(float(df[kk][j]), float(of[j]), delta);
-      }
-    }
-  }
-  delta += other_half(delta);
-  if (valid && h == 0 && w.split == 0) a.delta[stat] = delta;
   const uint8_t* mask = nullptr;
   if (kMask && valid)
     mask = a.mask + int64_t(w.batch) * a.ms[0] + int64_t(head) * a.ms[1] + int64_t(query) * a.ms[2];
@@ -112,6 +86,42 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
     Copy::start(s + kTile, len - key0, dim_in, [&](int r) { return vb + int64_t(key0 + r) * a.vs[1]; });
   };
 
+  if constexpr (kMask) s_bad.clear();
+  clear_tiles<T, DK>(s_tile, 6 * kTile, dim_in);
+  __syncthreads();
+  if (t0 < t1) start(t0, s_tile);
+  if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
+  Vec<T, 8> qf[DK / 16], df[DK / 16];
+#pragma unroll
+  for (int kk = 0; kk < DK / 16; ++kk) qf[kk] = df[kk] = zero_frag<T>();
+  // a row that saw no key (lse = -inf) has p = 0 everywhere; whatever its gradient holds counts as zeros
+  float lse2 = INFINITY, delta = 0.0f;
+  if (valid) {
+    const float lse = a.lse[stat];
+    const T* qr = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0] + int64_t(query) * a.qs[1] +
+                  int64_t(head) * a.qs[2];
+    const T* dr = static_cast<const T*>(a.dout) + int64_t(w.batch) * a.dos[0] + int64_t(query) * a.dos[1] +
+                  int64_t(head) * a.dos[2];
+    const T* orow = static_cast<const T*>(a.o) + int64_t(w.batch) * a.os[0] + int64_t(query) * a.os[1] +
+                    int64_t(head) * a.os[2];
+#pragma unroll
+    for (int kk = 0; kk < DK / 16; ++kk) {
+      qf[kk] = load_frag(qr, kk, dim_in);
+      df[kk] = load_frag(dr, kk, dim_in);
+      const Vec<T, 8> of = load_frag(orow, kk, dim_in);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) delta = fmaf(float(df[kk][j]), float(of[j]), delta);
+    }
+    if (lse != -INFINITY) {
+      lse2 = lse * kLog2e;
+    } else {
+      delta = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < DK / 16; ++kk) qf[kk] = df[kk] = zero_frag<T>();
+    }
+  }
+  delta += other_half(delta);
+  if (valid && h == 0 && w.split == 0) a.delta[stat] = delta;
   const float c = a.scale * kLog2e, delta_s = delta * a.scale;
   f32x16 acc[L::kOut];
 #pragma unroll
@@ -137,23 +147,21 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
           s[b][i] = (seen[b] >> i) & 1 ? s[b][i] : -INFINITY;
           dp[b][i] = (seen[b] >> i) & 1 ? dp[b][i] : 0.0f;
         }
+        if constexpr (kMask) {
+          if (odd) spoil_rows<T, DK, KT>(s[b], seen[b], 32 * b, t - t0, s_bad);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         s[b][i] = exp2_fast(fmaf(s[b][i], c, -lse2)) * fmaf(dp[b][i], a.scale, -delta_s);
       range.fit(s[b], acc);
-      contract<T, DK>(acc, s_k, 32 * b, s[b], kMask && odd, seen[b]);
+      contract<T, DK>(acc, s_k, 32 * b, s[b]);
     }
   };
-  if (tid < 3) s_odd[tid] = 0;
   if (kMask && t0 < t1) {
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) mask_words(mask, t0 * KT + 32 * b, len, words[b]);
   }
-  clear_tiles<T, DK>(s_tile, 6 * kTile, dim_in);
-  __syncthreads();
-  if (t0 < t1) start(t0, s_tile);
-  if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
   int at = 0;
   for (uint32_t t = t0; t < t1; ++t) {
     char *s_k = s_tile + at, *s_v = s_k + kTile;
@@ -171,7 +179,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
     if (t + 2 < t1) start(t + 2, s_tile + (at >= 2 * kTile ? at - 2 * kTile : at + 4 * kTile));
     bool odd = false;
     if constexpr (kMask)
-      odd = tile_nonfinite<T, DK, KT>(s_k, t - t0, s_odd, [](int) { return true; });
+      odd = tile_make_finite<T, DK, KT>(s_k, t - t0, s_bad, [](int) { return true; });
     if (row0 < a.rows) {
       if ((t + 1) * KT <= len)
         multiply(t, s_k, s_v, odd, std::false_type());
@@ -199,27 +207,13 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
   __shared__ __attribute__((aligned(16))) float s_lse[3][QT];
   __shared__ __attribute__((aligned(16))) float s_delta[3][QT];
   __shared__ int64_t s_mask[3][kMask ? QT : 1];
-  __shared__ int s_odd[3];
+  __shared__ BadBits<T, DK, kMask ? 2 * QT : 1> s_bad;
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, h = lane >> 5, dim = int(a.dim), dim_in = int(a.dim_in);
   const uint32_t key0 = w.tile * kAttnRows + (tid >> 6) * 32, key = key0 + (lane & 31);
   const uint32_t len = keys_of(a, w.batch);
   const bool valid = key < len;
-  Vec<T, 8> kf[DK / 16], vf[DK / 16];
-#pragma unroll
-  for (int kk = 0; kk < DK / 16; ++kk) kf[kk] = vf[kk] = zero_frag<T>();
-  if (valid) {
-    const T* kr = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(key) * a.ks[1] +
-                  int64_t(w.kv_head) * a.ks[2];
-    const T* vr = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(key) * a.vs[1] +
-                  int64_t(w.kv_head) * a.vs[2];
-#pragma unroll
-    for (int kk = 0; kk < DK / 16; ++kk) {
-      kf[kk] = load_frag(kr, kk, dim_in);
-      vf[kk] = load_frag(vr, kk, dim_in);
-    }
-  }
   const uint32_t tiles = w.tile * kAttnRows < len ? (a.rows + QT - 1) / QT : 0;  // no visible key: nothing to sum
   const uint32_t t0 = uint32_t(uint64_t(tiles) * w.split / a.splits);
   const uint32_t t1 = uint32_t(uint64_t(tiles) * (w.split + 1) / a.splits);
@@ -288,7 +282,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
     }
   };
   clear_tiles<T, DK>(s_tile, 6 * kTile, dim_in);
-  if (tid < 3) s_odd[tid] = 0;
+  if constexpr (kMask) s_bad.clear();
   __syncthreads();
   if (t0 < t1) {
     start(t0, s_tile);
@@ -299,6 +293,20 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
     }
   }
   if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
+  Vec<T, 8> kf[DK / 16], vf[DK / 16];
+#pragma unroll
+  for (int kk = 0; kk < DK / 16; ++kk) kf[kk] = vf[kk] = zero_frag<T>();
+  if (valid) {
+    const T* kr = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(key) * a.ks[1] +
+                  int64_t(w.kv_head) * a.ks[2];
+    const T* vr = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(key) * a.vs[1] +
+                  int64_t(w.kv_head) * a.vs[2];
+#pragma unroll
+    for (int kk = 0; kk < DK / 16; ++kk) {
+      kf[kk] = load_frag(kr, kk, dim_in);
+      vf[kk] = load_frag(vr, kk, dim_in);
+    }
+  }
   int buf = 0;
   for (uint32_t t = t0; t < t1; ++t) {
     char *s_q = s_tile + buf * 2 * kTile, *s_d = s_q + kTile;
@@ -316,7 +324,8 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
     }
     bool odd = false;
     if constexpr (kMask)  // a row that saw no key is taken as zeros, whatever it holds
-      odd = tile_nonfinite<T, DK, 2 * QT>(s_q, t - t0, s_odd, [&](int r) { return s_lse[buf][r % QT] != -INFINITY; });
+      odd = tile_make_finite<T, DK, 2 * QT>(s_q, t - t0, s_bad,
+                                            [&](int r) { return s_lse[buf][r % QT] != -INFINITY; });
     if (t + 2 < t1) start(t + 2, s_tile + (next == 2 ? 0 : next + 1) * 2 * kTile);
     if (key0 < len) {
       f32x16 s[kBlocks], dp[kBlocks];
@@ -347,9 +356,17 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
             }
           }
         }
-        contract<T, DK>(dv, s_d, 32 * b, s[b], kMask && odd, seen[b]);
+        if constexpr (kMask) {
+          if (odd) {  // a bad query or gradient that a key sees spoils its gradients
+            spoil_rows<T, DK, 2 * QT>(s[b], seen[b], 32 * b, t - t0, s_bad);
+            spoil_rows<T, DK, 2 * QT>(s[b], seen[b], QT + 32 * b, t - t0, s_bad);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dp[b][i] = s[b][i] == s[b][i] ? dp[b][i] : s[b][i];
+          }
+        }
+        contract<T, DK>(dv, s_d, 32 * b, s[b]);
         range.fit(dp[b], dk);
-        contract<T, DK>(dk, s_q, 32 * b, dp[b], kMask && odd, seen[b]);
+        contract<T, DK>(dk, s_q, 32 * b, dp[b]);
       }
     }
     buf = next;
@@ -372,13 +389,16 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
   store_column<L::kOut>(ov, dv, kDown, dim);
 }
 
-// Adds the parts of split rows in order: a thread per (row, four elements). blockIdx.y = 1 adds dv after dk.
-template <typename T, bool kKeys>
+// Adds the parts of split rows, in a fixed order: kTurns threads to each (row, four elements), taking every kTurns-th
+// part. blockIdx.y = 1 adds dv after dk.
+template <typename T, bool kKeys, int kTurns>
 __global__ __launch_bounds__(kAttnThreads) void k_attn_add(AttnArgs a) {
-  const uint64_t id = uint64_t(blockIdx.x) * kAttnThreads + threadIdx.x;
+  constexpr int kQuads = kAttnThreads / kTurns;
+  __shared__ float s_part[kTurns > 1 ? kAttnThreads : 1][4];
+  const uint32_t lane = threadIdx.x % kQuads, turn = threadIdx.x / kQuads;
+  const uint64_t id = uint64_t(blockIdx.x) * kQuads + lane;
   const uint32_t per = kKeys ? a.keys : a.rows, quads = (a.dim + 3) / 4;
   const uint64_t rows = uint64_t(a.batch) * a.kv_heads * per;
-  if (id >= rows * quads) return;
   const uint32_t d = uint32_t(id % quads) * 4;
   const int n = int(a.dim - d);
   const uint64_t at = id / quads, group = at / per;
@@ -386,13 +406,26 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_add(AttnArgs a) {
   const float* part = a.part + (group * a.splits * per + row) * a.dim + d;
   if (kKeys && blockIdx.y) part += rows * a.splits * a.dim;
   float v[4] = {};
+  if (id < rows * quads) {
 #pragma unroll 4
-  for (uint32_t s = 0; s < a.splits; ++s) {
-    float x[4];
-    load_f32<4>(part + uint64_t(s) * per * a.dim, n, x);
+    for (uint32_t s = turn; s < a.splits; s += kTurns) {
+      float x[4];
+      load_f32<4>(part + uint64_t(s) * per * a.dim, n, x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += x[i];
+      for (int i = 0; i < 4; ++i) v[i] += x[i];
+    }
   }
+  if constexpr (kTurns > 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_part[threadIdx.x][i] = v[i];
+    __syncthreads();
+    if (turn) return;
+#pragma unroll
+    for (int k = 1; k < kTurns; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] += s_part[k * kQuads + lane][i];
+  }
+  if (id >= rows * quads) return;
   if constexpr (kKeys) {
     const int64_t* st = blockIdx.y ? a.dvs : a.dks;
     T* out = static_cast<T*>(blockIdx.y ? a.dv : a.dk);
@@ -444,11 +477,12 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
   // one scratch buffer: copies of inputs, do.o of every row, then the parts of whichever kernel splits (in turn)
   AttnArgs b = a;
   const uint32_t streamed = d->dtype != GSR_F32 && !mask ? 64 : 32;  // keys or rows of a streamed tile
-  const uint32_t slots = d->dtype != GSR_F32 && a.dim <= 64 ? 512 : 256, cost = 1;
+  const uint32_t slots_q = a.dim <= 64 ? 512 : 256, cost = 1;
+  const uint32_t slots_k = a.dim <= (d->dtype != GSR_F32 ? 64 : mask ? 32 : 48) ? 512 : 256;
   const dim3 grid_q = attention_grid(&a, (a.rows + kAttnRows - 1) / kAttnRows,
-                                     (uint64_t(a.keys) + streamed - 1) / streamed, slots, cost);
+                                     (uint64_t(a.keys) + streamed - 1) / streamed, slots_q, cost);
   const dim3 grid_k = attention_grid(&b, (b.keys + kAttnRows - 1) / kAttnRows,
-                                     (uint64_t(b.rows) + streamed - 1) / streamed, slots, 2 * cost);
+                                     (uint64_t(b.rows) + streamed - 1) / streamed, slots_k, 2 * cost);
   const size_t groups = size_t(a.batch) * a.kv_heads, deltas = (groups * a.rows + 3) / 4 * 4;
   size_t parts = 0;
   if (a.splits > 1) parts = groups * a.splits * a.rows * a.dim;
@@ -474,15 +508,22 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
     constexpr int DK = decltype(dk_)::value;
     constexpr bool kMask = decltype(masked)::value;
     const dim3 block(kAttnThreads);
-    auto blocks = [&](uint64_t n) { return uint32_t((n + kAttnThreads - 1) / kAttnThreads); };
+    // eight threads an element where the parts are many (and the elements few)
+    auto add = [&](auto keys, const AttnArgs& x, uint64_t rows) {
+      constexpr bool kKeys = decltype(keys)::value;
+      const uint64_t n = rows * ((x.dim + 3) / 4);
+      if (x.splits > 8)
+        hipLaunchKernelGGL((k_attn_add<T, kKeys, 8>), dim3(uint32_t((n + 31) / 32), kKeys ? 2 : 1), block, 0, s, x);
+      else if (x.splits > 1)
+        hipLaunchKernelGGL((k_attn_add<T, kKeys, 1>), dim3(uint32_t((n + 255) / 256), kKeys ? 2 : 1), block, 0, s, x);
+    };
     if (has_q) {
       hipLaunchKernelGGL((k_attn_dq<T, DK, kMask>), grid_q, block, 0, s, a);
-      if (a.splits > 1) hipLaunchKernelGGL((k_attn_add<T, false>), dim3(blocks(groups * a.rows * ((a.dim + 3) / 4))), block, 0, s, a);
+      add(std::false_type(), a, groups * a.rows);
     }
     if (has_k) {
       hipLaunchKernelGGL((k_attn_dkv<T, DK, kMask>), grid_k, block, 0, s, b);
-      if (b.splits > 1)
-        hipLaunchKernelGGL((k_attn_add<T, true>), dim3(blocks(groups * b.keys * ((b.dim + 3) / 4)), 2), block, 0, s, b);
+      add(std::true_type(), b, groups * b.keys);
     }
   });
   timing_mark(ctx, GSR_STAGE_ATTENTION_BACKWARD, s, true);

@@ -270,60 +270,97 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// Whether a tile holds a non-finite element, to every thread; keep(row) false makes that row zeros first. s_odd[3] is
-// cleared at the start; turn counts the tiles.
+// Which elements of a tile are not finite, a bit each: [tile turn % 3][row][32 columns a word].
+template <typename T, int DK, int kRows>
+struct BadBits {
+  static constexpr int kWords = Tile<T, DK>::kRow / 32;
+  uint32_t bits[3][kRows][kWords];
+  int any[3];
+
+  __device__ __forceinline__ void clear() {
+    for (int e = int(threadIdx.x); e < 3 * kRows * kWords; e += kAttnThreads) (&bits[0][0][0])[e] = 0;
+    if (threadIdx.x < 3) any[threadIdx.x] = 0;
+  }
+};
+
+// Makes the non-finite elements of a tile zeros and notes them (a masked value is 0 as a probability, but 0 * NaN is
+// NaN); the caller puts NaN where a visible one belongs. keep(row) false makes that row zeros. Returns whether there
+// were any, to every thread; turn counts the tiles.
 template <typename T, int DK, int kRows, typename F>
-__device__ __forceinline__ bool tile_nonfinite(char* tile, uint32_t turn, int* s_odd, F keep) {
+__device__ __forceinline__ bool tile_make_finite(char* tile, uint32_t turn, BadBits<T, DK, kRows>& bad, F keep) {
   using L = Tile<T, DK>;
-  bool bad = false;
+  const uint32_t now = turn % 3, next = (turn + 1) % 3;
 #pragma unroll
   for (int e = int(threadIdx.x); e < kRows * L::kChunks; e += kAttnThreads) {
     u32x4* p = reinterpret_cast<u32x4*>(tile) + e;
-    if (!keep(e / L::kChunks))
+    const int row = e / L::kChunks;
+    if (!keep(row)) {
       *p = u32x4{0, 0, 0, 0};
-    else
-      bad |= any_nonfinite<T>(*p);
+    } else if (any_nonfinite<T>(*p)) {
+      Vec<T, L::kPer> v = __builtin_bit_cast(Vec<T, L::kPer>, *p);
+      uint32_t bits = 0;
+#pragma unroll
+      for (int j = 0; j < L::kPer; ++j)
+        if (!finite_bits<T>(v[j])) {
+          bits |= 1u << j;
+          v[j] = T(0.0f);
+        }
+      *p = __builtin_bit_cast(u32x4, v);
+      const int col = ((e % L::kChunks) ^ L::swizzle(row)) * L::kPer;
+      atomicOr(&bad.bits[now][row][col / 32], bits << (col % 32));
+      bad.any[now] = 1;
+    }
   }
-  if (bad) s_odd[turn % 3] = 1;
-  if (threadIdx.x == 0) s_odd[(turn + 1) % 3] = 0;
+  for (int e = int(threadIdx.x); e < kRows * bad.kWords; e += kAttnThreads) (&bad.bits[next][0][0])[e] = 0;
+  if (threadIdx.x == 0) bad.any[next] = 0;
   lds_barrier();
-  return s_odd[turn % 3] != 0;
+  return bad.any[now] != 0;
+}
+
+// Makes the values of a block NaN that are visible and belong to a bad row of the tile (rows r0 ..).
+template <typename T, int DK, int kRows>
+__device__ __forceinline__ void spoil_rows(f32x16& s, uint32_t seen, int r0, uint32_t turn,
+                                           const BadBits<T, DK, kRows>& bad) {
+  const int h = int(threadIdx.x & 63) >> 5;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t* w = bad.bits[turn % 3][r0 + 8 * (i / 4) + 4 * h + i % 4];
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < bad.kWords; ++k) any |= w[k];
+    if (any && ((seen >> i) & 1)) s[i] = __builtin_nanf("");
+  }
+}
+
+// Makes the outputs of a column NaN at the bad elements of the rows r0 .. r0 + 31 that it sees.
+template <typename T, int DK, int kRows>
+__device__ __forceinline__ void spoil_outputs(f32x16* o, uint32_t seen, int r0, uint32_t turn,
+                                              const BadBits<T, DK, kRows>& bad) {
+  const int h = int(threadIdx.x & 63) >> 5;
+  const uint32_t other = __float_as_uint(other_half(__uint_as_float(seen)));
+#pragma unroll 1
+  for (int r = 0; r < 32; ++r) {
+    const bool vis = (((r >> 2) & 1) == h ? seen : other) >> ((r >> 3) * 4 + (r & 3)) & 1;
+    if (!vis) continue;
+#pragma unroll
+    for (int dt = 0; dt < Tile<T, DK>::kOut; ++dt) {
+      const uint32_t w = bad.bits[turn % 3][r0 + r][dt];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if ((w >> (8 * (i / 4) + 4 * h + i % 4)) & 1) o[dt][i] = __builtin_nanf("");
+    }
+  }
 }
 
 // acc[dt] += (transposed tile rows) * (block p), over the block's 32 rows, which are tile rows r0 ..
-// A masked value is 0 in p, but 0 * NaN is NaN: when the tile holds a non-finite element (guard), its finite elements
-// are multiplied alone, and a result becomes NaN where a non-finite one is visible (bit i of `seen`: value i of the
-// block is visible). Plain code, for the rare tile that needs it.
 template <typename T, int DK>
-__device__ __forceinline__ void contract(f32x16* acc, const char* tile, int r0, const f32x16& p, bool guard,
-                                         uint32_t seen) {
+__device__ __forceinline__ void contract(f32x16* acc, const char* tile, int r0, const f32x16& p) {
   using L = Tile<T, DK>;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const Vec<T, 8> b = to_frag<T>(p, s);
-    if (!guard) {
 #pragma unroll
-      for (int dt = 0; dt < L::kOut; ++dt) acc[dt] = mma(L::frag_t(tile, r0 + 16 * s, dt), b, acc[dt]);
-    } else {
-      Vec<T, 8> vis;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) vis[j] = T((seen >> (8 * s + j)) & 1 ? 1.0f : 0.0f);
-#pragma unroll
-      for (int dt = 0; dt < L::kOut; ++dt) {
-        Vec<T, 8> a = L::frag_t(tile, r0 + 16 * s, dt), odd;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool fin = finite_bits<T>(a[j]);
-          odd[j] = T(fin ? 0.0f : 1.0f);
-          a[j] = fin ? a[j] : T(0.0f);
-        }
-        acc[dt] = mma(a, b, acc[dt]);
-        f32x16 zero = {};
-        const f32x16 hits = mma(odd, vis, zero);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[dt][i] = hits[i] != 0.0f ? __builtin_nanf("") : acc[dt][i];
-      }
-    }
+    for (int dt = 0; dt < L::kOut; ++dt) acc[dt] = mma(L::frag_t(tile, r0 + 16 * s, dt), b, acc[dt]);
   }
 }
 

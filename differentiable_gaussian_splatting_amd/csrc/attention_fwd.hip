@@ -31,7 +31,7 @@ struct Running {
 
   // Adds kBlocks blocks of scores of the keys in tile rows r0 .., whose values are rows of s_v.
   template <int kBlocks>
-  __device__ __forceinline__ void add(f32x16* s, float c, const char* s_v, int r0, bool guard, const uint32_t* seen) {
+  __device__ __forceinline__ void add(f32x16* s, float c, const char* s_v, int r0) {
     float top = s[0][0];
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
@@ -57,7 +57,7 @@ struct Running {
         s[b][i] = exp2_fast(fmaf(s[b][i], c, lift));
         l += s[b][i];
       }
-      contract<T, DK>(o, s_v, r0 + 32 * b, s[b], guard, seen[b]);
+      contract<T, DK>(o, s_v, r0 + 32 * b, s[b]);
     }
   }
 };
@@ -67,7 +67,7 @@ constexpr int kKeyTile = sizeof(T) == 2 && DK <= 64 ? 64 : 32;  // keys of a til
 
 // kFew: at most 32 rows, the waves share them and split each tile's keys.
 template <typename T, int DK, bool kMask, bool kFew>
-__global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64) ? 2 : 1) void k_attn_fwd(AttnArgs a) {
+__global__ __launch_bounds__(kAttnThreads, DK <= 64 || (sizeof(T) == 2 && !kMask) ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   using L = Tile<T, DK>;
   constexpr int KT = kFew ? 128 : kKeyTile<T, DK>, kBlocks = kFew ? 1 : KT / 32;
   constexpr int kTile = KT * L::kRowBytes, kBuffers = !kFew ? 3 : (kTile <= (32 << 10) ? 2 : 1);
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
   constexpr int kBytes = 2 * kBuffers * kTile > kJoin ? 2 * kBuffers * kTile : kJoin;
   __shared__ __attribute__((aligned(16))) char s_tile[kBytes];
   __shared__ float2 s_ml[kFew ? kAttnWaves * 32 : 1];
-  __shared__ int s_odd[3];
+  __shared__ BadBits<T, DK, kMask ? KT : 1> s_bad;
   AttnWork w;
   if (!w.set(a)) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, h = lane >> 5, dim = int(a.dim), dim_in = int(a.dim_in);
@@ -130,14 +130,20 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
         for (int i = 0; i < 16; ++i) s[b][i] = (seen[b] >> i) & 1 ? s[b][i] : -INFINITY;
       }
     }
-    run.template add<kBlocks>(s, c, s_v, r0, kMask && odd, seen);
+    run.template add<kBlocks>(s, c, s_v, r0);
+    if constexpr (kMask) {
+      if (odd) {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) spoil_outputs<T, DK, KT>(run.o, seen[b], r0 + 32 * b, t - t0, s_bad);
+      }
+    }
   };
-  clear_tiles<T, DK>(s_tile, 2 * kBuffers * kTile, dim_in);
-  if (tid < 3) s_odd[tid] = 0;
   if (kMask && t0 < t1) {
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) mask_words(mask, t0 * KT + r0 + 32 * b, len, words[b]);
   }
+  clear_tiles<T, DK>(s_tile, 2 * kBuffers * kTile, dim_in);
+  if constexpr (kMask) s_bad.clear();
   __syncthreads();
   constexpr int kAhead = kBuffers - 1;  // tiles in flight while one is multiplied
   if (t0 < t1) start(t0, s_tile);
@@ -158,7 +164,7 @@ __global__ __launch_bounds__(kAttnThreads, sizeof(T) == 2 && !(kMask && DK > 64)
     }
     if (kAhead > 0 && t + kAhead < t1) start(t + kAhead, s_tile + (buf == 0 ? kAhead : buf - 1) * 2 * kTile);
     bool odd = false;
-    if constexpr (kMask) odd = tile_nonfinite<T, DK, KT>(s_v, t - t0, s_odd, [](int) { return true; });
+    if constexpr (kMask) odd = tile_make_finite<T, DK, KT>(s_v, t - t0, s_bad, [](int) { return true; });
     if (row0 < a.rows) {
       if ((t + 1) * KT <= len)
         multiply(t, s_k, s_v, odd, std::false_type());
@@ -410,7 +416,7 @@ extern "C" gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, co
   const uint32_t key_tile = few ? 128 : (d->dtype != GSR_F32 && d->head_dim <= 64 ? 64 : 32);
   const dim3 grid = attention_grid(&a, few ? 1 : (a.rows + kAttnRows - 1) / kAttnRows,
                                    (uint64_t(a.keys) + key_tile - 1) / key_tile, few ? 256 : 512,
-                                   few ? 1 : (d->dtype == GSR_F32 ? 2 : 16));
+                                   few ? 6 : (d->dtype == GSR_F32 ? 2 : 16));
   const auto inputs = {AttnInput{&a.q, a.qs, a.queries, a.heads}, AttnInput{&a.k, a.ks, a.keys, a.kv_heads},
                        AttnInput{&a.v, a.vs, a.keys, a.kv_heads}};
   const size_t packed = attention_pack_bytes(a, d->dtype, inputs);
