@@ -352,15 +352,25 @@ __device__ __forceinline__ void spoil_outputs(f32x16* o, uint32_t seen, int r0, 
   }
 }
 
-// acc[dt] += (transposed tile rows) * (block p), over the block's 32 rows, which are tile rows r0 ..
-template <typename T, int DK>
+// acc[dt] += (transposed tile rows) * (block p), over the block's 32 rows, which are tile rows r0 .. With kTwice, p keeps
+// about twice the bits of a 16-bit type: what rounding left of it is multiplied too.
+template <typename T, int DK, bool kTwice = false>
 __device__ __forceinline__ void contract(f32x16* acc, const char* tile, int r0, const f32x16& p) {
   using L = Tile<T, DK>;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const Vec<T, 8> b = to_frag<T>(p, s);
+    Vec<T, 8> rest;
+    if constexpr (kTwice) {
 #pragma unroll
-    for (int dt = 0; dt < L::kOut; ++dt) acc[dt] = mma(L::frag_t(tile, r0 + 16 * s, dt), b, acc[dt]);
+      for (int j = 0; j < 8; ++j) rest[j] = T(p[8 * s + j] - float(b[j]));
+    }
+#pragma unroll
+    for (int dt = 0; dt < L::kOut; ++dt) {
+      const Vec<T, 8> f = L::frag_t(tile, r0 + 16 * s, dt);
+      acc[dt] = mma(f, b, acc[dt]);
+      if constexpr (kTwice) acc[dt] = mma(f, rest, acc[dt]);
+    }
   }
 }
 

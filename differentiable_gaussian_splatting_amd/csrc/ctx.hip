@@ -260,7 +260,8 @@ gsr_status gsr_set_option(gsr_ctx* ctx, int32_t option, int64_t value) {
 gsr_status gsr_kernel_times(gsr_ctx* ctx, int32_t stage, float* ms, uint32_t max, uint32_t* count) {
   if (!ctx || !count || (max && !ms)) return GSR_EINVAL;
   *count = 0;
-  if (stage < 0 || stage >= GSR_NUM_STAGES) return fail(ctx, GSR_EINVAL, "gsr_kernel_times: no stage %d", stage);
+  if (stage < 0 || stage >= GSR_NUM_STAGES || stage == GSR_STAGE_TILE_SCAN + 1)
+    return fail(ctx, GSR_EINVAL, "gsr_kernel_times: no stage %d", stage);
   if (!ctx->timing_cap) return fail(ctx, GSR_EINVAL, "gsr_kernel_times: kernel timing is off");
   gsr_status st = enter(ctx);
   if (st) return st;

@@ -30,8 +30,9 @@ GSR_BIN_TILE_DEPTH = 2
 GSR_OPT_FORWARD_EXP, GSR_EXP_EXACT, GSR_EXP_FAST = 11, 0, 1
 (GSR_STAGE_BIN, GSR_STAGE_FORWARD, GSR_STAGE_BACKWARD, GSR_STAGE_ADAM, GSR_STAGE_PROJECT_FORWARD,
  GSR_STAGE_PROJECT_BACKWARD, GSR_STAGE_LOSS, GSR_STAGE_DEPTH_SORT, GSR_STAGE_TILE_SORT, GSR_STAGE_TILE_DEPTH,
- GSR_STAGE_TILE_SCAN, GSR_STAGE_GROUP_NORM_FORWARD, GSR_STAGE_GROUP_NORM_BACKWARD, GSR_STAGE_ROTARY,
- GSR_STAGE_ATTENTION_FORWARD, GSR_STAGE_ATTENTION_BACKWARD) = range(16)
+ GSR_STAGE_TILE_SCAN) = range(11)
+(GSR_STAGE_GROUP_NORM_FORWARD, GSR_STAGE_GROUP_NORM_BACKWARD, GSR_STAGE_ROTARY, GSR_STAGE_ATTENTION_FORWARD,
+ GSR_STAGE_ATTENTION_BACKWARD) = range(12, 17)
 GSR_ADAM_MAX_GROUPS = 8
 GSR_F32, GSR_F16, GSR_BF16 = 0, 1, 2
 GSR_ACT_NONE, GSR_ACT_SILU, GSR_ACT_RELU = 0, 1, 2

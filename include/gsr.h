@@ -151,12 +151,12 @@ gsr_status gsr_set_option(gsr_ctx* ctx, int32_t option, int64_t value);
                                      /*   tile-first scheme                                                      */
 #define GSR_STAGE_TILE_SCAN 10       /* inside gsr_bin: the column scan and list starts of the tile-first        */
                                      /*   scheme's counting sort (its scatter is GSR_STAGE_TILE_SORT)            */
-#define GSR_STAGE_GROUP_NORM_FORWARD 11  /* the kernels of gsr_group_norm_forward                                */
-#define GSR_STAGE_GROUP_NORM_BACKWARD 12 /* the kernels of gsr_group_norm_backward                               */
-#define GSR_STAGE_ROTARY 13              /* the rotary kernel, either direction                                  */
-#define GSR_STAGE_ATTENTION_FORWARD 14   /* the kernels of gsr_cross_attention_forward                           */
-#define GSR_STAGE_ATTENTION_BACKWARD 15  /* the kernels of gsr_cross_attention_backward                          */
-#define GSR_NUM_STAGES 16
+#define GSR_STAGE_GROUP_NORM_FORWARD 12  /* the kernels of gsr_group_norm_forward                                */
+#define GSR_STAGE_GROUP_NORM_BACKWARD 13 /* the kernels of gsr_group_norm_backward                               */
+#define GSR_STAGE_ROTARY 14              /* the rotary kernel, either direction                                  */
+#define GSR_STAGE_ATTENTION_FORWARD 15   /* the kernels of gsr_cross_attention_forward                           */
+#define GSR_STAGE_ATTENTION_BACKWARD 16  /* the kernels of gsr_cross_attention_backward                          */
+#define GSR_NUM_STAGES 17 /* 11 is no stage: it stays an error of gsr_kernel_times                               */
 
 /* GPU durations in milliseconds of the recorded launches of `stage`, oldest first: the last min(recorded, ring
  * size, max) of them. Waits for the newest one to finish. *count = the number written.

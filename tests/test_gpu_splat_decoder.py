@@ -67,3 +67,24 @@ def test_training_lowers_the_loss():
     banner("splat decoder training")
     losses = example().train(40)
     assert all(x == x for x in losses) and losses[-1] < 0.6 * losses[0], losses
+
+
+def test_kernel_times_of_the_operators():
+    from differentiable_gaussian_splatting_amd import gsr
+    ex = example()
+    banner("kernel times of the feature operators")
+    ctx = gsr.Context(0)
+    try:
+        gsr.gsr_set_option(ctx, gsr.GSR_OPT_KERNEL_TIMING, 8)
+        w, cells = ex.weights(3), ex.SIZE // ex.PATCH
+        pos_q, pos_k = ex.grid(ex.SIDE, cells), ex.grid(cells, cells)
+        patches = ex.patches_of(torch.rand((ex.SIZE, ex.SIZE, 3)).cuda())
+        out, saved = ex.decoder_forward(ctx, w, patches, pos_q, pos_k)
+        ex.decoder_backward(ctx, w, saved, pos_q, pos_k, out)
+        counts = {gsr.GSR_STAGE_GROUP_NORM_FORWARD: 1, gsr.GSR_STAGE_GROUP_NORM_BACKWARD: 1, gsr.GSR_STAGE_ROTARY: 4,
+                  gsr.GSR_STAGE_ATTENTION_FORWARD: 1, gsr.GSR_STAGE_ATTENTION_BACKWARD: 1}
+        for stage, n in counts.items():
+            t = gsr.gsr_kernel_times(ctx, stage)
+            assert len(t) == n and all(0 < x < 1000 for x in t), (stage, t)
+    finally:
+        ctx.close()
