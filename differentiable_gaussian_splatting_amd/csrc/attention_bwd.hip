@@ -14,17 +14,27 @@
 namespace gsr {
 namespace {
 
+// Wide 16-bit heads: a wave's two operands (its rows' q and do, or its keys' k and v), the sums and two blocks of
+// scores pass 256 registers, and a wave alone on its SIMD waits out every LDS read. There one of the two operands is kept
+// in LDS, the stream goes by 32 rows through two buffers, and two waves share a SIMD. Both kernels of a bfloat16 training
+// step of 2,500 x 2,500, 8 heads, with its forward pass: 96 wide 448 -> 342 us (of it 364 by the keys' kernel alone),
+// 128 wide 516 -> 484 us by the keys' kernel. The queries' kernel keeps ds to twice the bits and at 128 wide still spills
+// (484 -> 824 us), so it stays at one wave there.
+template <typename T, int DK, bool kMask>
+constexpr bool kOneInLds = sizeof(T) == 2 && DK == 96 && !kMask;
+template <typename T, int DK, bool kMask>
+constexpr bool kOneInLdsKeys = sizeof(T) == 2 && DK > 64 && !kMask;
 // Waves that share a SIMD, so that one multiplies while another computes exponentials: two where 256 registers hold a
 // wave's operands and sums.
 template <typename T, int DK, bool kMask>
-constexpr int kWavesPerSimd = DK <= 64 || (sizeof(T) == 2 && DK <= 96 && !kMask) ? 2 : 1;
-// 32-row blocks of a streamed tile: two give the matrix cores one block's products while the other's exponentials are
-// taken (D = 128, where one wave has a SIMD to itself).
-template <typename T, bool kMask>
-constexpr int kStreamBlocks = sizeof(T) == 2 && !kMask ? 2 : 1;
+constexpr int kWavesPerSimd = DK <= 64 || kOneInLds<T, DK, kMask> ? 2 : 1;
 template <typename T, int DK, bool kMask>
 constexpr int kWavesPerSimdKeys =
-    sizeof(T) == 2 ? (DK <= 64 || (DK <= 96 && !kMask) ? 2 : 1) : (DK <= 32 || (DK <= 48 && !kMask) ? 2 : 1);
+    sizeof(T) == 2 ? (DK <= 64 || kOneInLdsKeys<T, DK, kMask> ? 2 : 1) : (DK <= 32 || (DK <= 48 && !kMask) ? 2 : 1);
+// 32-row blocks of a streamed tile: two halve the barriers and give the matrix cores one block's products while the
+// other's exponentials are taken.
+template <typename T, bool kMask, bool kOne>
+constexpr int kStreamBlocks = sizeof(T) == 2 && !kMask && !kOne ? 2 : 1;
 
 // float16 values of ds, whose size follows the loss's scale, are kept in range by a power of two per column of the
 // accumulator (a query's dq, a key's dk): set from the first block that has a value, lowered when a later block would
@@ -60,8 +70,11 @@ struct Ranged {
 template <typename T, int DK, bool kMask>
 __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, DK>;
-  constexpr int kBlocks = kStreamBlocks<T, kMask>, KT = 32 * kBlocks, kTile = KT * L::kRowBytes;
-  __shared__ __attribute__((aligned(16))) char s_tile[6 * kTile];
+  constexpr bool kOwn = kOneInLds<T, DK, kMask>;
+  constexpr int kBlocks = kStreamBlocks<T, kMask, kOwn>, KT = 32 * kBlocks, kTile = KT * L::kRowBytes;
+  constexpr int kRing = kOwn ? 2 : 3;  // tiles in LDS: the one multiplied and those on their way
+  __shared__ __attribute__((aligned(16))) char s_tile[2 * kRing * kTile];
+  __shared__ __attribute__((aligned(16))) char s_own[kOwn ? kAttnRows * L::kRowBytes : 16];
   __shared__ BadBits<T, DK, kMask ? KT : 1> s_bad;
   AttnWork w;
   if (!w.set(a)) return;
@@ -87,10 +100,19 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
   };
 
   if constexpr (kMask) s_bad.clear();
-  clear_tiles<T, DK>(s_tile, 6 * kTile, dim_in);
+  clear_tiles<T, DK>(s_tile, 2 * kRing * kTile, dim_in);
+  if constexpr (kOwn) clear_tiles<T, DK>(s_own, kAttnRows * L::kRowBytes, dim_in);
   __syncthreads();
   if (t0 < t1) start(t0, s_tile);
-  if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
+  if (kRing == 3 && t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
+  if (kOwn && t0 < t1) {
+    const T* db = static_cast<const T*>(a.dout) + int64_t(w.batch) * a.dos[0];
+    Copier<T, DK, kAttnRows>::start(s_own, a.rows - w.tile * kAttnRows, dim_in, [&](int r) {
+      uint32_t t, hd;
+      row_of(a, w.kv_head, w.tile * kAttnRows + r, &t, &hd);
+      return db + int64_t(t) * a.dos[1] + int64_t(hd) * a.dos[2];
+    });
+  }
   Vec<T, 8> qf[DK / 16], df[DK / 16];
 #pragma unroll
   for (int kk = 0; kk < DK / 16; ++kk) qf[kk] = df[kk] = zero_frag<T>();
@@ -136,7 +158,8 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
 #pragma unroll
       for (int kk = 0; kk < DK / 16; ++kk) s[b] = mma(L::frag(s_k, 32 * b, kk), qf[kk], s[b]);
 #pragma unroll
-      for (int kk = 0; kk < DK / 16; ++kk) dp[b] = mma(L::frag(s_v, 32 * b, kk), df[kk], dp[b]);
+      for (int kk = 0; kk < DK / 16; ++kk)
+        dp[b] = mma(L::frag(s_v, 32 * b, kk), kOwn ? L::frag(s_own, (tid >> 6) * 32, kk) : df[kk], dp[b]);
     }
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
@@ -164,10 +187,10 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) mask_words(mask, t0 * KT + 32 * b, len, words[b]);
   }
-  int at = 0;
+  int buf = 0;
   for (uint32_t t = t0; t < t1; ++t) {
-    char *s_k = s_tile + at, *s_v = s_k + kTile;
-    if (t + 1 < t1 && (t + 2) * KT <= len)
+    char *s_k = s_tile + buf * 2 * kTile, *s_v = s_k + kTile;
+    if (kRing == 3 && t + 1 < t1 && (t + 2) * KT <= len)
       tile_barrier<2 * Copy::kSteps>();
     else
       tile_barrier<0>();
@@ -178,7 +201,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
         mask_words(t + 1 < t1 ? mask : nullptr, (t + 1) * KT + 32 * b, len, words[b]);
       }
     }
-    if (t + 2 < t1) start(t + 2, s_tile + (at >= 2 * kTile ? at - 2 * kTile : at + 4 * kTile));
+    if (t + kRing - 1 < t1) start(t + kRing - 1, s_tile + (buf == 0 ? kRing - 1 : buf - 1) * 2 * kTile);
     bool odd = false;
     if constexpr (kMask)
       odd = tile_make_finite<T, DK, KT>(s_k, t - t0, s_bad, [](int) { return true; });
@@ -188,7 +211,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
       else
         multiply(t, s_k, s_v, odd, std::true_type());
     }
-    at = at == 4 * kTile ? 0 : at + 2 * kTile;
+    buf = buf == kRing - 1 ? 0 : buf + 1;
   }
   if (!valid) return;
   if (a.splits > 1) {
@@ -204,8 +227,11 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
 template <typename T, int DK, bool kMask>
 __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, DK>;
-  constexpr int kBlocks = kStreamBlocks<T, kMask>, QT = 32 * kBlocks, kTile = QT * L::kRowBytes;
-  __shared__ __attribute__((aligned(16))) char s_tile[6 * kTile];
+  constexpr bool kOwn = kOneInLdsKeys<T, DK, kMask>;
+  constexpr int kBlocks = kStreamBlocks<T, kMask, kOwn>, QT = 32 * kBlocks, kTile = QT * L::kRowBytes;
+  constexpr int kRing = kOwn ? 2 : 3;  // tiles in LDS: the one multiplied and those on their way
+  __shared__ __attribute__((aligned(16))) char s_tile[2 * kRing * kTile];
+  __shared__ __attribute__((aligned(16))) char s_own[kOwn ? kAttnRows * L::kRowBytes : 16];
   __shared__ __attribute__((aligned(16))) float s_lse[3][QT];
   __shared__ __attribute__((aligned(16))) float s_delta[3][QT];
   __shared__ int64_t s_mask[3][kMask ? QT : 1];
@@ -283,18 +309,25 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
       }
     }
   };
-  clear_tiles<T, DK>(s_tile, 6 * kTile, dim_in);
+  clear_tiles<T, DK>(s_tile, 2 * kRing * kTile, dim_in);
+  if constexpr (kOwn) clear_tiles<T, DK>(s_own, kAttnRows * L::kRowBytes, dim_in);
   if constexpr (kMask) s_bad.clear();
   __syncthreads();
   if (t0 < t1) {
     start(t0, s_tile);
-    put_stats(0);
+    if (kRing == 3) put_stats(0);
     if constexpr (kMask) {
       lds_barrier();
       fetch_mask(t0, 0);
     }
   }
-  if (t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
+  if (kRing == 3 && t0 + 1 < t1) start(t0 + 1, s_tile + 2 * kTile);
+  if (kOwn && t0 < t1) {
+    const T* vb = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(w.kv_head) * a.vs[2];
+    const uint32_t first = w.tile * kAttnRows;
+    Copier<T, DK, kAttnRows>::start(s_own, len - first, dim_in,
+                                    [&](int r) { return vb + int64_t(first + r) * a.vs[1]; });
+  }
   Vec<T, 8> kf[DK / 16], vf[DK / 16];
 #pragma unroll
   for (int kk = 0; kk < DK / 16; ++kk) kf[kk] = vf[kk] = zero_frag<T>();
@@ -306,15 +339,16 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
 #pragma unroll
     for (int kk = 0; kk < DK / 16; ++kk) {
       kf[kk] = load_frag(kr, kk, dim_in);
-      vf[kk] = load_frag(vr, kk, dim_in);
+      if constexpr (!kOwn) vf[kk] = load_frag(vr, kk, dim_in);
     }
   }
   int buf = 0;
   for (uint32_t t = t0; t < t1; ++t) {
     char *s_q = s_tile + buf * 2 * kTile, *s_d = s_q + kTile;
-    const int next = buf == 2 ? 0 : buf + 1;
-    if (t + 1 < t1) put_stats(next);
-    if (t + 1 < t1 && (t + 2) * QT <= a.rows)
+    const int next = buf == kRing - 1 ? 0 : buf + 1;
+    if (kRing == 2) put_stats(buf);
+    if (kRing == 3 && t + 1 < t1) put_stats(next);
+    if (kRing == 3 && t + 1 < t1 && (t + 2) * QT <= a.rows)
       tile_barrier<2 * Copy::kSteps>();
     else
       tile_barrier<0>();
@@ -328,7 +362,8 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
     if constexpr (kMask)  // a row that saw no key is taken as zeros, whatever it holds
       odd = tile_make_finite<T, DK, 2 * QT>(s_q, t - t0, s_bad,
                                             [&](int r) { return s_lse[buf][r % QT] != -INFINITY; });
-    if (t + 2 < t1) start(t + 2, s_tile + (next == 2 ? 0 : next + 1) * 2 * kTile);
+    if (kRing == 2 && t + 1 < t1) start(t + 1, s_tile + next * 2 * kTile);
+    if (kRing == 3 && t + 2 < t1) start(t + 2, s_tile + (next == 2 ? 0 : next + 1) * 2 * kTile);
     if (key0 < len) {
       f32x16 s[kBlocks], dp[kBlocks];
 #pragma unroll
@@ -337,7 +372,8 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
 #pragma unroll
         for (int kk = 0; kk < DK / 16; ++kk) s[b] = mma(L::frag(s_q, 32 * b, kk), kf[kk], s[b]);
 #pragma unroll
-        for (int kk = 0; kk < DK / 16; ++kk) dp[b] = mma(L::frag(s_d, 32 * b, kk), vf[kk], dp[b]);
+        for (int kk = 0; kk < DK / 16; ++kk)
+          dp[b] = mma(L::frag(s_d, 32 * b, kk), kOwn ? L::frag(s_own, (tid >> 6) * 32, kk) : vf[kk], dp[b]);
       }
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
@@ -478,13 +514,17 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
   a.dv = dv;
   // one scratch buffer: copies of inputs, do.o of every row, then the parts of whichever kernel splits (in turn)
   AttnArgs b = a;
-  const uint32_t streamed = d->dtype != GSR_F32 && !mask ? 64 : 32;  // keys or rows of a streamed tile
-  const uint32_t slots_q = a.dim <= 64 ? 512 : 256, cost = 1;
-  const uint32_t slots_k = a.dim <= (d->dtype != GSR_F32 ? 64 : mask ? 32 : 48) ? 512 : 256;
+  // as the kernels' kStreamBlocks and kWavesPerSimd have it: rows of a streamed tile, workgroups at once on the card
+  const bool half = d->dtype != GSR_F32, open = half && !mask;
+  const bool one_q = open && a.dim > 64 && a.dim <= 96, one_k = open && a.dim > 64;
+  const uint32_t streamed_q = open && !one_q ? 64 : 32, streamed_k = open && !one_k ? 64 : 32;
+  const uint32_t cost = half ? 2 : 1;  // 16 bits step faster: 96 wide, 2,500 x 2,500, 378 -> 342 us against 1
+  const uint32_t slots_q = a.dim <= 64 || one_q ? 512 : 256;
+  const uint32_t slots_k = (half ? a.dim <= 64 || one_k : a.dim <= (mask ? 32u : 48u)) ? 512 : 256;
   const dim3 grid_q = attention_grid(&a, (a.rows + kAttnRows - 1) / kAttnRows,
-                                     (uint64_t(a.keys) + streamed - 1) / streamed, slots_q, cost);
+                                     (uint64_t(a.keys) + streamed_q - 1) / streamed_q, slots_q, cost);
   const dim3 grid_k = attention_grid(&b, (b.keys + kAttnRows - 1) / kAttnRows,
-                                     (uint64_t(b.rows) + streamed - 1) / streamed, slots_k, 2 * cost);
+                                     (uint64_t(b.rows) + streamed_k - 1) / streamed_k, slots_k, 2 * cost);
   const size_t groups = size_t(a.batch) * a.kv_heads, deltas = (groups * a.rows + 3) / 4 * 4;
   size_t parts = 0;
   if (a.splits > 1) parts = groups * a.splits * a.rows * a.dim;
