@@ -19,7 +19,7 @@ namespace {
 // in LDS, the stream goes by 32 rows through two buffers, and two waves share a SIMD. Both kernels of a bfloat16 training
 // step of 2,500 x 2,500, 8 heads, with its forward pass: 96 wide 448 -> 342 us (of it 364 by the keys' kernel alone),
 // 128 wide 516 -> 484 us by the keys' kernel. The queries' kernel keeps ds to twice the bits and at 128 wide still spills
-// (484 -> 824 us), so it stays at one wave there.
+// (484 -> 824 us), so it stays at one wave there. (Measured while dk rounded its ds once: 358 and 511 us since.)
 template <typename T, int DK, bool kMask>
 constexpr bool kOneInLds = sizeof(T) == 2 && DK == 96 && !kMask;
 template <typename T, int DK, bool kMask>
@@ -178,8 +178,9 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
       for (int i = 0; i < 16; ++i)
         s[b][i] = exp2_fast(fmaf(s[b][i], c, -lse2)) * fmaf(dp[b][i], a.scale, -delta_s);
       range.fit(s[b], acc);
-      // kept to twice the bits: rounded once, ds and the o in do.o together leave dq over 1.5 times the error of its own
-      // rounding; this costs 4 % of a training step (for dk, whose error stays at 1.4 times, it would cost as much)
+      // ds is kept to twice the bits: rounded once, it and the o in do.o together leave dq and dk over 1.5 times the
+      // error of their own rounding (now 1.0 to 1.2); that costs 4 % of a training step for dq and 5 % for dk
+      // (2,500 x 2,500, 8 heads, 128 wide, bfloat16: 484 -> 511 us). p is rounded once: dv stays below 1.48 times.
       contract<T, DK, (sizeof(T) == 2)>(acc, s_k, 32 * b, s[b]);
     }
   };
@@ -404,7 +405,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
         }
         contract<T, DK>(dv, s_d, 32 * b, s[b]);
         range.fit(dp[b], dk);
-        contract<T, DK>(dk, s_q, 32 * b, dp[b]);
+        contract<T, DK, (sizeof(T) == 2)>(dk, s_q, 32 * b, dp[b]);
       }
     }
     buf = next;
