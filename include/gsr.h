@@ -412,7 +412,7 @@ typedef struct gsr_group_norm {
  * features whose mean is far from 0 lose nothing. Uses the context arena as scratch.
  * Errors: GSR_EINVAL (null pointers, channels not a multiple of groups, unknown dtype or activation, eps < 0 or NaN,
  * output strides that overlap, pointers not aligned to their element), GSR_EOVERFLOW (pixels * channels / groups >=
- * 2^31 or images >= 2^16), GSR_ENOMEM, GSR_EHIP. */
+ * 2^31, images >= 2^16 or channels >= 2^20), GSR_ENOMEM, GSR_EHIP. */
 gsr_status gsr_group_norm_forward(gsr_ctx* ctx, void* stream, const gsr_group_norm* desc, const void* x,
                                   const float* gamma, const float* beta, void* y, float* stats);
 
@@ -451,7 +451,7 @@ typedef struct gsr_rotary {
  *   out        written; may be x itself (same strides)
  * The angle is reduced to a turn with an exact remainder, so a position costs no accuracy up to 2^24.
  * Errors: GSR_EINVAL (null pointers, axes or pairs out of range, base not > 0, overlapping output strides, pointers
- * not aligned to their element), GSR_EOVERFLOW (batch * tokens >= 2^31), GSR_EHIP. */
+ * not aligned to their element), GSR_EOVERFLOW (batch * tokens >= 2^31, heads or head_dim >= 2^16), GSR_EHIP. */
 gsr_status gsr_rotary_forward(gsr_ctx* ctx, void* stream, const gsr_rotary* desc, const void* x,
                               const float* positions, void* out);
 
@@ -485,17 +485,19 @@ typedef struct gsr_attention {
  *   o           written;  lse  device [batch][heads][queries] float32, written (for the backward), or NULL
  * 16-bit features are multiplied on the matrix cores with float32 sums; the probabilities are rounded to the
  * features' type before their product with v. float32 features are multiplied as float32.
- * Uses the context arena as scratch when few queries meet many keys (the keys are then split and joined).
+ * Uses the context arena as scratch when few queries meet many keys (the keys are then split and joined), and for
+ * copies of inputs whose rows do not start and end at multiples of 16 bytes.
  * Errors: GSR_EINVAL (null pointers, head counts, head_dim or scale out of range, overlapping output strides,
  * pointers not aligned to their element), GSR_EOVERFLOW (batch * heads * queries or batch * keys * kv_heads >=
- * 2^31), GSR_ENOMEM, GSR_EHIP. */
+ * 2^31, heads >= 2^16 or batch >= 2^24), GSR_ENOMEM, GSR_EHIP. */
 gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, const gsr_attention* desc, const void* q,
                                        const void* k, const void* v, const int32_t* kv_lengths, const uint8_t* mask,
                                        void* o, float* lse);
 
 /* Backward pass: dv_j = sum p_j do;  ds_j = scale p_j (do.v_j - do.o);  dq = sum_j ds_j k_j;  dk_j = sum ds_j q, the
  * sums for a key over the queries of every head that shares it. Gradients of an input broadcast over a stride of 0
- * are those of each copy.
+ * are those of each copy. As in the formulas, a visible key whose query or gradient holds a NaN or an infinity gets
+ * NaN gradients; a query that sees no key gives nothing to any, whatever it holds.
  *   o, lse  as written by the forward for the same inputs;  do (`dout`) as o
  *   dq, dk, dv  written (zero where nothing is visible)
  * Uses the context arena as scratch. Errors: as gsr_cross_attention_forward. */

@@ -89,6 +89,21 @@ def test_lengths(ctx, dtype, lengths):
             assert (got[0][b] == 0).all() and (got[2][b] == 0).all() and (got[1][b] == -math.inf).all()
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [72, 96, 104, 128])
+def test_wide_heads_of_several_tiles_with_lengths(ctx, dtype, dim):
+    """Heads past 64 elements, whose backward keeps an operand in LDS: several tiles of queries and keys, lengths that end
+    inside a tile, NaN and infinities beyond them."""
+    banner(f"attention wide heads {dtype} {dim}")
+    q, k, v, do = inputs(dim, 3, 300, 290, 4, 2, dim, DTYPES[dtype])
+    lengths = [290, 0, 141]
+    for b, n in enumerate(lengths):
+        k[b, n:], v[b, n:] = math.nan, math.inf
+    got = check(ctx, q, k, v, do, lengths=lengths)
+    for b, n in enumerate(lengths):
+        assert (got[3][b, n:] == 0).all() and (got[4][b, n:] == 0).all()
+
+
 def some_mask(seed, *shape, share=0.5):
     return torch.rand(shape, generator=torch.Generator().manual_seed(seed)) < share
 
