@@ -284,8 +284,8 @@ struct BadBits {
 };
 
 // Makes the non-finite elements of a tile zeros and notes them (a masked value is 0 as a probability, but 0 * NaN is
-// NaN); the caller puts NaN where a visible one belongs. keep(row) false makes that row zeros. Returns whether there
-// were any, to every thread; turn counts the tiles.
+// NaN); the caller adds what they contribute where they are seen (add_outputs) or puts NaN there (spoil_rows). keep(row) false makes that
+// row zeros. Returns whether there were any, to every thread; turn counts the tiles.
 template <typename T, int DK, int kRows, typename F>
 __device__ __forceinline__ bool tile_make_finite(char* tile, uint32_t turn, BadBits<T, DK, kRows>& bad, F keep) {
   using L = Tile<T, DK>;
@@ -332,22 +332,32 @@ __device__ __forceinline__ void spoil_rows(f32x16& s, uint32_t seen, int r0, uin
   }
 }
 
-// Makes the outputs of a column NaN at the bad elements of the rows r0 .. r0 + 31 that it sees.
-template <typename T, int DK, int kRows>
-__device__ __forceinline__ void spoil_outputs(f32x16* o, uint32_t seen, int r0, uint32_t turn,
-                                              const BadBits<T, DK, kRows>& bad) {
+// Adds to a column's outputs the bad elements of the tile rows r0 .. r0 + 31 that it sees, each times its value of the
+// block p (whose tile rows they are): an infinity times a weight above 0 is that infinity, 0 times it is NaN.
+template <typename T, int DK, int kRows, typename F>
+__device__ __forceinline__ void add_outputs(f32x16* o, const f32x16& p, uint32_t seen, int r0, uint32_t turn,
+                                            const BadBits<T, DK, kRows>& bad, F value) {
   const int h = int(threadIdx.x & 63) >> 5;
   const uint32_t other = __float_as_uint(other_half(__uint_as_float(seen)));
 #pragma unroll 1
   for (int r = 0; r < 32; ++r) {
-    const bool vis = (((r >> 2) & 1) == h ? seen : other) >> ((r >> 3) * 4 + (r & 3)) & 1;
-    if (!vis) continue;
+    const int i = (r >> 3) * 4 + (r & 3);
+    const bool mine = ((r >> 2) & 1) == h;  // whose half holds row r
+    float f = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f = j == i ? p[j] : f;
+    const float theirs = other_half(f);
+    f = mine ? f : theirs;
+    if (!(((mine ? seen : other) >> i) & 1)) continue;
 #pragma unroll
     for (int dt = 0; dt < Tile<T, DK>::kOut; ++dt) {
       const uint32_t w = bad.bits[turn % 3][r0 + r][dt];
+      if (!w) continue;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if ((w >> (8 * (i / 4) + 4 * h + i % 4)) & 1) o[dt][i] = __builtin_nanf("");
+      for (int j = 0; j < 16; ++j) {
+        const int d = 8 * (j / 4) + 4 * h + j % 4;
+        if ((w >> d) & 1) o[dt][j] = fmaf(f, float(value(r0 + r, 32 * dt + d)), o[dt][j]);
+      }
     }
   }
 }

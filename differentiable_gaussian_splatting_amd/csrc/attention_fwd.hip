@@ -142,7 +142,9 @@ __global__ __launch_bounds__(kAttnThreads, DK <= 64 || (sizeof(T) == 2 && !kMask
     if constexpr (kMask) {
       if (odd) {
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) spoil_outputs<T, DK, KT>(run.o, seen[b], r0 + 32 * b, t - t0, s_bad);
+        for (int b = 0; b < kBlocks; ++b)
+          add_outputs<T, DK, KT>(run.o, s[b], seen[b], r0 + 32 * b, t - t0, s_bad,
+                                 [&](int r, int d) { return vb[int64_t(t * KT + r) * a.vs[1] + d]; });
       }
     }
   };
