@@ -167,15 +167,20 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
     }
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
+      auto key_element = [&](int r, int d) { return kb[int64_t(t * KT + r) * a.ks[1] + d]; };
+      if constexpr (kMask) {
+        if (odd) {
+          const T* qr = static_cast<const T*>(a.q) + int64_t(w.batch) * a.qs[0] + int64_t(keep_here(query)) * a.qs[1] +
+                        int64_t(keep_here(head)) * a.qs[2];
+          add_products<T, DK, KT>(s[b], seen[b], 32 * b, t - t0, s_bad, key_element, [&](int d) { return qr[d]; });
+        }
+      }
       if constexpr (kMask || decltype(edge)::value) {
         if constexpr (!kMask) seen[b] = visible<false>(nullptr, t * KT + 32 * b, len);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           s[b][i] = (seen[b] >> i) & 1 ? s[b][i] : -INFINITY;
           dp[b][i] = (seen[b] >> i) & 1 ? dp[b][i] : 0.0f;
-        }
-        if constexpr (kMask) {
-          if (odd) spoil_rows<T, DK, KT>(s[b], seen[b], 32 * b, t - t0, s_bad);
         }
       }
 #pragma unroll
@@ -186,6 +191,9 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
       // error of their own rounding (now 1.0 to 1.2); that costs 4 % of a training step for dq and 5 % for dk
       // (2,500 x 2,500, 8 heads, 128 wide, bfloat16: 484 -> 511 us). p is rounded once: dv stays below 1.48 times.
       contract<T, DK, (sizeof(T) == 2)>(acc, s_k, 32 * b, s[b]);
+      if constexpr (kMask) {
+        if (odd) add_outputs<T, DK, KT>(acc, s[b], seen[b], 32 * b, t - t0, s_bad, key_element);
+      }
     }
   };
   if (kMask && t0 < t1) {
@@ -385,6 +393,25 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
       }
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
+        // elements of the tile's q and do in memory, for the bad ones
+        auto element = [&](const void* x, const int64_t* st, int r, int d) {
+          uint32_t query, head;
+          row_of(a, w.kv_head, t * QT + r, &query, &head);
+          return static_cast<const T*>(x)[int64_t(w.batch) * st[0] + int64_t(query) * st[1] + int64_t(head) * st[2] + d];
+        };
+        auto q_element = [&](int r, int d) { return element(a.q, a.qs, r, d); };
+        auto do_element = [&](int r, int d) { return element(a.dout, a.dos, r - QT, d); };
+        if constexpr (kMask) {
+          if (odd) {
+            const T* kr = static_cast<const T*>(a.k) + int64_t(w.batch) * a.ks[0] + int64_t(keep_here(key)) * a.ks[1] +
+                          int64_t(w.kv_head) * a.ks[2];
+            const T* vr = static_cast<const T*>(a.v) + int64_t(w.batch) * a.vs[0] + int64_t(keep_here(key)) * a.vs[1] +
+                          int64_t(w.kv_head) * a.vs[2];
+            add_products<T, DK, 2 * QT>(s[b], seen[b], 32 * b, t - t0, s_bad, q_element, [&](int d) { return kr[d]; });
+            add_products<T, DK, 2 * QT>(dp[b], seen[b], QT + 32 * b, t - t0, s_bad, do_element,
+                                        [&](int d) { return vr[d]; });
+          }
+        }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int r = 32 * b + 8 * g + 4 * h;
@@ -402,17 +429,15 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
             }
           }
         }
-        if constexpr (kMask) {
-          if (odd) {  // a bad query or gradient that a key sees spoils its gradients
-            spoil_rows<T, DK, 2 * QT>(s[b], seen[b], 32 * b, t - t0, s_bad);
-            spoil_rows<T, DK, 2 * QT>(s[b], seen[b], QT + 32 * b, t - t0, s_bad);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dp[b][i] = s[b][i] == s[b][i] ? dp[b][i] : s[b][i];
-          }
-        }
         contract<T, DK>(dv, s_d, 32 * b, s[b]);
         range.fit(dp[b], dk);
         contract<T, DK, (sizeof(T) == 2)>(dk, s_q, 32 * b, dp[b]);
+        if constexpr (kMask) {
+          if (odd) {
+            add_outputs<T, DK, 2 * QT>(dv, s[b], seen[b], QT + 32 * b, t - t0, s_bad, do_element);
+            add_outputs<T, DK, 2 * QT>(dk, dp[b], seen[b], 32 * b, t - t0, s_bad, q_element);
+          }
+        }
       }
     }
     buf = next;

@@ -284,7 +284,7 @@ struct BadBits {
 };
 
 // Makes the non-finite elements of a tile zeros and notes them (a masked value is 0 as a probability, but 0 * NaN is
-// NaN); the caller adds what they contribute where they are seen (add_outputs) or puts NaN there (spoil_rows). keep(row) false makes that
+// NaN); the caller adds what they contribute where they are seen (add_products, add_outputs). keep(row) false makes that
 // row zeros. Returns whether there were any, to every thread; turn counts the tiles.
 template <typename T, int DK, int kRows, typename F>
 __device__ __forceinline__ bool tile_make_finite(char* tile, uint32_t turn, BadBits<T, DK, kRows>& bad, F keep) {
@@ -317,18 +317,33 @@ __device__ __forceinline__ bool tile_make_finite(char* tile, uint32_t turn, BadB
   return bad.any[now] != 0;
 }
 
-// Makes the values of a block NaN that are visible and belong to a bad row of the tile (rows r0 ..).
-template <typename T, int DK, int kRows>
-__device__ __forceinline__ void spoil_rows(f32x16& s, uint32_t seen, int r0, uint32_t turn,
-                                           const BadBits<T, DK, kRows>& bad) {
+// x, in a way that keeps what a rare path computes from it inside that path: hoisted out of the loop over the tiles,
+// addresses would hold registers that the loop needs.
+__device__ __forceinline__ uint32_t keep_here(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// Adds to the visible values of a block (tile rows r0 .. by this lane's column) the products of the rows' bad elements,
+// as they lie in memory, with the column's: value(row, element) value of the tile, column(element) of the lane.
+template <typename T, int DK, int kRows, typename F, typename G>
+__device__ __forceinline__ void add_products(f32x16& s, uint32_t seen, int r0, uint32_t turn,
+                                             const BadBits<T, DK, kRows>& bad, F value, G column) {
   const int h = int(threadIdx.x & 63) >> 5;
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < 16; ++i) {
-    const uint32_t* w = bad.bits[turn % 3][r0 + 8 * (i / 4) + 4 * h + i % 4];
-    uint32_t any = 0;
+    if (!((seen >> i) & 1)) continue;
+    const int row = r0 + 8 * (i / 4) + 4 * h + i % 4;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int k = 0; k < bad.kWords; ++k)
+      for (uint32_t w = bad.bits[turn % 3][row][k]; w; w &= w - 1) {
+        const int d = 32 * k + __ffs(int(w)) - 1;
+        sum = fmaf(float(value(row, d)), float(column(d)), sum);
+      }
 #pragma unroll
-    for (int k = 0; k < bad.kWords; ++k) any |= w[k];
-    if (any && ((seen >> i) & 1)) s[i] = __builtin_nanf("");
+    for (int j = 0; j < 16; ++j)
+      if (j == i) s[j] += sum;
   }
 }
 

@@ -496,8 +496,9 @@ gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, const gsr_att
 
 /* Backward pass: dv_j = sum p_j do;  ds_j = scale p_j (do.v_j - do.o);  dq = sum_j ds_j k_j;  dk_j = sum ds_j q, the
  * sums for a key over the queries of every head that shares it. Gradients of an input broadcast over a stride of 0
- * are those of each copy. As in the formulas, a visible key whose query or gradient holds a NaN or an infinity gets
- * NaN gradients; a query that sees no key gives nothing to any, whatever it holds.
+ * are those of each copy. A visible NaN or infinity reaches what the formulas say, with a mask or without: one in dout
+ * that element of dv, and all of dq and dk that its query has part in (whether those are then infinite or NaN depends
+ * on the order of their sums); a query that sees no key gives nothing to any, whatever it holds.
  *   o, lse  as written by the forward for the same inputs;  do (`dout`) as o
  *   dq, dk, dv  written (zero where nothing is visible)
  * Uses the context arena as scratch. Errors: as gsr_cross_attention_forward. */

@@ -111,7 +111,52 @@ def test_visible_bad_values(ctx, dtype, dim, tq, tk, h, hk):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("which", ["v"])
+@pytest.mark.parametrize("dim", [24, 40, 64, 80, 128])
+@pytest.mark.parametrize("tq,tk,h,hk", SHAPES, ids=str)
+def test_visible_bad_gradients(ctx, dtype, dim, tq, tk, h, hk):
+    """do holds infinities and NaN: dv is bad at that element alone (of the keys the query sees), their other gradients
+    throughout."""
+    banner(f"attention visible bad gradients {dtype} {dim} {tq} x {tk}")
+    q, k, v, do = inputs(dim, 2, tq, tk, h, hk, dim, DTYPES[dtype])
+    mask = some_mask(dim + 1, 2, h, tq, tk, share=0.3)
+    mask[:, :, 1] = False
+    do[0, 0, 0, 3], do[1, tq - 1, 1, 17], do[0, 2, 1, 5] = math.inf, math.nan, -math.inf
+    do[1, 1, 0, 2] = math.inf  # of a query that sees nothing
+    check(run(ctx, q, k, v, do, mask), formulas(q, k, v, do, mask), oracle_of(q, k, v, do, mask))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [24, 64, 80, 128])
+@pytest.mark.parametrize("tq,tk,h,hk", SHAPES, ids=str)
+def test_visible_bad_queries_and_keys(ctx, dtype, dim, tq, tk, h, hk):
+    """A NaN in q spoils its query and, of what its keys get, their gradients; a NaN in k every query that sees it."""
+    banner(f"attention visible bad queries and keys {dtype} {dim} {tq} x {tk}")
+    q, k, v, do = inputs(dim, 2, tq, tk, h, hk, dim, DTYPES[dtype])
+    mask = some_mask(dim + 1, 2, h, tq, tk, share=0.3)
+    mask[:, :, 1] = False
+    mask[1, :, :, 40] = False
+    mask[1, 0, 2, 40] = True
+    q[0, 0, 0, 3], q[0, 1, 0, 1] = math.nan, math.inf  # the second sees nothing
+    k[1, 40, 0, 5] = math.nan
+    check(run(ctx, q, k, v, do, mask), formulas(q, k, v, do, mask), oracle_of(q, k, v, do, mask))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [32, 96, 128])
+def test_a_key_at_minus_infinity_is_a_weight_of_zero(ctx, dtype, dim):
+    """k = inf where q < 0: the score is -inf, its weight 0; dq is NaN (0 inf) at that element alone."""
+    banner(f"attention key at minus infinity {dtype} {dim}")
+    q, k, v, do = inputs(dim, 1, 40, 100, 2, 1, dim, DTYPES[dtype])
+    q[..., 7] = -q[..., 7].abs() - 0.1
+    k[0, 50, 0, 7] = math.inf
+    mask = some_mask(dim + 1, 1, 2, 40, 100)
+    clean = of.attention(q.double(), zeroed(k).double(), v.double(), dim ** -0.5, q.dtype, None,
+                         mask & (torch.arange(100) != 50), do.double())
+    check(run(ctx, q, k, v, do, mask), formulas(q, k, v, do, mask), clean)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("which", ["v", "do"])
 def test_a_mask_that_shows_everything_is_no_mask(ctx, dtype, which):
     banner(f"attention all-true mask, bad {which} {dtype}")
     q, k, v, do = inputs(3, 1, 70, 90, 2, 1, 48, DTYPES[dtype])
