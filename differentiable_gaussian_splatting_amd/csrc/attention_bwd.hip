@@ -284,8 +284,10 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
         if constexpr (kMask) mask_at = int64_t(head) * a.ms[1] + int64_t(query) * a.ms[2];
       }
     }
+    // past the last row, q's is repeated, not made zeros: a key's infinity times 0 would be NaN, and its score has to be
+    // what p = 0 leaves alone (do is zeros there)
     if (plain) {
-      Copy::start(s, a.rows - row0, dim_in, [&](int r) { return qb + int64_t(row0 + r) * a.qs[1]; });
+      Copy::start(s, QT, dim_in, [&](int r) { return qb + int64_t(min(row0 + r, a.rows - 1)) * a.qs[1]; });
       Copy::start(s + kTile, a.rows - row0, dim_in,
                   [&](int r) { return db + int64_t(row0 + r) * a.dos[1]; });
     } else {
@@ -294,7 +296,7 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) vo
         row_of(a, w.kv_head, row0 + r, &query, &head);
         return base + int64_t(query) * st[1] + int64_t(head) * st[2];
       };
-      Copy::start(s, a.rows - row0, dim_in, [&](int r) { return row_at(qb, a.qs, r); });
+      Copy::start(s, QT, dim_in, [&](int r) { return row_at(qb, a.qs, min(row0 + r, a.rows - 1) - row0); });
       Copy::start(s + kTile, a.rows - row0, dim_in, [&](int r) { return row_at(db, a.dos, r); });
     }
   };

@@ -156,6 +156,22 @@ def test_a_key_at_minus_infinity_is_a_weight_of_zero(ctx, dtype, dim):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("dim", [32, 96, 128])
+@pytest.mark.parametrize("masked", [False, True])
+def test_a_key_of_no_weight_gets_no_gradient(ctx, dtype, dim, masked):
+    """k = inf where every query is negative: each weight is 0, and so are the key's dk and dv, also beside the rows past
+    the last that fill up a tile."""
+    banner(f"attention key of no weight {dtype} {dim} masked {masked}")
+    q, k, v, do = inputs(dim, 1, 45, 100, 1, 1, dim, DTYPES[dtype])
+    q[..., 7] = -q[..., 7].abs() - 0.1
+    k[0, 50, 0, 7] = math.inf
+    got = run(ctx, q, k, v, do, torch.ones((1, 1, 45, 100), dtype=torch.bool) if masked else None)
+    assert (got["dk"][0, 50] == 0).all() and (got["dv"][0, 50] == 0).all()
+    for name in ("o", "lse", "dk", "dv"):
+        assert got[name].isfinite().all(), name
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("which", ["v", "do"])
 def test_a_mask_that_shows_everything_is_no_mask(ctx, dtype, which):
     banner(f"attention all-true mask, bad {which} {dtype}")
