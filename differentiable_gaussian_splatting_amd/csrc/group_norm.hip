@@ -30,6 +30,11 @@ struct GnShape {
   float eps;
 };
 
+// Statistics as the caller keeps them, aligned as float.
+struct GnStats {
+  float mean, rstd;
+};
+
 // 1 / (1 + exp(-z)) with the hardware exponential and reciprocal, each within 1 ulp of its own result (an overflowing
 // exponential gives 0).
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
@@ -223,7 +228,7 @@ __device__ __forceinline__ void for_parts(const GnShape& g, uint32_t img, uint32
 // M2 = sum M2_i + n_i (mean_i - mean)^2.
 // Bound by latency (one pass for the means, one for the deviations, over at most a megabyte): 6 us at either size above.
 __global__ __launch_bounds__(kJoinThreads) void k_gn_finish(GnShape g, const float2* __restrict__ part,
-                                                        float2* __restrict__ stats) {
+                                                        GnStats* __restrict__ stats) {
   __shared__ float s[kJoinThreads / 64];
   const uint32_t grp = blockIdx.x, img = blockIdx.y;
   const float last = float(g.pixels - (g.chunks - 1) * g.chunk), full = float(g.chunk);
@@ -239,21 +244,21 @@ __global__ __launch_bounds__(kJoinThreads) void k_gn_finish(GnShape g, const flo
     q += fmaf((k + 1 == g.chunks ? last : full) * d, d, v.y);
   });
   const float var = block_sum(q, s) / total;
-  if (threadIdx.x == 0) stats[img * g.groups + grp] = make_float2(mean, 1.0f / sqrtf(var + g.eps));
+  if (threadIdx.x == 0) stats[img * g.groups + grp] = GnStats{mean, 1.0f / sqrtf(var + g.eps)};
 }
 
 // The channel constants a thread keeps for its V channels of one image.
 template <int V>
 struct Channel {
   float mean[V], rstd[V], gamma[V], beta[V];
-  __device__ __forceinline__ void load(const GnShape& g, uint32_t img, uint32_t c0, int n_c, const float2* stats,
+  __device__ __forceinline__ void load(const GnShape& g, uint32_t img, uint32_t c0, int n_c, const GnStats* stats,
                                        const float* gm, const float* bt) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const uint32_t c = i < n_c ? c0 + i : g.channels - 1;
-      const float2 st = stats[img * g.groups + c / g.cpg];
-      mean[i] = st.x;
-      rstd[i] = st.y;
+      const GnStats st = stats[img * g.groups + c / g.cpg];
+      mean[i] = st.mean;
+      rstd[i] = st.rstd;
       gamma[i] = gm ? gm[c] : 1.0f;
       beta[i] = bt ? bt[c] : 0.0f;
     }
@@ -267,7 +272,7 @@ template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void k_gn_apply(GnShape g, const T* __restrict__ x, int64_t xi, int64_t xp,
                                                        const float* __restrict__ gamma,
                                                        const float* __restrict__ beta,
-                                                       const float2* __restrict__ stats, T* y, int64_t yi,
+                                                       const GnStats* __restrict__ stats, T* y, int64_t yi,
                                                        int64_t yp) {
   constexpr int V = 16 / sizeof(T);
   const uint32_t col = threadIdx.x % g.cols, row = threadIdx.x / g.cols;
@@ -308,7 +313,7 @@ template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void k_gn_sums(GnShape g, const T* __restrict__ x, int64_t xi, int64_t xp,
                                                       const float* __restrict__ gamma,
                                                       const float* __restrict__ beta,
-                                                      const float2* __restrict__ stats, const T* __restrict__ dy,
+                                                      const GnStats* __restrict__ stats, const T* __restrict__ dy,
                                                       int64_t di, int64_t dp, float2* __restrict__ part) {
   constexpr int V = 16 / sizeof(T);
   __shared__ float s[kThreads][V * 2];
@@ -409,7 +414,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_gn_sums_join(GnShape g, const 
 template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void k_gn_dx(GnShape g, const T* __restrict__ x, int64_t xi, int64_t xp,
                                                     const float* __restrict__ gamma, const float* __restrict__ beta,
-                                                    const float2* __restrict__ stats, const T* dy, int64_t di,
+                                                    const GnStats* __restrict__ stats, const T* dy, int64_t di,
                                                     int64_t dp, const float2* __restrict__ chan,
                                                     const float2* __restrict__ group, T* dx, int64_t oi, int64_t op,
                                                     float* __restrict__ dgamma, float* __restrict__ dbeta) {
@@ -561,7 +566,7 @@ template <typename T, int ACT, int V>
 __global__ __launch_bounds__(kSmallThreads) void k_gn_small(GnShape g, GnSet t, const T* x, int64_t xi, int64_t xp,
                                                             const float* __restrict__ gamma,
                                                             const float* __restrict__ beta,
-                                                            float2* __restrict__ stats, T* y, int64_t yi,
+                                                            GnStats* __restrict__ stats, T* y, int64_t yi,
                                                             int64_t yp) {
   constexpr int kHold = kHoldForward;
   __shared__ SmallShared<V> s;
@@ -596,7 +601,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_gn_small(GnShape g, GnSet t, 
   group_totals(groups, g.cpg, s.chan[0], nullptr, s.group[1]);
   for (uint32_t k = threadIdx.x; k < groups; k += kSmallThreads)
     stats[blockIdx.y * g.groups + grp0 + k] =
-        make_float2(s.group[0][k] / total, 1.0f / sqrtf(s.group[1][k] / total + g.eps));
+        GnStats{s.group[0][k] / total, 1.0f / sqrtf(s.group[1][k] / total + g.eps)};
   if (!live) return;
   float shift[V];
 #pragma unroll
@@ -622,7 +627,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_gn_small(GnShape g, GnSet t, 
 template <typename T, int ACT, int V>
 __global__ __launch_bounds__(kSmallThreads) void k_gn_small_back(
     GnShape g, GnSet t, const T* __restrict__ x, int64_t xi, int64_t xp, const float* __restrict__ gamma,
-    const float* __restrict__ beta, const float2* __restrict__ stats, const T* dy, int64_t di, int64_t dp, T* dx,
+    const float* __restrict__ beta, const GnStats* __restrict__ stats, const T* dy, int64_t di, int64_t dp, T* dx,
     int64_t oi, int64_t op, float* __restrict__ dgamma, float* __restrict__ dbeta, float2* __restrict__ chan) {
   constexpr int kHold = kHoldBackward;
   __shared__ SmallShared<V> s;
@@ -814,7 +819,7 @@ extern "C" gsr_status gsr_group_norm_forward(gsr_ctx* ctx, void* stream, const g
   if (!d->images || !d->pixels || !d->channels) return GSR_OK;
   if (!x || !y || !stats) return fail(ctx, GSR_EINVAL, "%s: null pointer", who);
   const size_t eb = elem_bytes(d->dtype);
-  if (misaligned(x, eb) || misaligned(y, eb) || misaligned(gamma, 4) || misaligned(beta, 4) || misaligned(stats, 8))
+  if (misaligned(x, eb) || misaligned(y, eb) || misaligned(gamma, 4) || misaligned(beta, 4) || misaligned(stats, 4))
     return fail(ctx, GSR_EINVAL, "%s: a pointer is not aligned to its element", who);
   if ((st = check_out(ctx, d, d->y_stride, who, "y"))) return st;
   if ((st = enter(ctx))) return st;
@@ -829,7 +834,7 @@ extern "C" gsr_status gsr_group_norm_forward(gsr_ctx* ctx, void* stream, const g
       auto launch = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3((g.groups + set.groups - 1) / set.groups, g.images), dim3(kSmallThreads), 0, s,
                            g, set, static_cast<const T*>(x), d->x_stride[0], d->x_stride[1], gamma, beta,
-                           reinterpret_cast<float2*>(stats), static_cast<T*>(y), d->y_stride[0], d->y_stride[1]);
+                           reinterpret_cast<GnStats*>(stats), static_cast<T*>(y), d->y_stride[0], d->y_stride[1]);
       };
       if (vec == 2)
         launch(k_gn_small<T, decltype(a)::value, 2>);
@@ -841,7 +846,7 @@ extern "C" gsr_status gsr_group_norm_forward(gsr_ctx* ctx, void* stream, const g
   }
   if ((st = grow(ctx, ctx->arena.feat_part, size_t(g.images) * g.chunks * g.channels * sizeof(float2)))) return st;
   float2* part = static_cast<float2*>(ctx->arena.feat_part.ptr);
-  float2* out = reinterpret_cast<float2*>(stats);
+  GnStats* out = reinterpret_cast<GnStats*>(stats);
   hipStream_t s = static_cast<hipStream_t>(stream);
   timing_mark(ctx, GSR_STAGE_GROUP_NORM_FORWARD, s, false);
   by_kind(d, [&](auto t, auto a) {
@@ -876,7 +881,7 @@ extern "C" gsr_status gsr_group_norm_backward(gsr_ctx* ctx, void* stream, const 
   }
   if (!x || !stats || !dy) return fail(ctx, GSR_EINVAL, "%s: null pointer", who);
   const size_t eb = elem_bytes(d->dtype);
-  if (misaligned(x, eb) || misaligned(dy, eb) || misaligned(dx, eb) || misaligned(stats, 8))
+  if (misaligned(x, eb) || misaligned(dy, eb) || misaligned(dx, eb) || misaligned(stats, 4))
     return fail(ctx, GSR_EINVAL, "%s: a pointer is not aligned to its element", who);
   if (dx && (st = check_out(ctx, d, d->dx_stride, who, "dx"))) return st;
   if ((st = enter(ctx))) return st;
@@ -887,7 +892,7 @@ extern "C" gsr_status gsr_group_norm_backward(gsr_ctx* ctx, void* stream, const 
   float2* part = static_cast<float2*>(ctx->arena.feat_part.ptr);
   float2* chan = part + n_part;
   float2* group = chan + n_chan;
-  const float2* in = reinterpret_cast<const float2*>(stats);
+  const GnStats* in = reinterpret_cast<const GnStats*>(stats);
   GnSet set;
   timing_mark(ctx, GSR_STAGE_GROUP_NORM_BACKWARD, s, false);
   uint32_t vec;

@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+from featurehelp import normal
 from gpuhelp import banner
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +48,18 @@ def test_counts_of_more_than_32_bits_are_refused(ctx, extra):
         overflow(gsr.gsr_cross_attention_backward, ctx, one.expand(shape), kv, kv, one.expand(shape), lse,
                  one.expand(shape))
     overflow(gsr.gsr_cross_attention_forward, ctx, one, one.expand(1, n, 1, 8), one.expand(1, n, 1, 8))
+
+
+def test_statistics_at_any_float_alignment(ctx):
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("group norm statistics off 8-byte boundaries")
+    for p in (40, 9000):  # one launch, several
+        x, dy = normal(1, (2, p, 24)).cuda(), normal(2, (2, p, 24)).cuda()
+        y, stats = gsr.gsr_group_norm_forward(ctx, x, None, None, 4, 1e-5, 1)
+        ref = gsr.gsr_group_norm_backward(ctx, x, None, None, 4, stats, dy, 1)
+        odd = torch.full((2 * 4 * 2 + 2,), 7.0, device="cuda")
+        at = odd[1:-1].view(2, 4, 2)
+        y2, _ = gsr.gsr_group_norm_forward(ctx, x, None, None, 4, 1e-5, 1, stats=at)
+        assert torch.equal(y, y2) and torch.equal(at, stats) and odd[0] == 7 and odd[-1] == 7
+        got = gsr.gsr_group_norm_backward(ctx, x, None, None, 4, at, dy, 1)
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
