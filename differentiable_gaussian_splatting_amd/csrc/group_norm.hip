@@ -244,7 +244,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_gn_finish(GnShape g, const flo
     q += fmaf((k + 1 == g.chunks ? last : full) * d, d, v.y);
   });
   const float var = block_sum(q, s) / total;
-  if (threadIdx.x == 0) stats[img * g.groups + grp] = GnStats{mean, 1.0f / sqrtf(var + g.eps)};
+  if (threadIdx.x == 0) stats[uint64_t(img) * g.groups + grp] = GnStats{mean, 1.0f / sqrtf(var + g.eps)};
 }
 
 // The channel constants a thread keeps for its V channels of one image.
@@ -256,7 +256,7 @@ struct Channel {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const uint32_t c = i < n_c ? c0 + i : g.channels - 1;
-      const GnStats st = stats[img * g.groups + c / g.cpg];
+      const GnStats st = stats[uint64_t(img) * g.groups + c / g.cpg];
       mean[i] = st.mean;
       rstd[i] = st.rstd;
       gamma[i] = gm ? gm[c] : 1.0f;
@@ -405,7 +405,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_gn_sums_join(GnShape g, const 
   gb = block_sum(gb, s);
   if (threadIdx.x == 0) {
     const float m = float(g.pixels) * float(g.cpg);
-    group[img * g.groups + grp] = make_float2(ga / m, gb / m);
+    group[uint64_t(img) * g.groups + grp] = make_float2(ga / m, gb / m);
   }
 }
 
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_dx(GnShape g, const T* __restri
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const uint32_t c = i < n_c ? c0 + i : g.channels - 1;
-    const float2 v = group[blockIdx.y * g.groups + c / g.cpg];
+    const float2 v = group[uint64_t(blockIdx.y) * g.groups + c / g.cpg];
     m1[i] = v.x;
     m2[i] = v.y;
   }
@@ -600,7 +600,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_gn_small(GnShape g, GnSet t, 
   channel_totals<V>(t, row < t.rows, v, s.part, s.sub, s.chan[0]);
   group_totals(groups, g.cpg, s.chan[0], nullptr, s.group[1]);
   for (uint32_t k = threadIdx.x; k < groups; k += kSmallThreads)
-    stats[blockIdx.y * g.groups + grp0 + k] =
+    stats[uint64_t(blockIdx.y) * g.groups + grp0 + k] =
         GnStats{s.group[0][k] / total, 1.0f / sqrtf(s.group[1][k] / total + g.eps)};
   if (!live) return;
   float shift[V];

@@ -63,3 +63,17 @@ def test_statistics_at_any_float_alignment(ctx):
         assert torch.equal(y, y2) and torch.equal(at, stats) and odd[0] == 7 and odd[-1] == 7
         got = gsr.gsr_group_norm_backward(ctx, x, None, None, 4, at, dy, 1)
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_statistics_past_32_bits(ctx):
+    """More than 2^32 (image, group) pairs: every image's statistics in its own place. One value a group, so the mean is
+    the value itself and the result 0."""
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("group norm of 2^32 + 4 * 2^19 groups")
+    n, c = (1 << 13) + 4, 1 << 19
+    row = normal(1, (c,), torch.bfloat16).cuda()
+    y, stats = gsr.gsr_group_norm_forward(ctx, row.expand(n, 1, c), None, None, c, 1.0)
+    for i in (0, 1, 3, 4, 4096, n - 5, n - 4, n - 1):
+        assert torch.equal(stats[i, :, 0], row.float()) and (stats[i, :, 1] == 1).all() and (y[i] == 0).all(), i
+    del y, stats
+    torch.cuda.empty_cache()  # 43 GB
