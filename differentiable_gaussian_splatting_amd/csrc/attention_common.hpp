@@ -73,8 +73,9 @@ struct AttnArgs {
 struct AttnWork {
   uint32_t tile, split, kv_head, batch;
   __device__ __forceinline__ bool set(const AttnArgs& a) {
-    uint32_t w = (blockIdx.x % kFeatXcds) * a.per_xcd + blockIdx.x / kFeatXcds;
-    if (w >= a.works || blockIdx.x / kFeatXcds >= a.per_xcd) return false;
+    const uint32_t id = uint32_t(grid_index());
+    uint32_t w = (id % kFeatXcds) * a.per_xcd + id / kFeatXcds;
+    if (w >= a.works || id / kFeatXcds >= a.per_xcd) return false;
     tile = w % a.tiles;
     w /= a.tiles;
     split = w % a.splits;
@@ -482,7 +483,7 @@ inline dim3 attention_grid(AttnArgs* a, uint32_t tiles, uint64_t steps, uint32_t
   }
   a->works = uint32_t(base * a->splits);
   a->per_xcd = (a->works + kFeatXcds - 1) / kFeatXcds;
-  return dim3(a->per_xcd * kFeatXcds);
+  return grid_rows(uint64_t(a->per_xcd) * kFeatXcds);
 }
 
 // Calls f(element type, head dimension padded to a multiple of 16, whether there is a mask).

@@ -347,7 +347,7 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_pack(const T* __restrict_
                                                             int64_t s2, uint32_t tokens, uint32_t heads, uint32_t dim,
                                                             uint64_t chunks, uint32_t per_row, T* __restrict__ out) {
   constexpr int kPer = 16 / int(sizeof(T));
-  const uint64_t id = uint64_t(blockIdx.x) * kAttnThreads + threadIdx.x;
+  const uint64_t id = grid_index() * kAttnThreads + threadIdx.x;
   if (id >= chunks) return;
   const uint32_t c = uint32_t(id % per_row) * kPer;
   const uint64_t row = id / per_row, token = row / heads;
@@ -385,7 +385,7 @@ void attention_pack(AttnArgs* a, uint32_t dtype, std::initializer_list<AttnInput
     if (chunks) {
       auto launch = [&](auto e) {
         using T = decltype(e);
-        hipLaunchKernelGGL((k_attn_pack<T>), dim3(uint32_t((chunks + kAttnThreads - 1) / kAttnThreads)),
+        hipLaunchKernelGGL((k_attn_pack<T>), grid_rows((chunks + kAttnThreads - 1) / kAttnThreads),
                            dim3(kAttnThreads), 0, s, static_cast<const T*>(*t.p), t.stride[0], t.stride[1],
                            t.stride[2], t.tokens, t.heads, a->dim, chunks, uint32_t(row / 16),
                            reinterpret_cast<T*>(to));

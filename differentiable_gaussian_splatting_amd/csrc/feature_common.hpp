@@ -14,6 +14,17 @@ namespace gsr {
 
 constexpr uint32_t kFeatXcds = 8;  // accelerator dies; workgroups are dealt to them round-robin
 
+// A launch's dimension holds fewer than 2^32 threads: more workgroups than kGridRow are laid out in rows of that many
+// (a multiple of the dies, so that their order stays), the last row perhaps past the count.
+constexpr uint32_t kGridRow = 1u << 23;
+
+inline dim3 grid_rows(uint64_t workgroups) {
+  if (workgroups <= kGridRow) return dim3(uint32_t(workgroups));
+  return dim3(kGridRow, uint32_t((workgroups + kGridRow - 1) / kGridRow));
+}
+
+__device__ __forceinline__ uint64_t grid_index() { return uint64_t(blockIdx.y) * kGridRow + blockIdx.x; }
+
 // Storage types: float, _Float16, __bf16. Conversions to and from float round to nearest even.
 template <typename T, int N>
 using Vec = T __attribute__((ext_vector_type(N)));

@@ -49,7 +49,9 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs a, const T* x, c
                                                      T* out, bool back) {
   constexpr int V = 16 / sizeof(T), kAtOnce = kHalves ? 2 : 4;
   __shared__ float2 s_turn[kAngles];
-  const uint32_t tok0 = blockIdx.x * a.group, group = min(a.group, a.all_tokens - tok0);
+  const uint64_t first = grid_index() * a.group;
+  if (first >= a.all_tokens) return;
+  const uint32_t tok0 = uint32_t(first), group = min(a.group, a.all_tokens - tok0);
   const uint32_t items = group * a.heads * a.units.d;
   struct Item {
     const T* from;
@@ -182,7 +184,7 @@ gsr_status rotary(gsr_ctx* ctx, void* stream, const gsr_rotary* d, const void* x
   uint64_t group = std::max<uint64_t>(1, std::min<uint64_t>(2048 / per_token, kAngles / std::max(1u, a.pairs)));
   group = std::min(group, std::max<uint64_t>(1, a.all_tokens / 1024));
   a.group = uint32_t(group);
-  const dim3 grid(uint32_t((uint64_t(a.all_tokens) + group - 1) / group));
+  const dim3 grid = grid_rows((uint64_t(a.all_tokens) + group - 1) / group);
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto launch = [&](auto t) {
     using T = decltype(t);

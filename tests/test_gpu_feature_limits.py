@@ -1,4 +1,6 @@
 """The feature operators at their limits: counts that do not fit 32 bits, offsets and launches past them, alignment."""
+import math
+
 import pytest
 import torch
 
@@ -77,3 +79,61 @@ def test_statistics_past_32_bits(ctx):
         assert torch.equal(stats[i, :, 0], row.float()) and (stats[i, :, 1] == 1).all() and (y[i] == 0).all(), i
     del y, stats
     torch.cuda.empty_cache()  # 43 GB
+
+
+def test_more_workgroups_than_one_dimension_of_a_launch(ctx):
+    """2^24 + 64 key heads of one query each: more than 2^32 threads."""
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("attention of 2^24 + 64 key heads")
+    b, h, tk, d = (1 << 22) + 16, 4, 3, 8
+    k, v = normal(1, (1, tk, h, d), torch.float16).cuda(), normal(2, (1, tk, h, d), torch.float16).cuda()
+    q = normal(3, (64, 1, h, d), torch.float16).cuda()
+    few = [t.expand(64, tk, h, d) for t in (k, v)]
+    ref_o, ref_lse = gsr.gsr_cross_attention_forward(ctx, q, *few)
+    ref = gsr.gsr_cross_attention_backward(ctx, q, *few, ref_o, ref_lse, q)
+    many = q.repeat(b // 64 + 1, 1, 1, 1)[:b]
+    kv = [t.expand(b, tk, h, d) for t in (k, v)]
+    o, lse = gsr.gsr_cross_attention_forward(ctx, many, *kv)
+    got = gsr.gsr_cross_attention_backward(ctx, many, *kv, o, lse, many)
+    for x, want in ((o, ref_o), (lse, ref_lse)) + tuple(zip(got, ref)):
+        whole = x[:b // 64 * 64].view(-1, 64, *x.shape[1:])
+        assert (whole == want).all() and torch.equal(x[b // 64 * 64:], want[:b % 64])
+
+
+def test_more_chunks_to_copy_than_one_dimension_of_a_launch():
+    """2^28 + 40 keys off a 16-byte boundary, of which 2^32 + 640 chunks are copied to the scratch (64 GiB): one key seen
+    2^28 times, whose value is a power of two, so that the output is exact."""
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("attention of 2^28 + 40 unaligned keys")
+    n, d = (1 << 28) + 40, 128
+    c = gsr.Context(0)
+    try:
+        q = torch.full((1, 1, 1, d), 0.125, dtype=torch.bfloat16, device="cuda")
+        k = torch.full((d + 1,), 0.25, dtype=torch.bfloat16, device="cuda")[1:].view(1, 1, 1, d).expand(1, n, 1, d)
+        v = torch.full((1, 1, 1, d), 0.5, dtype=torch.bfloat16, device="cuda")
+        v[..., ::2] = -4
+        o, lse = gsr.gsr_cross_attention_forward(c, q, k, v.expand(1, n, 1, d), 1.0)
+        assert torch.equal(o, v)
+        assert abs(float(lse) - (128 / 32 + math.log(n))) < 1e-5
+    finally:
+        c.close()
+
+
+def test_more_rotary_workgroups_than_one_dimension_of_a_launch(ctx):
+    """2^28 + 40 tokens of 128 pairs, 16 to a workgroup, turned in place (137 GB)."""
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("rotary of 2^28 + 40 tokens of 256")
+    n, d = (1 << 28) + 40, 256
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < n * (2 * d + 4) + (8 << 30):
+        pytest.skip("needs 146 GB of device memory")
+    x = torch.ones((1, n, 1, d), dtype=torch.bfloat16, device="cuda")
+    pos = (torch.arange(n, device="cuda", dtype=torch.int32) % 1000).float().view(1, n, 1)
+    gsr.gsr_rotary_forward(ctx, x, pos, [d // 2], out=x)
+    for at in (0, 12345, (1 << 27) - 7, (1 << 28) - 100, n - 100):
+        part = slice(at, at + 100)
+        want = gsr.gsr_rotary_forward(ctx, torch.ones((1, 100, 1, d), dtype=torch.bfloat16, device="cuda"),
+                                      pos[:, part].contiguous(), [d // 2])
+        assert torch.equal(x[:, part], want), at
+    del x
+    torch.cuda.empty_cache()
