@@ -492,10 +492,11 @@ def _need_feature(t, name, device, dtype=None, shape=None):
         raise ValueError(f"the last dimension of {name} must be adjacent in memory")
 
 
-def _fit(names, *values):
-    """Refuses what the descriptors' 32-bit fields would cut off (the library checks the range of what they hold)."""
-    if min(values) < 0 or max(values) >> 32:
-        raise GsrError(GSR_EOVERFLOW, f"{names}: {values} do not fit 32 bits")
+def _fit(names, bits):
+    """Refuses counts, or-ed together, that the descriptors' 32-bit fields would cut off (the library checks the range of
+    what they hold)."""
+    if bits >> 32:  # also of a negative one
+        raise GsrError(GSR_EOVERFLOW, f"{names}: a value does not fit 32 bits")
 
 
 def _image_strides(t, name):
@@ -529,7 +530,7 @@ def _group_norm_desc(ctx, x, gamma, beta, groups, eps, activation):
     pixels = 1
     for n in x.shape[1:-1]:
         pixels *= n
-    _fit("images, pixels, channels, groups, activation", x.shape[0], pixels, C, groups, activation)
+    _fit("images, pixels, channels, groups, activation", x.shape[0] | pixels | C | groups | activation)
     d = gsr_group_norm(_DTYPES[x.dtype], x.shape[0], pixels, C, groups, activation, eps)
     d.x_stride[:] = _image_strides(x, "x")
     return d
@@ -593,7 +594,10 @@ def _rotary(ctx, x, positions, axis_pairs, base, layout, out, stream, name):
             or positions.shape[0] not in (1, B):
         raise ValueError(f"positions must be float32 [{B} or 1, {T}, {axes}]")
     _need(positions, "positions", (torch.float32,), None, dev)
-    _fit("batch, tokens, heads, head_dim, layout, axis_pairs", B, T, H, D, layout, *axis_pairs)
+    bits = B | T | H | D | layout
+    for n in axis_pairs:
+        bits |= n
+    _fit("batch, tokens, heads, head_dim, layout, axis_pairs", bits)
     if out is None:
         out = _like(x)
     _need_feature(out, "out", dev, x.dtype, x.shape)
@@ -628,7 +632,7 @@ def _attention_desc(ctx, q, k, v, scale, kv_lengths, mask):
         raise ValueError("q must be [batch, queries, heads, dim], k and v [batch, keys, kv_heads, dim]")
     B, Tq, H, D = q.shape
     Tk, Hk = k.shape[1], k.shape[2]
-    _fit("batch, queries, heads, keys, kv_heads, head_dim", B, Tq, H, Tk, Hk, D)
+    _fit("batch, queries, heads, keys, kv_heads, head_dim", B | Tq | H | Tk | Hk | D)
     _need_feature(k, "k", dev, q.dtype, (B, Tk, Hk, D))
     _need_feature(v, "v", dev, q.dtype, (B, Tk, Hk, D))
     if kv_lengths is not None:
