@@ -524,7 +524,7 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
   static const char* who = "gsr_cross_attention_backward";
   if (!ctx) return GSR_EINVAL;
   AttnArgs a;
-  gsr_status st = attention_args(ctx, d, q, k, v, kv_lengths, mask, o, dout, who, &a);
+  gsr_status st = attention_args(ctx, d, q, k, v, kv_lengths, mask, o, who, &a);
   if (st) return st;
   const size_t eb = elem_bytes(d->dtype);
   const bool has_q = d->batch && d->queries, has_k = d->batch && d->keys;

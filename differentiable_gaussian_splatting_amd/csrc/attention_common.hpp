@@ -104,7 +104,6 @@ __device__ __forceinline__ uint32_t keys_of(const AttnArgs& a, uint32_t batch) {
 template <typename T, int DK>
 struct Tile {
   static constexpr int kPer = 16 / int(sizeof(T));                 // elements per chunk
-  static constexpr int kUsed = DK / kPer;                          // chunks of a row that hold elements
   static constexpr int kRow = DK <= 32 ? 32 : (DK <= 64 ? 64 : 128);  // elements from row to row
   static constexpr int kChunks = kRow / kPer;
   static constexpr int kRowBytes = kRow * int(sizeof(T));
@@ -449,8 +448,8 @@ __device__ __forceinline__ uint32_t visible(const uint32_t* words, uint32_t key0
 
 // Host side (attention_fwd.hip): checks the descriptor and the inputs both directions share and fills the arguments.
 gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, const void* k, const void* v,
-                          const int32_t* kv_lengths, const uint8_t* mask, const void* o, const void* dout,
-                          const char* who, AttnArgs* a);
+                          const int32_t* kv_lengths, const uint8_t* mask, const void* o, const char* who,
+                          AttnArgs* a);
 
 // An input of the kernels: its tensor and strides in the arguments, and the tokens and heads it has.
 struct AttnInput {

@@ -291,8 +291,8 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs a) {
 }  // namespace
 
 gsr_status attention_args(gsr_ctx* ctx, const gsr_attention* d, const void* q, const void* k, const void* v,
-                          const int32_t* kv_lengths, const uint8_t* mask, const void* o, const void* dout,
-                          const char* who, AttnArgs* a) {
+                          const int32_t* kv_lengths, const uint8_t* mask, const void* o, const char* who,
+                          AttnArgs* a) {
   if (!d) return fail(ctx, GSR_EINVAL, "%s: null descriptor", who);
   if (d->dtype > GSR_BF16) return fail(ctx, GSR_EINVAL, "%s: unknown dtype %u", who, d->dtype);
   if (d->kv_heads == 0 || d->heads == 0 || d->heads % d->kv_heads)
@@ -413,7 +413,7 @@ extern "C" gsr_status gsr_cross_attention_forward(gsr_ctx* ctx, void* stream, co
   static const char* who = "gsr_cross_attention_forward";
   if (!ctx) return GSR_EINVAL;
   AttnArgs a;
-  gsr_status st = attention_args(ctx, d, q, k, v, kv_lengths, mask, o, nullptr, who, &a);
+  gsr_status st = attention_args(ctx, d, q, k, v, kv_lengths, mask, o, who, &a);
   if (st) return st;
   if (misaligned(lse, 4)) return fail(ctx, GSR_EINVAL, "%s: a pointer is not aligned to its element", who);
   if (!distinct({{d->o_stride[0], d->batch}, {d->o_stride[1], d->queries}, {d->o_stride[2], d->heads}}, d->head_dim))
