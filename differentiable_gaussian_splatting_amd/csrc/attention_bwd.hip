@@ -25,9 +25,12 @@ constexpr bool kOneInLds = sizeof(T) == 2 && DK == 96 && !kMask;
 template <typename T, int DK, bool kMask>
 constexpr bool kOneInLdsKeys = sizeof(T) == 2 && DK > 64 && !kMask;
 // Waves that share a SIMD, so that one multiplies while another computes exponentials: two where 256 registers hold a
-// wave's operands and sums.
+// wave's operands and sums, or all but a few of them. 16 bits at 64 wide spill 2 to 15 registers of the queries' kernel,
+// 96 wide 13 to 24, the keys' kernel at 128 wide 10 to 31, and two waves are faster all the same (training steps of
+// 2,500 x 2,500, 8 heads, bfloat16: 237 against 266 us, 353 against 395, 486 against 515); so is float32 at 48 wide
+// (1,300 x 1,369: 355 against 361), but not at 64 wide (16 to 35 spilled: 431 against 427, with a mask 550 against 533).
 template <typename T, int DK, bool kMask>
-constexpr int kWavesPerSimd = DK <= 64 || kOneInLds<T, DK, kMask> ? 2 : 1;
+constexpr int kWavesPerSimd = DK <= (sizeof(T) == 2 ? 64 : 48) || kOneInLds<T, DK, kMask> ? 2 : 1;
 template <typename T, int DK, bool kMask>
 constexpr int kWavesPerSimdKeys =
     sizeof(T) == 2 ? (DK <= 64 || kOneInLdsKeys<T, DK, kMask> ? 2 : 1) : (DK <= 32 || (DK <= 48 && !kMask) ? 2 : 1);
@@ -555,7 +558,7 @@ extern "C" gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, c
   const bool one_q = open && a.dim > 64 && a.dim <= 96, one_k = open && a.dim > 64;
   const uint32_t streamed_q = open && !one_q ? 64 : 32, streamed_k = open && !one_k ? 64 : 32;
   const uint32_t cost = half ? 2 : 1;  // 16 bits step faster: 96 wide, 2,500 x 2,500, 378 -> 342 us against 1
-  const uint32_t slots_q = a.dim <= 64 || one_q ? 512 : 256;
+  const uint32_t slots_q = a.dim <= (half ? 64u : 48u) || one_q ? 512 : 256;
   const uint32_t slots_k = (half ? a.dim <= 64 || one_k : a.dim <= (mask ? 32u : 48u)) ? 512 : 256;
   const dim3 grid_q = attention_grid(&a, (a.rows + kAttnRows - 1) / kAttnRows,
                                      (uint64_t(a.keys) + streamed_q - 1) / streamed_q, slots_q, cost);
