@@ -485,7 +485,8 @@ inline dim3 attention_grid(AttnArgs* a, uint32_t tiles, uint64_t steps, uint32_t
   return grid_rows(uint64_t(a->per_xcd) * kFeatXcds);
 }
 
-// Calls f(element type, head dimension padded to a multiple of 16, whether there is a mask).
+// Calls f(element type, head dimension padded to 32, 48, 64, 96 or 128, whether there is a mask). Heads between two of
+// these pay for the wider one: five widths by three types and two masks are what the kernels are built for.
 template <typename F>
 void attention_by_kind(uint32_t dtype, uint32_t dim, bool mask, F f) {
   auto m = [&](auto t, auto dk) {
