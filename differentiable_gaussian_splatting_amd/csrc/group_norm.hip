@@ -887,17 +887,20 @@ extern "C" gsr_status gsr_group_norm_backward(gsr_ctx* ctx, void* stream, const 
   if (dx && (st = check_out(ctx, d, d->dx_stride, who, "dx"))) return st;
   if ((st = enter(ctx))) return st;
   const GnShape g = shape_of(d);
-  const size_t n_part = size_t(g.images) * g.chunks * g.channels, n_chan = size_t(g.images) * g.channels;
-  if ((st = grow(ctx, ctx->arena.feat_part, (n_part + n_chan + size_t(g.images) * g.groups) * sizeof(float2))))
-    return st;
+  GnSet set;
+  uint32_t vec;
+  const bool small = small_set(g, d->dtype, kHoldBackward, &set, &vec);
+  // one launch leaves the sums of several images alone in the scratch
+  const size_t n_part = small ? 0 : size_t(g.images) * g.chunks * g.channels;
+  const size_t n_chan = small && g.images == 1 ? 0 : size_t(g.images) * g.channels;
+  const size_t n_group = small ? 0 : size_t(g.images) * g.groups;
+  if ((st = grow(ctx, ctx->arena.feat_part, (n_part + n_chan + n_group) * sizeof(float2)))) return st;
   float2* part = static_cast<float2*>(ctx->arena.feat_part.ptr);
   float2* chan = part + n_part;
   float2* group = chan + n_chan;
   const GnStats* in = reinterpret_cast<const GnStats*>(stats);
-  GnSet set;
   timing_mark(ctx, GSR_STAGE_GROUP_NORM_BACKWARD, s, false);
-  uint32_t vec;
-  if (small_set(g, d->dtype, kHoldBackward, &set, &vec)) {
+  if (small) {
     by_kind(d, [&](auto t, auto a) {
       using T = decltype(t);
       auto launch = [&](auto kernel) {

@@ -2,8 +2,8 @@
 in the arena. Element by element within the fp64 oracle's bounds.
 
 Which route a forward takes is read off its scratch: one launch needs none, so it works under an arena limit of one byte,
-and several launches fail there. A backward needs some on either; 8,193 pixels and more are beyond the registers of a
-workgroup (1,024 threads of 8 vectors forward, 4 backward, a pixel each at least)."""
+and several launches fail there. 8,193 pixels and more are beyond the registers of a workgroup (1,024 threads of 8 vectors
+forward, 4 backward, a pixel each at least), so their backward takes several launches too."""
 import ctypes
 
 import pytest
@@ -191,6 +191,24 @@ def test_strided_and_in_place(ctx, bare, n, h, w):
     b = xc[:1].expand(n, h, w, 48)
     yb, _ = gsr.gsr_group_norm_forward(ctx, b, gamma, beta, 4, 1e-5, 1)
     assert torch.equal(yb, y[:1].expand(n, h, w, 48))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_the_backward_in_one_launch_asks_for_the_images_sums_alone(ctx, dtype):
+    """Two floats per image and channel, and nothing for one image."""
+    from differentiable_gaussian_splatting_amd import gsr
+    banner(f"group norm backward scratch {dtype}")
+    for n, p, c, room in ((1, 40, 24, 1), (160, 120, 48, 8 * 160 * 48)):
+        x, dy = features(3, n, p, c, DTYPES[dtype]).cuda(), normal(4, (n, p, c), DTYPES[dtype]).cuda()
+        y, st = gsr.gsr_group_norm_forward(ctx, x, None, None, 4, 1e-5, 1)
+        ref = gsr.gsr_group_norm_backward(ctx, x, None, None, 4, st, dy, 1)
+        tight = gsr.Context(0)
+        try:
+            gsr.gsr_set_option(tight, gsr.GSR_OPT_ARENA_LIMIT, room)
+            got = gsr.gsr_group_norm_backward(tight, x, None, None, 4, st, dy, 1)
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        finally:
+            tight.close()
 
 
 @pytest.mark.parametrize("n,p", [(2, MANY), (160, 120)], ids=str)
