@@ -637,7 +637,7 @@ def _attention_desc(ctx, q, k, v, scale, kv_lengths, mask):
     _need_feature(v, "v", dev, q.dtype, (B, Tk, Hk, D))
     if kv_lengths is not None:
         _need(kv_lengths, "kv_lengths", (torch.int32,), B, dev)
-    d = gsr_attention(_DTYPES[q.dtype], B, H, Hk, Tq, Tk, D, D ** -0.5 if scale is None else scale)
+    d = gsr_attention(_DTYPES[q.dtype], B, H, Hk, Tq, Tk, D, max(D, 1) ** -0.5 if scale is None else scale)
     d.q_stride[:] = q.stride()[:3]
     d.k_stride[:] = k.stride()[:3]
     d.v_stride[:] = v.stride()[:3]

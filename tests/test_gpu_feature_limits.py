@@ -52,6 +52,15 @@ def test_counts_of_more_than_32_bits_are_refused(ctx, extra):
     overflow(gsr.gsr_cross_attention_forward, ctx, one, one.expand(1, n, 1, 8), one.expand(1, n, 1, 8))
 
 
+def test_heads_of_no_elements_are_refused(ctx):
+    from differentiable_gaussian_splatting_amd import gsr
+    banner("attention heads of no elements")
+    q, kv = torch.zeros((1, 2, 1, 0), device="cuda"), torch.zeros((1, 3, 1, 0), device="cuda")
+    with pytest.raises(gsr.GsrError) as e:
+        gsr.gsr_cross_attention_forward(ctx, q, kv, kv)
+    assert e.value.status == gsr.GSR_EINVAL
+
+
 def test_statistics_at_any_float_alignment(ctx):
     from differentiable_gaussian_splatting_amd import gsr
     banner("group norm statistics off 8-byte boundaries")
