@@ -109,7 +109,8 @@ __device__ __forceinline__ void two_sum(float a, float b, float* sum, float* res
 // cancelled anywhere, so neither a far mean nor an outlier, wherever it stands, costs more than the roundings of the
 // sum of positive terms. The differences are taken from the thread's first value (exact for values near each other);
 // the means come from the values' own sum, its roundings carried along.
-// Bound by memory: 2 x 800 x 800 x 64 bfloat16 (164 MB) 36 us, 4.5 TB/s; 4 x 100 x 100 x 320 float32 (51 MB) 12 us. About
+// 2 x 800 x 800 x 64 bfloat16 (164 MB) 39 us, 4.2 TB/s, the vector units busy 62 % (36 us with sums of squares about the
+// first value, which an outlier there spoils); 4 x 100 x 100 x 320 float32 (51 MB) 13.4 us. About
 // 2,048 chunks over the images: eight workgroups a compute unit, and few enough partial sums that their join is short.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_gn_stats(GnShape g, const T* __restrict__ x, int64_t xi, int64_t xp,
@@ -409,7 +410,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_gn_sums_join(GnShape g, const 
   }
 }
 
-// Bound by memory, x and dy read and dx written: 4 x 100 x 100 x 320 float32 (154 MB) 26 us, 5.9 TB/s (part of x and dy is
+// Bound by memory, x and dy read and dx written: 4 x 100 x 100 x 320 float32 (154 MB) 25 us, 6.1 TB/s (part of x and dy is
 // still in the last level of cache).
 template <typename T, int ACT>
 __global__ __launch_bounds__(kThreads) void k_gn_dx(GnShape g, const T* __restrict__ x, int64_t xi, int64_t xp,

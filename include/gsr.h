@@ -383,7 +383,9 @@ gsr_status gsr_loss_l1_ssim(gsr_ctx* ctx, void* stream, uint32_t width, uint32_t
  * statistics and normalisation statistics are float32, and a 16-bit result is rounded once, to nearest even. All of
  * them give the same bits on every run. Strides count elements; outputs must not overlap themselves or an input
  * (except where stated), which is checked for an output's own strides. Any pointer aligned to its element works;
- * pointers and strides of whole 16 bytes are fastest. */
+ * pointers and strides of whole 16 bytes are fastest. The scratch that some calls take from the context arena grows on
+ * the first call that needs more and is not part of gsr_reserve: before such calls are captured in a graph, make the
+ * largest of them once; a later, larger one moves the scratch, and graphs captured before it have to be captured again. */
 #define GSR_F32 0
 #define GSR_F16 1
 #define GSR_BF16 2
