@@ -70,10 +70,10 @@ struct Ranged {
   __device__ __forceinline__ float undo() const { return kOn ? (f == 0.0f ? 0.0f : 1.0f / f) : 1.0f; }
 };
 
-// dq of the workgroup's rows. 2 x 2,500 x 2,500, 8 heads, 128 wide, bfloat16: 185 us, 415 TFLOP/s of its three products
-// (553 with the second one of ds); 777 x 1,369, 6 heads on 2, 48 wide, masked, float32: 69 us. Bound by LDS latency with one
-// wave on a SIMD at 128 wide (the matrix cores busy 24 %), by issue below; float32 by its products, which the vector units
-// do not overlap.
+// dq of the workgroup's rows. 2 x 2,500 x 2,500, 8 heads, 128 wide, bfloat16: 185 us, 415 TFLOP/s of its three
+// products (553 with the second one of ds); 777 x 1,369, 6 heads on 2, 48 wide, masked, float32: 69 us. Bound by LDS
+// latency with one wave on a SIMD at 128 wide (the matrix cores busy 24 %), by issue below; float32 by its products,
+// which the vector units do not overlap.
 template <typename T, int DK, bool kMask>
 __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k_attn_dq(AttnArgs a) {
   using L = Tile<T, DK>;
@@ -141,9 +141,9 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
 #pragma unroll
       for (int j = 0; j < 8; ++j) delta = fmaf(float(df[kk][j]), float(of[j]), delta);
     }
-    // p carries the rounding of lse: 2^-24 |lse| of a whole row. In float32 that leaves dv at 1.7 times the error of a form
-    // that keeps its probabilities where |lse| is 116, at 4 times (1.3e-5) where it is 464, and dk and dv at twice
-    // (7e-7) on 10,000 nearly equal keys; dq and dk differ by less.
+    // p carries the rounding of lse: 2^-24 |lse| of a whole row. In float32 that leaves dv at 1.7 times the error of a
+    // form that keeps its probabilities where |lse| is 116, at 4 times (1.3e-5) where it is 464, and dk and dv at
+    // twice (7e-7) on 10,000 nearly equal keys; dq and dk differ by less.
     if (lse != -INFINITY) {
       lse2 = lse * kLog2e;
     } else {
@@ -243,9 +243,9 @@ __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimd<T, DK, kMask>)) void k
   store_column<L::kOut>(out, acc, range.undo(), dim);
 }
 
-// dk and dv of the workgroup's keys, at the same sizes: 190 us, 539 TFLOP/s of its four products (674 with the second one
-// of ds), the matrix cores busy 30 %; float32 105 us. Bound by LDS: every operand of a streamed tile is read by row and
-// once more transposed.
+// dk and dv of the workgroup's keys, at the same sizes: 190 us, 539 TFLOP/s of its four products (674 with the second
+// one of ds), the matrix cores busy 30 %; float32 105 us. Bound by LDS: every operand of a streamed tile is read by
+// row and once more transposed.
 template <typename T, int DK, bool kMask>
 __global__ __launch_bounds__(kAttnThreads, (kWavesPerSimdKeys<T, DK, kMask>)) void k_attn_dkv(AttnArgs a) {
   using L = Tile<T, DK>;

@@ -70,13 +70,13 @@ constexpr int kKeyTile = sizeof(T) == 2 && DK <= 64 ? 64 : 32;  // keys of a til
 
 // kFew: at most 32 rows, the waves share them and split each tile's keys.
 // 4,096 queries x 10,000 keys, 16 heads, 64 wide, bfloat16: 237 to 246 us, about 700 TFLOP/s where a large product of
-// matrices reaches 1,235; 2 x 2,500 x 2,500, 8 heads, 128 wide: 105 us, 488 TFLOP/s. Bound by issue and by the latency of
-// LDS: the matrix cores are busy 29 % of the cycles (19 % at 128 wide), exponentials and conversions take the vector
-// units half of them, and a wave issues one or the other. A 128-row tile keeps a wave's rows in registers, so a byte of LDS feeds 32 rows; waves of 64 rows
-// (half the LDS reads) were no faster at 64 wide (261 against 268 us then) and slower at 128 (177 against 118), more
-// splits for three or four waves a SIMD slower (279 to 283 against 267), scores a tile ahead of their softmax no faster
-// (260 against 257). kFew: 4 x 10,000 ragged keys, 16 heads on 4 key heads, 128 wide, 17 us, about 3.6 TB/s of keys and
-// values.
+// matrices reaches 1,235; 2 x 2,500 x 2,500, 8 heads, 128 wide: 105 us, 488 TFLOP/s. Bound by issue and by the latency
+// of LDS: the matrix cores are busy 29 % of the cycles (19 % at 128 wide), exponentials and conversions take the
+// vector units half of them, and a wave issues one or the other. A 128-row tile keeps a wave's rows in registers, so a
+// byte of LDS feeds 32 rows; waves of 64 rows (half the LDS reads) were no faster at 64 wide (261 against 268 us then)
+// and slower at 128 (177 against 118), more splits for three or four waves a SIMD slower (279 to 283 against 267),
+// scores a tile ahead of their softmax no faster (260 against 257). kFew: 4 x 10,000 ragged keys, 16 heads on 4 key
+// heads, 128 wide, 17 us, about 3.6 TB/s of keys and values.
 template <typename T, int DK, bool kMask, bool kFew>
 __global__ __launch_bounds__(kAttnThreads, DK <= 64 || (sizeof(T) == 2 && !kMask) ? 2 : 1) void k_attn_fwd(AttnArgs a) {
   using L = Tile<T, DK>;
