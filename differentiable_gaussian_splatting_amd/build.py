@@ -25,7 +25,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgsr.so")
 SOURCES = ["ctx.hip", "bin.hip", "sort.hip", "raster_fwd.hip", "raster_bwd.hip", "adam.hip", "project.hip", "loss.hip",
-           "tile_depth.hip", "group_norm.hip", "rotary.hip", "attention_fwd.hip", "attention_bwd.hip"]
+           "tile_depth.hip", "group_norm.hip", "rotary.hip", "attention_fwd.hip", "attention_bwd.hip",
+           "layer_norm.hip", "orthogonalize.hip"]
 ARCH = os.environ.get("GSR_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [

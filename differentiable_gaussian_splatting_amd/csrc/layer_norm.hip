@@ -1,0 +1,532 @@
+// Layer norm over the channels of each token, and its backward pass.
+//
+// A team of lanes (part of a wave, a wave, or a workgroup of several) holds a token's channels in registers, 16 bytes a
+// load, so that each feature is read once: the mean, the squared deviations about it (no difference of squares) and the
+// result come from the same registers. Teams walk tokens in a fixed stride and keep gamma, beta and, in the backward, the
+// running sums of dgamma and dbeta of their channels in registers too; the teams' sums are then joined in a fixed order,
+// so results repeat bit for bit. Tokens of more channels than a workgroup's registers hold are read again for each step
+// (k_ln_wide, k_ln_wide_back, k_ln_columns).
+#include <type_traits>
+
+#include "feature_common.hpp"
+
+namespace gsr {
+namespace {
+
+struct LnShape {
+  uint32_t rows, tokens, channels;  // rows = batch * tokens
+  float eps;
+  FastDiv by_token;
+};
+
+// Statistics as the caller keeps them, aligned as float.
+struct LnStats {
+  float mean, rstd;
+};
+
+struct LnRows {
+  int64_t batch, token;  // strides in elements
+  __device__ __forceinline__ int64_t at(const LnShape& g, uint32_t row) const {
+    const uint32_t b = g.by_token.div(row);
+    return int64_t(b) * batch + int64_t(row - b * g.tokens) * token;
+  }
+};
+
+// Sum over a team of TEAM adjacent lanes (a power of two up to 64) or over the workgroup's TEAM threads, in a fixed
+// order; every lane of the team gets it. `s` holds TEAM / 64 floats where TEAM > 64; two sums in turn need two of them.
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float v, float* s) {
+#pragma unroll
+  for (int k = (TEAM < 64 ? TEAM : 64) / 2; k > 0; k >>= 1) v += __shfl_xor(v, k);
+  if constexpr (TEAM > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < TEAM / 64; ++k) v += s[k];
+  }
+  return v;
+}
+
+constexpr int threads_of(int team) { return team > 256 ? team : 256; }
+
+template <typename T>
+constexpr int kVec = 16 / int(sizeof(T));
+
+// A lane's K vectors of V channels: vector k is channels (k * TEAM + lane) * V ...
+template <typename T, int TEAM, int K>
+__global__ __launch_bounds__(threads_of(TEAM)) void k_ln(LnShape g, const T* x, LnRows xr,
+                                                         const float* __restrict__ gamma,
+                                                         const float* __restrict__ beta, T* y, LnRows yr,
+                                                         LnStats* __restrict__ stats) {
+  constexpr int V = kVec<T>, kThreads = threads_of(TEAM), kTeams = kThreads / TEAM;
+  __shared__ float s[2][TEAM > 64 ? TEAM / 64 : 1];
+  const uint32_t lane = threadIdx.x % TEAM, team = blockIdx.x * kTeams + threadIdx.x / TEAM;
+  const uint32_t stride = gridDim.x * kTeams;
+  const int C = int(g.channels);
+  const float n = float(C);
+  float gm[K][V], bt[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = int(k * TEAM + lane) * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      gm[k][i] = gamma && c + i < C ? gamma[c + i] : 1.0f;
+      bt[k][i] = beta && c + i < C ? beta[c + i] : 0.0f;
+    }
+  }
+  for (uint32_t row = team; row < g.rows; row += stride) {
+    const T* xp = x + xr.at(g, row);
+    float f[K][V], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) load_f32<V>(xp + (k * TEAM + lane) * V, C - int(k * TEAM + lane) * V, f[k]);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += f[k][i];
+    const float mean = team_sum<TEAM>(sum, s[0]) / n;
+    float sq = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        f[k][i] -= mean;
+        if (int(k * TEAM + lane) * V + i < C) sq = fmaf(f[k][i], f[k][i], sq);
+      }
+    const float rstd = 1.0f / sqrtf(team_sum<TEAM>(sq, s[1]) / n + g.eps);
+    T* yp = y + yr.at(g, row);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[k][i] = fmaf(f[k][i] * rstd, gm[k][i], bt[k][i]);
+      store_f32<V>(yp + (k * TEAM + lane) * V, C - int(k * TEAM + lane) * V, f[k]);
+    }
+    if (lane == 0) stats[row] = LnStats{mean, rstd};
+  }
+}
+
+// dx, and the team's sums of dy xh and dy over its tokens; the workgroup's teams are added through LDS, and `part` gets
+// [workgroup][2][channels].
+template <typename T, int TEAM, int K>
+__global__ __launch_bounds__(threads_of(TEAM)) void k_ln_back(LnShape g, const T* __restrict__ x, LnRows xr,
+                                                              const float* __restrict__ gamma,
+                                                              const LnStats* __restrict__ stats, const T* dy,
+                                                              LnRows dr, T* dx, LnRows or_,
+                                                              float* __restrict__ part) {
+  constexpr int V = kVec<T>, kThreads = threads_of(TEAM), kTeams = kThreads / TEAM;
+  __shared__ float s[2][TEAM > 64 ? TEAM / 64 : 1];
+  const uint32_t lane = threadIdx.x % TEAM, team = blockIdx.x * kTeams + threadIdx.x / TEAM;
+  const uint32_t stride = gridDim.x * kTeams;
+  const int C = int(g.channels);
+  const float n = float(C);
+  float gm[K][V], dg[K][V], db[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = int(k * TEAM + lane) * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      gm[k][i] = gamma && c + i < C ? gamma[c + i] : 1.0f;
+      dg[k][i] = db[k][i] = 0.0f;
+    }
+  }
+  for (uint32_t row = team; row < g.rows; row += stride) {
+    const T *xp = x + xr.at(g, row), *dp = dy + dr.at(g, row);
+    float f[K][V], d[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      load_f32<V>(xp + (k * TEAM + lane) * V, C - int(k * TEAM + lane) * V, f[k]);
+      load_f32<V>(dp + (k * TEAM + lane) * V, C - int(k * TEAM + lane) * V, d[k]);
+    }
+    const LnStats st = stats[row];
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        f[k][i] = (f[k][i] - st.mean) * st.rstd;
+        db[k][i] += d[k][i];
+        dg[k][i] = fmaf(d[k][i], f[k][i], dg[k][i]);
+        d[k][i] *= gm[k][i];
+        if (int(k * TEAM + lane) * V + i < C) {
+          a += d[k][i];
+          b = fmaf(d[k][i], f[k][i], b);
+        }
+      }
+    if (!dx) continue;
+    a = team_sum<TEAM>(a, s[0]) / n;
+    b = team_sum<TEAM>(b, s[1]) / n;
+    T* op = dx + or_.at(g, row);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[k][i] = st.rstd * (d[k][i] - a - f[k][i] * b);
+      store_f32<V>(op + (k * TEAM + lane) * V, C - int(k * TEAM + lane) * V, d[k]);
+    }
+  }
+  if (!part) return;
+  float* out = part + size_t(blockIdx.x) * 2 * g.channels;
+  if constexpr (kTeams > 1) {
+    __shared__ float sums[kThreads * V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      for (int which = 0; which < 2; ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) sums[i * kThreads + threadIdx.x] = which ? db[k][i] : dg[k][i];
+        __syncthreads();
+        for (int e = threadIdx.x; e < TEAM * V; e += kThreads) {
+          const int l = e / V, i = e % V, c = (k * TEAM + l) * V + i;
+          float t = 0.0f;
+#pragma unroll
+          for (int n = 0; n < kTeams; ++n) t += sums[i * kThreads + n * TEAM + l];
+          if (c < C) out[which * C + c] = t;
+        }
+      }
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = int(k * TEAM + lane) * V + i;
+        if (c < C) {
+          out[c] = dg[k][i];
+          out[C + c] = db[k][i];
+        }
+      }
+  }
+}
+
+// dgamma and dbeta: the parts added, a workgroup to 64 columns of [dgamma | dbeta], its 16 rows of threads each taking
+// every 16th part.
+__global__ __launch_bounds__(1024) void k_ln_join(uint32_t channels, uint32_t parts, const float* __restrict__ part,
+                                                  float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  __shared__ float s[16][64];
+  const uint32_t col = blockIdx.x * 64 + threadIdx.x % 64, row = threadIdx.x / 64, width = 2 * channels;
+  float t = 0.0f;
+  if (col < width) {
+#pragma unroll 8
+    for (uint32_t p = row; p < parts; p += 16) t += part[size_t(p) * width + col];
+  }
+  s[row][threadIdx.x % 64] = t;
+  __syncthreads();
+  if (row || col >= width) return;
+#pragma unroll
+  for (int k = 1; k < 16; ++k) t += s[k][threadIdx.x];
+  if (col < channels) {
+    if (dgamma) dgamma[col] = t;
+  } else if (dbeta) {
+    dbeta[col - channels] = t;
+  }
+}
+
+constexpr int kWide = 1024;  // threads of a workgroup that reads a token again for each step
+
+// f(channel, number of adjacent channels from it that exist (at most V)) over a token's channels.
+template <int V, typename F>
+__device__ __forceinline__ void for_channels(uint32_t channels, F f) {
+  for (uint32_t c = threadIdx.x * V; c < channels; c += kWide * V) f(c, int(channels - c));
+}
+
+template <typename T>
+__global__ __launch_bounds__(kWide) void k_ln_wide(LnShape g, const T* x, LnRows xr, const float* __restrict__ gamma,
+                                                   const float* __restrict__ beta, T* y, LnRows yr,
+                                                   LnStats* __restrict__ stats) {
+  constexpr int V = kVec<T>;
+  __shared__ float s[2][kWide / 64];
+  const float width = float(g.channels);
+  for (uint32_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
+    const T* xp = x + xr.at(g, row);
+    float sum = 0.0f, sq = 0.0f;
+    for_channels<V>(g.channels, [&](uint32_t c, int n) {
+      float f[V];
+      load_f32<V>(xp + c, n, f);
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += f[i];
+    });
+    const float mean = team_sum<kWide>(sum, s[0]) / width;
+    for_channels<V>(g.channels, [&](uint32_t c, int n) {
+      float f[V];
+      load_f32<V>(xp + c, n, f);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) sq = fmaf(f[i] - mean, f[i] - mean, sq);
+    });
+    const float rstd = 1.0f / sqrtf(team_sum<kWide>(sq, s[1]) / width + g.eps);
+    T* yp = y + yr.at(g, row);
+    for_channels<V>(g.channels, [&](uint32_t c, int n) {
+      float f[V];
+      load_f32<V>(xp + c, n, f);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) f[i] = fmaf((f[i] - mean) * rstd, gamma ? gamma[c + i] : 1.0f, beta ? beta[c + i] : 0.0f);
+      store_f32<V>(yp + c, n, f);
+    });
+    if (threadIdx.x == 0) stats[row] = LnStats{mean, rstd};
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kWide) void k_ln_wide_back(LnShape g, const T* __restrict__ x, LnRows xr,
+                                                        const float* __restrict__ gamma,
+                                                        const LnStats* __restrict__ stats, const T* dy, LnRows dr,
+                                                        T* dx, LnRows or_) {
+  constexpr int V = kVec<T>;
+  __shared__ float s[2][kWide / 64];
+  const float width = float(g.channels);
+  for (uint32_t row = blockIdx.x; row < g.rows; row += gridDim.x) {
+    const T *xp = x + xr.at(g, row), *dp = dy + dr.at(g, row);
+    const LnStats st = stats[row];
+    float a = 0.0f, b = 0.0f;
+    // xh and dh of the token's channels from c on
+    auto take = [&](uint32_t c, int n, float* f, float* d) {
+      load_f32<V>(xp + c, n, f);
+      load_f32<V>(dp + c, n, d);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) {
+          f[i] = (f[i] - st.mean) * st.rstd;
+          d[i] *= gamma ? gamma[c + i] : 1.0f;
+        }
+    };
+    for_channels<V>(g.channels, [&](uint32_t c, int n) {
+      float f[V], d[V];
+      take(c, n, f, d);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) {
+          a += d[i];
+          b = fmaf(d[i], f[i], b);
+        }
+    });
+    a = team_sum<kWide>(a, s[0]) / width;
+    b = team_sum<kWide>(b, s[1]) / width;
+    T* op = dx + or_.at(g, row);
+    for_channels<V>(g.channels, [&](uint32_t c, int n) {
+      float f[V], d[V];
+      take(c, n, f, d);
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = st.rstd * (d[i] - a - f[i] * b);
+      store_f32<V>(op + c, n, d);
+    });
+  }
+}
+
+// The sums of dy xh and dy over every gridDim.y-th token from blockIdx.y on, of V adjacent channels a thread; `part` as
+// k_ln_back leaves it.
+template <typename T>
+__global__ __launch_bounds__(256) void k_ln_columns(LnShape g, const T* __restrict__ x, LnRows xr,
+                                                    const LnStats* __restrict__ stats, const T* __restrict__ dy,
+                                                    LnRows dr, float* __restrict__ part) {
+  constexpr int V = kVec<T>;
+  const uint32_t c = (blockIdx.x * 256 + threadIdx.x) * V;
+  if (c >= g.channels) return;
+  const int n = int(g.channels - c);
+  float dg[V], db[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) dg[i] = db[i] = 0.0f;
+#pragma unroll 2
+  for (uint32_t row = blockIdx.y; row < g.rows; row += gridDim.y) {
+    float f[V], d[V];
+    load_f32<V>(x + xr.at(g, row) + c, n, f);
+    load_f32<V>(dy + dr.at(g, row) + c, n, d);
+    const LnStats st = stats[row];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dg[i] = fmaf(d[i], (f[i] - st.mean) * st.rstd, dg[i]);
+      db[i] += d[i];
+    }
+  }
+  float* out = part + size_t(blockIdx.y) * 2 * g.channels + c;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < n) {
+      out[i] = dg[i];
+      out[g.channels + i] = db[i];
+    }
+}
+
+// dgamma and dbeta when no token is there to sum.
+__global__ void k_ln_zero(float* a, float* b, uint32_t n) {
+  const uint32_t i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  if (a) a[i] = 0.0f;
+  if (b) b[i] = 0.0f;
+}
+
+gsr_status check_desc(gsr_ctx* ctx, const gsr_layer_norm* d, const char* who) {
+  if (!d) return fail(ctx, GSR_EINVAL, "%s: null descriptor", who);
+  if (d->dtype > GSR_BF16) return fail(ctx, GSR_EINVAL, "%s: unknown dtype %u", who, d->dtype);
+  if (!(d->eps >= 0.0f) || std::isinf(d->eps)) return fail(ctx, GSR_EINVAL, "%s: eps must be finite and >= 0", who);
+  if (uint64_t(d->batch) * d->tokens >= (uint64_t(1) << 31))
+    return fail(ctx, GSR_EOVERFLOW, "%s: batch * tokens >= 2^31", who);
+  if (d->channels >= (1u << 20)) return fail(ctx, GSR_EOVERFLOW, "%s: channels >= 2^20", who);
+  return GSR_OK;
+}
+
+gsr_status check_out(gsr_ctx* ctx, const gsr_layer_norm* d, const int64_t* st, const char* who, const char* name) {
+  if (!distinct({{st[0], d->batch}, {st[1], d->tokens}}, d->channels))
+    return fail(ctx, GSR_EINVAL, "%s: the strides of %s overlap", who, name);
+  return GSR_OK;
+}
+
+LnShape shape_of(const gsr_layer_norm* d) {
+  LnShape g{};
+  g.rows = d->batch * d->tokens;
+  g.tokens = d->tokens;
+  g.channels = d->channels;
+  g.eps = d->eps;
+  g.by_token.set(d->tokens);
+  return g;
+}
+
+// Calls f(element type, team, vectors) with compile-time values for the smallest team that holds a token, or
+// wide(element type).
+template <typename F, typename W>
+void by_kind(const gsr_layer_norm* d, F f, W wide) {
+  auto shaped = [&](auto t) {
+    using T = decltype(t);
+    const uint32_t vecs = (d->channels + kVec<T> - 1) / kVec<T>;
+    auto take = [&](auto team, auto k) { f(t, team, k); };
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    using I4 = std::integral_constant<int, 4>;
+    using Wave = std::integral_constant<int, 64>;
+    if (vecs <= 8)
+      take(std::integral_constant<int, 8>(), I1());
+    else if (vecs <= 16)
+      take(std::integral_constant<int, 16>(), I1());
+    else if (vecs <= 32)
+      take(std::integral_constant<int, 32>(), I1());
+    else if (vecs <= 64)
+      take(Wave(), I1());
+    else if (vecs <= 128)
+      take(Wave(), I2());
+    else if (vecs <= 192)
+      take(Wave(), I3());
+    else if (vecs <= 256)
+      take(Wave(), I4());
+    else if (vecs <= 512)
+      take(std::integral_constant<int, 256>(), I2());
+    else if (vecs <= 1024)
+      take(std::integral_constant<int, 256>(), I4());
+    else if (vecs <= 2048)
+      take(std::integral_constant<int, 1024>(), I2());
+    else
+      wide(t);
+  };
+  if (d->dtype == GSR_F32)
+    shaped(float());
+  else if (d->dtype == GSR_F16)
+    shaped(_Float16());
+  else
+    shaped(__bf16());
+}
+
+}  // namespace
+}  // namespace gsr
+
+using namespace gsr;
+
+extern "C" gsr_status gsr_layer_norm_forward(gsr_ctx* ctx, void* stream, const gsr_layer_norm* d, const void* x,
+                                             const float* gamma, const float* beta, void* y, float* stats) {
+  static const char* who = "gsr_layer_norm_forward";
+  if (!ctx) return GSR_EINVAL;
+  gsr_status st = check_desc(ctx, d, who);
+  if (st) return st;
+  if (!d->batch || !d->tokens || !d->channels) return GSR_OK;
+  if (!x || !y || !stats) return fail(ctx, GSR_EINVAL, "%s: null pointer", who);
+  const size_t eb = elem_bytes(d->dtype);
+  if (misaligned(x, eb) || misaligned(y, eb) || misaligned(gamma, 4) || misaligned(beta, 4) || misaligned(stats, 4))
+    return fail(ctx, GSR_EINVAL, "%s: a pointer is not aligned to its element", who);
+  if ((st = check_out(ctx, d, d->y_stride, who, "y"))) return st;
+  if ((st = enter(ctx))) return st;
+  const LnShape g = shape_of(d);
+  const LnRows xr{d->x_stride[0], d->x_stride[1]}, yr{d->y_stride[0], d->y_stride[1]};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  LnStats* out = reinterpret_cast<LnStats*>(stats);
+  timing_mark(ctx, GSR_STAGE_LAYER_NORM_FORWARD, s, false);
+  by_kind(
+      d,
+      [&](auto t, auto team, auto k) {
+        using T = decltype(t);
+        constexpr int kTeam = decltype(team)::value, kT = threads_of(kTeam), kTeams = kT / kTeam;
+        const uint32_t blocks = std::min<uint32_t>((g.rows + kTeams - 1) / kTeams, 2048);
+        hipLaunchKernelGGL((k_ln<T, kTeam, decltype(k)::value>), dim3(blocks), dim3(kT), 0, s, g,
+                           static_cast<const T*>(x), xr, gamma, beta, static_cast<T*>(y), yr, out);
+      },
+      [&](auto t) {
+        using T = decltype(t);
+        hipLaunchKernelGGL((k_ln_wide<T>), dim3(std::min<uint32_t>(g.rows, 512)), dim3(kWide), 0, s, g,
+                           static_cast<const T*>(x), xr, gamma, beta, static_cast<T*>(y), yr, out);
+      });
+  timing_mark(ctx, GSR_STAGE_LAYER_NORM_FORWARD, s, true);
+  return check_launch(ctx, who);
+}
+
+extern "C" gsr_status gsr_layer_norm_backward(gsr_ctx* ctx, void* stream, const gsr_layer_norm* d, const void* x,
+                                              const float* gamma, const float* stats, const void* dy, void* dx,
+                                              float* dgamma, float* dbeta) {
+  static const char* who = "gsr_layer_norm_backward";
+  if (!ctx) return GSR_EINVAL;
+  gsr_status st = check_desc(ctx, d, who);
+  if (st) return st;
+  if (!d->channels || (!dx && !dgamma && !dbeta)) return GSR_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (misaligned(dgamma, 4) || misaligned(dbeta, 4) || misaligned(gamma, 4))
+    return fail(ctx, GSR_EINVAL, "%s: a pointer is not aligned to its element", who);
+  if (!d->batch || !d->tokens) {
+    if (!dgamma && !dbeta) return GSR_OK;
+    if ((st = enter(ctx))) return st;
+    hipLaunchKernelGGL(k_ln_zero, dim3((d->channels + 255) / 256), dim3(256), 0, s, dgamma, dbeta, d->channels);
+    return check_launch(ctx, who);
+  }
+  if (!x || !stats || !dy) return fail(ctx, GSR_EINVAL, "%s: null pointer", who);
+  const size_t eb = elem_bytes(d->dtype);
+  if (misaligned(x, eb) || misaligned(dy, eb) || misaligned(dx, eb) || misaligned(stats, 4))
+    return fail(ctx, GSR_EINVAL, "%s: a pointer is not aligned to its element", who);
+  if (dx && (st = check_out(ctx, d, d->dx_stride, who, "dx"))) return st;
+  if ((st = enter(ctx))) return st;
+  const LnShape g = shape_of(d);
+  const LnRows xr{d->x_stride[0], d->x_stride[1]}, dr{d->dy_stride[0], d->dy_stride[1]};
+  const LnRows outr{d->dx_stride[0], d->dx_stride[1]};
+  const LnStats* in = reinterpret_cast<const LnStats*>(stats);
+  const bool sums = dgamma || dbeta;
+  // the teams' workgroups, or the rows of workgroups of the column sums; each leaves one part
+  uint32_t parts = 0;
+  by_kind(
+      d,
+      [&](auto, auto team, auto) {
+        constexpr int kTeam = decltype(team)::value, kTeams = threads_of(kTeam) / kTeam;
+        parts = std::min<uint32_t>((g.rows + kTeams - 1) / kTeams, 512);
+      },
+      [&](auto) { parts = std::min<uint32_t>(g.rows, 64); });
+  if (sums && (st = grow(ctx, ctx->arena.feat_part, size_t(parts) * 2 * g.channels * sizeof(float)))) return st;
+  float* part = sums ? static_cast<float*>(ctx->arena.feat_part.ptr) : nullptr;
+  timing_mark(ctx, GSR_STAGE_LAYER_NORM_BACKWARD, s, false);
+  by_kind(
+      d,
+      [&](auto t, auto team, auto k) {
+        using T = decltype(t);
+        constexpr int kTeam = decltype(team)::value;
+        hipLaunchKernelGGL((k_ln_back<T, kTeam, decltype(k)::value>), dim3(parts), dim3(threads_of(kTeam)), 0, s, g,
+                           static_cast<const T*>(x), xr, gamma, in, static_cast<const T*>(dy), dr, static_cast<T*>(dx),
+                           outr, part);
+      },
+      [&](auto t) {
+        using T = decltype(t);
+        const T *xt = static_cast<const T*>(x), *dt = static_cast<const T*>(dy);
+        if (sums)
+          hipLaunchKernelGGL((k_ln_columns<T>), dim3((g.channels + 256 * kVec<T> - 1) / (256 * kVec<T>), parts),
+                             dim3(256), 0, s, g, xt, xr, in, dt, dr, part);
+        if (dx)
+          hipLaunchKernelGGL((k_ln_wide_back<T>), dim3(std::min<uint32_t>(g.rows, 512)), dim3(kWide), 0, s, g, xt, xr,
+                             gamma, in, dt, dr, static_cast<T*>(dx), outr);
+      });
+  if (sums)
+    hipLaunchKernelGGL(k_ln_join, dim3((2 * g.channels + 63) / 64), dim3(1024), 0, s, g.channels, parts, part, dgamma,
+                       dbeta);
+  timing_mark(ctx, GSR_STAGE_LAYER_NORM_BACKWARD, s, true);
+  return check_launch(ctx, who);
+}

@@ -32,12 +32,14 @@ GSR_OPT_FORWARD_EXP, GSR_EXP_EXACT, GSR_EXP_FAST = 11, 0, 1
  GSR_STAGE_PROJECT_BACKWARD, GSR_STAGE_LOSS, GSR_STAGE_DEPTH_SORT, GSR_STAGE_TILE_SORT, GSR_STAGE_TILE_DEPTH,
  GSR_STAGE_TILE_SCAN) = range(11)
 (GSR_STAGE_GROUP_NORM_FORWARD, GSR_STAGE_GROUP_NORM_BACKWARD, GSR_STAGE_ROTARY, GSR_STAGE_ATTENTION_FORWARD,
- GSR_STAGE_ATTENTION_BACKWARD) = range(12, 17)
+ GSR_STAGE_ATTENTION_BACKWARD, GSR_STAGE_LAYER_NORM_FORWARD, GSR_STAGE_LAYER_NORM_BACKWARD, GSR_STAGE_ORTHOGONALIZE,
+ GSR_STAGE_MUON) = range(12, 21)
 GSR_ADAM_MAX_GROUPS = 8
 GSR_F32, GSR_F16, GSR_BF16 = 0, 1, 2
 GSR_ACT_NONE, GSR_ACT_SILU, GSR_ACT_RELU = 0, 1, 2
 GSR_ROTARY_INTERLEAVED, GSR_ROTARY_HALVES, GSR_ROTARY_MAX_AXES, GSR_ROTARY_MAX_PAIRS = 0, 1, 4, 128
 GSR_ATTENTION_MAX_DIM = 128
+GSR_ORTHOGONALIZE_MAX_STEPS = 8
 _STATUS = {GSR_EINVAL: "GSR_EINVAL", GSR_ENOMEM: "GSR_ENOMEM", GSR_EHIP: "GSR_EHIP", GSR_EOVERFLOW: "GSR_EOVERFLOW"}
 
 
@@ -88,6 +90,20 @@ class gsr_attention(ctypes.Structure):
                 ("dv_stride", ctypes.c_int64 * 3)]
 
 
+class gsr_layer_norm(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_uint32), ("batch", ctypes.c_uint32), ("tokens", ctypes.c_uint32),
+                ("channels", ctypes.c_uint32), ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64 * 2),
+                ("y_stride", ctypes.c_int64 * 2), ("dy_stride", ctypes.c_int64 * 2), ("dx_stride", ctypes.c_int64 * 2)]
+
+
+class gsr_newton_schulz(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_uint32), ("batch", ctypes.c_uint32), ("rows", ctypes.c_uint32),
+                ("cols", ctypes.c_uint32), ("steps", ctypes.c_uint32), ("eps", ctypes.c_float),
+                ("coefficients", (ctypes.c_float * 3) * GSR_ORTHOGONALIZE_MAX_STEPS),
+                ("grad_stride", ctypes.c_int64 * 2), ("out_stride", ctypes.c_int64 * 2),
+                ("momentum_stride", ctypes.c_int64 * 2)]
+
+
 def camera(R, tv, fx: float, fy: float, cx: float, cy: float, near: float = 0.01) -> gsr_camera:
     """A gsr_camera from a 3x3 world-to-camera rotation R (any nested sequence or array), a translation tv and the
     pinhole intrinsics."""
@@ -126,6 +142,10 @@ SIGNATURES = {
     "gsr_rotary_backward": (_I32, [_P, _P, ctypes.POINTER(gsr_rotary), _P, _P, _P]),
     "gsr_cross_attention_forward": (_I32, [_P, _P, ctypes.POINTER(gsr_attention)] + [_P] * 7),
     "gsr_cross_attention_backward": (_I32, [_P, _P, ctypes.POINTER(gsr_attention)] + [_P] * 11),
+    "gsr_layer_norm_forward": (_I32, [_P, _P, ctypes.POINTER(gsr_layer_norm)] + [_P] * 5),
+    "gsr_layer_norm_backward": (_I32, [_P, _P, ctypes.POINTER(gsr_layer_norm)] + [_P] * 7),
+    "gsr_orthogonalize": (_I32, [_P, _P, ctypes.POINTER(gsr_newton_schulz), _P, _P]),
+    "gsr_muon_step": (_I32, [_P, _P, ctypes.POINTER(gsr_newton_schulz), _P, _P, _P, _F, _F, _I32, _F]),
 }
 
 _lib = None
@@ -706,3 +726,122 @@ def gsr_cross_attention_backward(ctx: Context, q: torch.Tensor, k: torch.Tensor,
                                                   _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk), _ptr(dv)),
               "gsr_cross_attention_backward")
     return dq, dk, dv
+
+
+def _layer_norm_desc(ctx, x, gamma, beta, eps):
+    dev = ctx.device
+    _need_feature(x, "x", dev)
+    if x.dim() < 2:
+        raise ValueError("x must be [batch, ..., channels]")
+    C = x.shape[-1]
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _need(t, name, (torch.float32,), C, dev)
+    tokens = 1
+    for n in x.shape[1:-1]:
+        tokens *= n
+    _fit("batch, tokens, channels", x.shape[0] | tokens | C)
+    d = gsr_layer_norm(_DTYPES[x.dtype], x.shape[0], tokens, C, eps)
+    d.x_stride[:] = _image_strides(x, "x")
+    return d
+
+
+def gsr_layer_norm_forward(ctx: Context, x: torch.Tensor, gamma: torch.Tensor | None = None,
+                           beta: torch.Tensor | None = None, eps: float = 1e-5, y: torch.Tensor | None = None,
+                           stats: torch.Tensor | None = None, stream=None):
+    """Layer norm over the last dimension of x [B, ..., C] (float32, float16 or bfloat16; gamma and beta float32 [C] or
+    None). `y` may be x. Returns (y like x, stats float32 [B, ..., 2] = (mean, rstd))."""
+    d = _layer_norm_desc(ctx, x, gamma, beta, eps)
+    if y is None:
+        y = _like(x)
+    if stats is None:
+        stats = torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=x.device)
+    _need_feature(y, "y", ctx.device, x.dtype, x.shape)
+    _need(stats, "stats", (torch.float32,), d.batch * d.tokens * 2, ctx.device)
+    d.y_stride[:] = _image_strides(y, "y")
+    ctx.check(load().gsr_layer_norm_forward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(x),
+                                            _ptr(gamma), _ptr(beta), _ptr(y), _ptr(stats)), "gsr_layer_norm_forward")
+    return y, stats
+
+
+def gsr_layer_norm_backward(ctx: Context, x: torch.Tensor, gamma: torch.Tensor | None, stats: torch.Tensor,
+                            dy: torch.Tensor, dx: torch.Tensor | None = None, dgamma: torch.Tensor | None = None,
+                            dbeta: torch.Tensor | None = None, stream=None):
+    """Returns (dx like x, dgamma float32 [C], dbeta float32 [C]) for the upstream gradient dy (like x); `dx` may be
+    dy."""
+    d = _layer_norm_desc(ctx, x, gamma, None, 0.0)
+    dev, C = ctx.device, x.shape[-1]
+    _need(stats, "stats", (torch.float32,), d.batch * d.tokens * 2, dev)
+    _need_feature(dy, "dy", dev, x.dtype, x.shape)
+    if dx is None:
+        dx = _like(x)
+    if dgamma is None:
+        dgamma = torch.empty(C, dtype=torch.float32, device=dev)
+    if dbeta is None:
+        dbeta = torch.empty(C, dtype=torch.float32, device=dev)
+    _need_feature(dx, "dx", dev, x.dtype, x.shape)
+    _need(dgamma, "dgamma", (torch.float32,), C, dev)
+    _need(dbeta, "dbeta", (torch.float32,), C, dev)
+    d.dy_stride[:] = _image_strides(dy, "dy")
+    d.dx_stride[:] = _image_strides(dx, "dx")
+    ctx.check(load().gsr_layer_norm_backward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(x),
+                                             _ptr(gamma), _ptr(stats), _ptr(dy), _ptr(dx), _ptr(dgamma),
+                                             _ptr(dbeta)), "gsr_layer_norm_backward")
+    return dx, dgamma, dbeta
+
+
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)  # singular values of 0.003 and more to 0.7 .. 1.2 in five steps
+
+
+def _newton_schulz_desc(ctx, g, name, steps, coefficients, eps):
+    _need_feature(g, name, ctx.device)
+    if g.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [rows, cols] or [batch, rows, cols]")
+    if not 1 <= steps <= GSR_ORTHOGONALIZE_MAX_STEPS:
+        raise ValueError(f"1 to {GSR_ORTHOGONALIZE_MAX_STEPS} steps are supported, got {steps}")
+    table = tuple(coefficients)
+    if not isinstance(table[0], (tuple, list)):
+        table = (table,) * steps
+    if len(table) != steps or any(len(c) != 3 for c in table):
+        raise ValueError("coefficients must be (a, b, c), or one such triple for each step")
+    batch = g.shape[0] if g.dim() == 3 else 1
+    _fit("batch, rows, cols", batch | g.shape[-2] | g.shape[-1])
+    d = gsr_newton_schulz(_DTYPES[g.dtype], batch, g.shape[-2], g.shape[-1], steps, eps)
+    for k, c in enumerate(table):
+        d.coefficients[k][:] = c
+    d.grad_stride[:] = _matrix_strides(g)
+    return d
+
+
+def _matrix_strides(t):
+    """(matrix, row) strides of [rows, cols] or [batch, rows, cols]."""
+    return (t.stride(0) if t.dim() == 3 else 0), t.stride(-2)
+
+
+def gsr_orthogonalize(ctx: Context, g: torch.Tensor, steps: int = 5, coefficients=NEWTON_SCHULZ, eps: float = 1e-7,
+                      out: torch.Tensor | None = None, stream=None):
+    """Moves the singular values of g [rows, cols] or [batch, rows, cols] (float32, float16 or bfloat16) near 1 by
+    `steps` Newton-Schulz steps X <- a X + (b A + c A^2) X, A = X X^T, from X = g / (|g| + eps). `coefficients` is
+    (a, b, c) or one triple for each step. `out` may be g. Returns out, like g."""
+    d = _newton_schulz_desc(ctx, g, "g", steps, coefficients, eps)
+    if out is None:
+        out = _like(g)
+    _need_feature(out, "out", ctx.device, g.dtype, g.shape)
+    d.out_stride[:] = _matrix_strides(out)
+    ctx.check(load().gsr_orthogonalize(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(g), _ptr(out)),
+              "gsr_orthogonalize")
+    return out
+
+
+def gsr_muon_step(ctx: Context, param: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, lr: float,
+                  mu: float = 0.95, nesterov: bool = True, decay: float = 1.0, steps: int = 5,
+                  coefficients=NEWTON_SCHULZ, eps: float = 1e-7, stream=None):
+    """One step by orthogonalised momentum, in place: m = mu m + g; u = g + mu m or m; param = decay param - lr O(u).
+    param and momentum float32, grad float32, float16 or bfloat16, all [rows, cols] or [batch, rows, cols]."""
+    d = _newton_schulz_desc(ctx, grad, "grad", steps, coefficients, eps)
+    _need_feature(param, "param", ctx.device, torch.float32, grad.shape)
+    _need_feature(momentum, "momentum", ctx.device, torch.float32, grad.shape)
+    d.out_stride[:] = _matrix_strides(param)
+    d.momentum_stride[:] = _matrix_strides(momentum)
+    ctx.check(load().gsr_muon_step(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(grad), _ptr(param),
+                                   _ptr(momentum), lr, mu, int(bool(nesterov)), decay), "gsr_muon_step")

@@ -9,8 +9,10 @@
  * and, on either side of it, the projection of 3D Gaussians to those splats and the projection's backward pass
  * (gsr_project_forward / gsr_project_backward), and the L1 + SSIM loss that gives the backward its v_out
  * (gsr_loss_l1_ssim). For models that predict splats from images, in front of the projection: group norm with an
- * activation over channels-last feature maps (gsr_group_norm_*), rotary positions with several axes (gsr_rotary_*)
- * and cross attention from splat queries to image tokens (gsr_cross_attention_*), each with its backward pass.
+ * activation over channels-last feature maps (gsr_group_norm_*), layer norm over tokens (gsr_layer_norm_*), rotary
+ * positions with several axes (gsr_rotary_*) and cross attention from splat queries to image tokens
+ * (gsr_cross_attention_*), each with its backward pass, and for their weight matrices an optimiser step by
+ * orthogonalised updates (gsr_muon_step, gsr_orthogonalize).
  *
  * Conventions shared by every entry point
  *   - Pointers named as device pointers must point to memory allocated on the context's device (hipMalloc or a
@@ -156,7 +158,11 @@ gsr_status gsr_set_option(gsr_ctx* ctx, int32_t option, int64_t value);
 #define GSR_STAGE_ROTARY 14              /* the rotary kernel, either direction                                  */
 #define GSR_STAGE_ATTENTION_FORWARD 15   /* the kernels of gsr_cross_attention_forward                           */
 #define GSR_STAGE_ATTENTION_BACKWARD 16  /* the kernels of gsr_cross_attention_backward                          */
-#define GSR_NUM_STAGES 17 /* 11 is no stage: it stays an error of gsr_kernel_times                               */
+#define GSR_STAGE_LAYER_NORM_FORWARD 17  /* the kernels of gsr_layer_norm_forward                                */
+#define GSR_STAGE_LAYER_NORM_BACKWARD 18 /* the kernels of gsr_layer_norm_backward                               */
+#define GSR_STAGE_ORTHOGONALIZE 19       /* the kernels of gsr_orthogonalize                                     */
+#define GSR_STAGE_MUON 20                /* the kernels of gsr_muon_step                                         */
+#define GSR_NUM_STAGES 21 /* 11 is no stage: it stays an error of gsr_kernel_times                               */
 
 /* GPU durations in milliseconds of the recorded launches of `stage`, oldest first: the last min(recorded, ring
  * size, max) of them. Waits for the newest one to finish. *count = the number written.
@@ -508,6 +514,78 @@ gsr_status gsr_cross_attention_backward(gsr_ctx* ctx, void* stream, const gsr_at
                                         const void* k, const void* v, const int32_t* kv_lengths,
                                         const uint8_t* mask, const void* o, const float* lse, const void* dout,
                                         void* dq, void* dk, void* dv);
+
+/* Layer norm over the channels of each token x[batch entry][token][channel]: with mean and var the mean and the (biased)
+ * variance of a token's channels,
+ *   rstd = 1 / sqrt(var + eps);  y = (x - mean) rstd gamma[channel] + beta[channel].
+ * Strides are those of a batch entry and of a token (0 broadcasts an input); channels are adjacent. */
+typedef struct gsr_layer_norm {
+  uint32_t dtype;                   /* x, y, dy, dx. gamma, beta and their gradients are float32                  */
+  uint32_t batch, tokens, channels; /* any may be 0                                                               */
+  float eps;                        /* >= 0                                                                       */
+  int64_t x_stride[2], y_stride[2];   /* (batch entry, token)                                                     */
+  int64_t dy_stride[2], dx_stride[2]; /* read by the backward only                                                */
+} gsr_layer_norm;
+
+/*   gamma, beta  device [channels] float32, either may be NULL (1 and 0)
+ *   y            written; may be x itself (same strides)
+ *   stats        device [batch][tokens][2] float32, written: (mean, rstd), for the backward
+ * The variance is taken about the mean (no difference of squares). A token's infinities and NaN stay in that token.
+ * Errors: GSR_EINVAL (null pointers, unknown dtype, eps < 0 or not finite, output strides that overlap, pointers not
+ * aligned to their element), GSR_EOVERFLOW (batch * tokens >= 2^31 or channels >= 2^20), GSR_EHIP. */
+gsr_status gsr_layer_norm_forward(gsr_ctx* ctx, void* stream, const gsr_layer_norm* desc, const void* x,
+                                  const float* gamma, const float* beta, void* y, float* stats);
+
+/* Backward pass: with xh = (x - mean) rstd and dh = dy gamma, dgamma = sum dy xh and dbeta = sum dy (over all tokens),
+ * and over a token's channels
+ *   dx = rstd (dh - (mean of dh) - xh (mean of dh xh)).
+ *   stats   as written by the forward;  dy as y
+ *   dx      written, or NULL to skip it; may be dy itself (same strides)
+ *   dgamma, dbeta  device [channels] float32, overwritten (zeros where there are no tokens), either may be NULL
+ * eps is not read. Uses the context arena as scratch for dgamma and dbeta. Errors: as gsr_layer_norm_forward, and
+ * GSR_ENOMEM. */
+gsr_status gsr_layer_norm_backward(gsr_ctx* ctx, void* stream, const gsr_layer_norm* desc, const void* x,
+                                   const float* gamma, const float* stats, const void* dy, void* dx, float* dgamma,
+                                   float* dbeta);
+
+#define GSR_ORTHOGONALIZE_MAX_STEPS 8
+
+/* A stack of matrices [batch][rows][cols] whose singular vectors are kept while their singular values are moved near 1
+ * by Newton-Schulz steps: X_0 = G / (|G| + eps), |G| the Frobenius norm of the matrix, and with A = X X^T
+ *   X <- a X + (b A + c A^2) X     (each singular value s becomes s (a + b s^2 + c s^4)).
+ * A matrix of zeros stays one (eps = 0 too); one that holds an infinity or NaN becomes NaN throughout. Strides are those
+ * of a matrix and of a row; a row's elements are adjacent. */
+typedef struct gsr_newton_schulz {
+  uint32_t dtype; /* of the matrices in (and out, of gsr_orthogonalize)                                           */
+  uint32_t batch, rows, cols; /* any may be 0                                                                     */
+  uint32_t steps;             /* 1 .. GSR_ORTHOGONALIZE_MAX_STEPS                                                 */
+  float eps;                  /* >= 0                                                                             */
+  float coefficients[GSR_ORTHOGONALIZE_MAX_STEPS][3]; /* (a, b, c) of each step; 3.4445, -4.7750, 2.0315 brings   */
+                                                      /* singular values of 0.003 and more to 0.7 .. 1.2 in five. */
+                                                      /* They must keep singular values of at most 1 below 8      */
+  int64_t grad_stride[2];     /* (matrix, row) of g or grad; 0 broadcasts                                         */
+  int64_t out_stride[2];      /* of out or param                                                                  */
+  int64_t momentum_stride[2]; /* read by gsr_muon_step only                                                       */
+} gsr_newton_schulz;
+
+/*   g    the matrices;  out  written, of g's type; may be g itself (same strides)
+ * float32 and float16 results have the accuracy of a float32 evaluation, rounded once at the end; bfloat16 results are
+ * within 2^-9 of their norm before their own rounding. Uses the context arena as scratch (8 bytes an element, padded to
+ * whole tiles, and 8 an element of two squares of the shorter side).
+ * Errors: GSR_EINVAL (null pointers, unknown dtype, steps, eps or coefficients out of range, output strides that
+ * overlap, pointers not aligned to their element), GSR_EOVERFLOW (batch >= 2^16, rows or cols >= 2^20, rows * cols >=
+ * 2^31), GSR_ENOMEM, GSR_EHIP. */
+gsr_status gsr_orthogonalize(gsr_ctx* ctx, void* stream, const gsr_newton_schulz* desc, const void* g, void* out);
+
+/* One optimiser step by orthogonalised momentum, for each matrix:
+ *   m = mu m + g;  u = g + mu m (nesterov not 0) or m;  param = decay param - lr O(u),
+ * O the orthogonalisation above, with the accuracy of a float32 evaluation whatever grad's type. The caller supplies lr
+ * with any factor for the matrix's shape, and decay = 1 - lr * (weight decay).
+ *   grad      device, of desc->dtype
+ *   param, momentum  device float32, updated; they, and grad, must not overlap each other
+ * Errors: as gsr_orthogonalize, and GSR_EINVAL for lr, mu or decay that are not finite. */
+gsr_status gsr_muon_step(gsr_ctx* ctx, void* stream, const gsr_newton_schulz* desc, const void* grad, float* param,
+                         float* momentum, float lr, float mu, int32_t nesterov, float decay);
 
 #ifdef __cplusplus
 }

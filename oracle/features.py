@@ -1,5 +1,5 @@
-"""Plain fp64 evaluation of the feature operators (group norm with an activation, rotary positions, cross attention),
-their gradients by the written formulas, and the error bounds their float kernels are held to.
+"""Plain fp64 evaluation of the feature operators (group norm with an activation, layer norm, rotary positions, cross
+attention, orthogonalised matrix updates), their gradients by the written formulas, and the error bounds their float kernels are held to.
 
 Everything runs on CPU torch tensors in float64 and shares no code with the library. tests/test_oracle_features.py
 checks the gradients against automatic differentiation and central differences of the forward definitions.
@@ -149,3 +149,79 @@ def attention(q, k, v, scale, dtype, lengths=None, mask=None, do=None):
         for name in ("dq", "dk", "dv"):
             out["e_" + name] = out["e_" + name] + TINY[dtype]
     return out
+
+
+def layer_norm(x, gamma, beta, eps, dy=None):
+    """x [R, C] float64. As group_norm's dict (mean and rstd [R]): every token is an image of one pixel and one group."""
+    wide = lambda t: None if t is None else t[:, None]  # noqa: E731
+    out = group_norm(x[:, None], gamma, beta, 1, eps, "none", wide(dy))
+    for name in ("y", "e_y", "dx", "e_dx"):
+        if name in out:
+            out[name] = out[name][:, 0]
+    for name in ("mean", "rstd", "e_mean", "e_rstd"):
+        out[name] = out[name][:, 0]
+    return out
+
+
+def newton_schulz(g, steps, eps=0.0, dtype=torch.float64):
+    """X = g / (|g| + eps) and X <- a X + (b A + c A^2) X, A = X X^T, for each (a, b, c) of `steps`, in dtype; g [m, n]."""
+    x = g.to(dtype)
+    tall = x.shape[0] > x.shape[1]
+    x = x.T.contiguous() if tall else x
+    norm = x.double().square().sum().sqrt() + eps
+    x = x * (1 / norm).to(dtype) if norm > 0 else x * 0
+    for a, b, c in steps:
+        gram = x @ x.T
+        x = a * x + (b * gram + c * (gram @ gram)) @ x
+    return x.T if tall else x
+
+
+def newton_schulz_svd(g, steps, eps=0.0):
+    """The same by its meaning: the scalar steps applied to the singular values."""
+    u, s, vh = torch.linalg.svd(g.double(), full_matrices=False)
+    s = s / (s.square().sum().sqrt() + eps)
+    for a, b, c in steps:
+        s = s * (a + b * s ** 2 + c * s ** 4)
+    return (u * s) @ vh
+
+
+def newton_schulz_error(g, steps, u, from_hi):
+    """The size expected of |X^ - X|_F, to first order, where X is the exact result for g [m, n] and X^ one whose left
+    factors A and P are rounded to a half step of u (relative) and whose X is not (A taken from a rounded X where
+    from_hi). Roundings are taken as independent, their size that of values spread evenly between steps: u |x| / sqrt(3)
+    at most.
+
+    Let X = U S V^T before a step, s' its singular values after, and f the remaining steps' scalar map. An error D of
+    P = b A + c A^2 moves the result of the step by D X, in the singular bases D_ij s_j. The derivative of the remaining
+    map scales the symmetric part of a change by the divided differences (f_i - f_j) / (s'_i - s'_j) and its
+    antisymmetric part by (f_i + f_j) / (s'_i + s'_j); with d the larger of the two, an entry grows to at most
+    d max(s_i, s_j) |D_ij|. Independent roundings spread evenly over the bases, E|D_ij|^2 = |D|^2 / r^2, and add in
+    squares over the sources: P's own rounding u |P|; A's, u |A| through b + 2 c s^2; and X's in A, sqrt(2) u |X| s_1
+    through the same."""
+    s = torch.linalg.svdvals(g.double())
+    s = s / s.square().sum().sqrt()
+
+    def rest(v, k):
+        for a, b, c in steps[k:]:
+            v = v * (a + b * v ** 2 + c * v ** 4)
+        return v
+
+    total = 0.0
+    for k, (a, b, c) in enumerate(steps):
+        nxt = s * (a + b * s ** 2 + c * s ** 4)
+        f = rest(nxt, k + 1)
+        h = 1e-6
+        slope = ((rest(nxt + h, k + 1) - rest(nxt - h, k + 1)) / (2 * h)).abs()
+        gap = nxt[:, None] - nxt[None]
+        near = gap.abs() <= 1e-5
+        even = torch.where(near, torch.maximum(slope[:, None], slope[None]),
+                           (f[:, None] - f[None]) / torch.where(near, 1.0, gap))
+        odd = (f[:, None] + f[None]) / (nxt[:, None] + nxt[None]).abs().clamp_min(1e-30)
+        grow = (torch.maximum(even.abs(), odd.abs()) * torch.maximum(s[:, None], s[None])).square().mean()
+        into = (b + 2 * c * s ** 2).abs().max()
+        own = (u * (b * s ** 2 + c * s ** 4).norm()) ** 2 + (into * u * s.square().norm()) ** 2
+        if from_hi:
+            own = own + 2 * (into * u * s.norm() * s.max()) ** 2
+        total = total + float(grow * own / 3)
+        s = nxt.abs()
+    return math.sqrt(total)
