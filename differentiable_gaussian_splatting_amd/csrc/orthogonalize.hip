@@ -99,10 +99,11 @@ __global__ __launch_bounds__(kThreads) void k_orth_norm(OrthShape g, Source<T, M
   if (threadIdx.x == 0) part[size_t(b) * g.parts + blockIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// X_0 in two planes, transposed if the matrix is tall, zeros in the padding. A workgroup takes a 64 x 64 tile.
+// X_0 and its transpose in two planes each, zeros in the padding. A workgroup takes a 64 x 64 tile.
 template <typename T, bool MUON>
 __global__ __launch_bounds__(kThreads) void k_orth_start(OrthShape g, Source<T, MUON> src,
-                                                         const double* __restrict__ part, half* __restrict__ x) {
+                                                         const double* __restrict__ part, half* __restrict__ x,
+                                                         half* __restrict__ xt) {
   __shared__ float tile[64][65];
   __shared__ double scale_s;
   const uint32_t b = blockIdx.z, r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
@@ -132,27 +133,29 @@ __global__ __launch_bounds__(kThreads) void k_orth_start(OrthShape g, Source<T, 
   }
   __syncthreads();
   const uint64_t plane = g.rp * g.cp;
-  half* out = x + 2 * plane * b;
-  for (int e = threadIdx.x; e < 64 * 8; e += kThreads) {
-    const uint32_t i = e / 8, j = (e % 8) * 8;
-    Vec<half, 8> hi, lo;
+  for (int turned = 0; turned < 2; ++turned) {
+    half* out = (turned ? xt : x) + 2 * plane * b;
+    for (int e = threadIdx.x; e < 64 * 8; e += kThreads) {
+      const uint32_t i = e / 8, j = (e % 8) * 8;
+      Vec<half, 8> hi, lo;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      half h, l;
-      split(tile[i][j + k], &h, &l);
-      hi[k] = h;
-      lo[k] = l;
+      for (int k = 0; k < 8; ++k) {
+        half h, l;
+        split(turned ? tile[j + k][i] : tile[i][j + k], &h, &l);
+        hi[k] = h;
+        lo[k] = l;
+      }
+      const uint64_t at = turned ? (c0 + i) * g.rp + r0 + j : (r0 + i) * g.cp + c0 + j;
+      *reinterpret_cast<Vec<half, 8>*>(out + at) = hi;
+      *reinterpret_cast<Vec<half, 8>*>(out + plane + at) = lo;
     }
-    const uint64_t at = (r0 + i) * g.cp + c0 + j;
-    *reinterpret_cast<Vec<half, 8>*>(out + at) = hi;
-    *reinterpret_cast<Vec<half, 8>*>(out + plane + at) = lo;
   }
 }
 
-// One operand of a product: `planes` of [.][ld] float16 from base, `stride` apart.
+// One operand of a product: planes of [rows][ld] float16 from base on, `plane` elements apart.
 struct Operand {
   const half* base;
-  uint64_t plane, ld;
+  uint64_t plane, ld, rows;
 };
 
 __device__ __forceinline__ void to_lds(const half* p, char* s) {
@@ -160,136 +163,204 @@ __device__ __forceinline__ void to_lds(const half* p, char* s) {
                                    (__attribute__((address_space(3))) void*)s, 16, 0, 0);
 }
 
-// The two kinds of LDS tiles: kTile rows of kDeep values (both operands' depths adjacent), or kDeep rows of kTile values.
-template <int kTile, bool DEEP_ROWS>
+// An LDS tile of kTile rows of kDeep values.
+template <int kTile>
 struct Stage {
-  using L = Tile<half, DEEP_ROWS ? kTile : kDeep>;
-  static constexpr int kRows = DEEP_ROWS ? kDeep : kTile;
+  using L = Tile<half, kDeep>;
   static constexpr int kBytes = kTile * kDeep * 2;
   static constexpr int kPass = kThreads / L::kChunks;  // rows that the workgroup copies at a time
-  static constexpr int kCopies = kRows / kPass;
+  static constexpr int kCopies = kTile / kPass;
 
-  // Starts the copy of rows row .. , values col .. of one plane.
-  __device__ static __forceinline__ void start(const half* p, uint64_t ld, uint64_t row, uint64_t col, char* s) {
+  // Starts the copy of rows row .. , values k .. of one plane of rows x ld; rows beyond repeat the last.
+  __device__ static __forceinline__ void start(const half* p, uint64_t ld, uint64_t rows, uint64_t row, uint64_t k,
+                                               char* s) {
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+    const int r = int(threadIdx.x) / L::kChunks;
+    const int c = ((int(threadIdx.x) % L::kChunks) ^ L::swizzle(r)) * 8;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) {
-      const int r = int(threadIdx.x) / L::kChunks + i * kPass;
-      const int c = ((int(threadIdx.x) % L::kChunks) ^ L::swizzle(r)) * 8;
-      to_lds(p + (row + r) * ld + col + c, s + i * kPass * L::kRowBytes + wave * 1024);
-    }
-  }
-
-  // Depths 16 kk + 8 h .. + 7 of row (or column) at + l % 32.
-  __device__ static __forceinline__ Vec<half, 8> frag(const char* s, int at, int kk) {
-    if constexpr (!DEEP_ROWS) {
-      return L::frag(s, at, kk);
-    } else {
-      // sixteen lanes read four rows of sixteen columns; lane j of them receives column j
-      const int l = threadIdx.x & 63, r = 16 * kk + 8 * (l >> 5) + ((l & 15) >> 2);
-      const int chunk = at / 8 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1);
-      using s16x4 = Vec<short, 4>;
-      using P = __attribute__((address_space(3))) s16x4*;
-      const Vec<half, 4> a = __builtin_bit_cast(
-          Vec<half, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(s + L::at(r, chunk) + (l & 1) * 8)));
-      const Vec<half, 4> b = __builtin_bit_cast(
-          Vec<half, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(s + L::at(r + 4, chunk) + (l & 1) * 8)));
-      return Vec<half, 8>{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    }
+    for (int i = 0; i < kCopies; ++i)
+      to_lds(p + min(row + r + i * kPass, rows - 1) * ld + k + c, s + i * kPass * L::kRowBytes + wave * 1024);
   }
 };
 
-// One kTile x kTile tile of a product of depth `deep`, on 2 x 2 waves: rows row .. of the left operand (LP planes, depths
-// adjacent), columns col .. of the right one (RP planes; its depths adjacent, or its columns where DEEP_ROWS). The
-// blocks are computed transposed, so that a lane holds one row of the result (l % 32 of its block) and adjacent columns:
-// f(row, column, four sums) is called for each four.
-template <int kTile, int LP, int RP, bool DEEP_ROWS, typename F>
-__device__ __forceinline__ void product(const Operand& left, const Operand& right, uint64_t row, uint64_t col,
-                                        uint64_t deep, F f) {
-  using SL = Stage<kTile, false>;
-  using SR = Stage<kTile, DEEP_ROWS>;
-  constexpr int kStage = LP * SL::kBytes + RP * SR::kBytes;
-  constexpr int kBlocks = kTile / 64;
-  __shared__ alignas(16) char lds[2][kStage];
-  const int wave = threadIdx.x >> 6, l = threadIdx.x & 63;
-  const int wr = (wave >> 1) * (kTile / 2), wc = (wave & 1) * (kTile / 2);
+// How many stages of tiles LDS holds: copies run that many ahead, less what is being multiplied.
+template <int kTile, int PLANES>
+constexpr int kStages = kTile == 64 ? 4 : (kTile == 128 && PLANES < 4 ? 3 : 2);
+
+// The sums of a workgroup's tile: wave (w / 2, w % 2) of 2 x 2 has rows row .. and columns col .. , lane l row
+// row + 32 i + l % 32 and columns col + 32 j + 8 q + 4 (l / 32) + {0..3} in acc[i][j][4 q ..].
+template <int kTile>
+struct Sums {
+  static constexpr int kBlocks = kTile / 64;
   f32x16 acc[kBlocks][kBlocks];
+  uint64_t row, col;
+};
+
+// Asks the compiler to issue PRODUCTS matrix products with READS LDS reads spread over the first half of them (the whole,
+// if there are no copies) and COPIES copies over the rest.
+template <int SYNC, int PRODUCTS, int READS, int COPIES, int E>
+__device__ __forceinline__ void spread_one() {
+  constexpr int kFirst = COPIES ? (PRODUCTS + 1) / 2 : (PRODUCTS * 3 + 3) / 4, kRest = PRODUCTS - kFirst;
+  __builtin_amdgcn_sched_group_barrier(0x008, 1, SYNC);  // a matrix product
+  if constexpr (E < kFirst) {
+    constexpr int n = (E + 1) * READS / kFirst - E * READS / kFirst;
+    if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x100, n, SYNC);  // LDS reads
+  } else if constexpr (COPIES > 0) {
+    constexpr int e = E - kFirst, n = (e + 1) * COPIES / kRest - e * COPIES / kRest;
+    if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x020, n, SYNC);  // copies
+  }
+}
+
+template <int SYNC, int PRODUCTS, int READS, int COPIES, int... E>
+__device__ __forceinline__ void spread(std::integer_sequence<int, E...>) {
+  (spread_one<SYNC, PRODUCTS, READS, COPIES, E>(), ...);
+}
+
+// One kTile x kTile tile of a product of depth `deep`: rows row .. of the left operand (LP planes) by rows col .. of the
+// right one (RP planes), depths adjacent in both. The blocks are computed transposed, so that a lane holds one row of the
+// result and adjacent columns. What lies past the operands' rows is computed and of no use. The workgroup's waves are
+// past the LDS `lds` (Lds::kBytes of it) when this returns.
+template <int kTile, int LP, int RP>
+struct Lds {
+  static constexpr int kStage = (LP + RP) * kTile * kDeep * 2, kBytes = kStage * kStages<kTile, LP + RP>;
+};
+
+template <int kTile, int LP, int RP>
+__device__ __forceinline__ void product(const Operand& left, const Operand& right, uint64_t row, uint64_t col,
+                                        uint64_t deep, char* lds, Sums<kTile>& s) {
+  using S = Stage<kTile>;
+  constexpr int kStage = Lds<kTile, LP, RP>::kStage, kCount = kStages<kTile, LP + RP>, kBlocks = kTile / 64;
+  constexpr int kCopies = (LP + RP) * S::kCopies;  // of a stage, by each wave
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int wr = (wave >> 1) * (kTile / 2), wc = (wave & 1) * (kTile / 2);
+  s.row = row + wr;
+  s.col = col + wc;
 #pragma unroll
   for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
     for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  auto start = [&](uint64_t k, char* s) {
+      for (int e = 0; e < 16; ++e) s.acc[i][j][e] = 0.0f;
+  auto start = [&](uint64_t k, int stage) {
+    char* to = lds + stage * kStage;
 #pragma unroll
-    for (int p = 0; p < LP; ++p) SL::start(left.base + p * left.plane, left.ld, row, k, s + p * SL::kBytes);
+    for (int p = 0; p < LP; ++p)
+      S::start(left.base + p * left.plane, left.ld, left.rows, row, k, to + p * S::kBytes);
 #pragma unroll
     for (int p = 0; p < RP; ++p)
-      SR::start(right.base + p * right.plane, right.ld, DEEP_ROWS ? k : col, DEEP_ROWS ? col : k,
-                s + LP * SL::kBytes + p * SR::kBytes);
+      S::start(right.base + p * right.plane, right.ld, right.rows, col, k, to + (LP + p) * S::kBytes);
   };
-  start(0, lds[0]);
-  int turn = 0;
-  for (uint64_t k = 0; k < deep; k += kDeep, turn ^= 1) {
-    tile_barrier<0>();
-    if (k + kDeep < deep) start(k + kDeep, lds[turn ^ 1]);
-    const char *sl = lds[turn], *sr = lds[turn] + LP * SL::kBytes;
+  // Fragments of the two halves of a stage. While one half is multiplied the next half's are read, so that the matrix cores
+  // wait for neither LDS nor the barrier, which lies between the halves: behind it this stage's tiles are read to the end
+  // by every wave, the next stage's have landed, and the copies of the stage kCount on may start. Those past the end
+  // repeat the last stage.
+  Vec<half, 8> a[2][LP][kBlocks], b[2][RP][kBlocks];
+  auto read = [&](const char* sl, int kk) {
+    const char* sr = sl + LP * S::kBytes;
 #pragma unroll
-    for (int kk = 0; kk < kDeep / 16; ++kk) {
-      Vec<half, 8> a[LP][kBlocks], b[RP][kBlocks];
+    for (int i = 0; i < kBlocks; ++i) {
 #pragma unroll
-      for (int i = 0; i < kBlocks; ++i) {
+      for (int p = 0; p < LP; ++p) a[kk][p][i] = S::L::frag(sl + p * S::kBytes, wr + 32 * i, kk);
 #pragma unroll
-        for (int p = 0; p < LP; ++p) a[p][i] = SL::frag(sl + p * SL::kBytes, wr + 32 * i, kk);
+      for (int p = 0; p < RP; ++p) b[kk][p][i] = S::L::frag(sr + p * S::kBytes, wc + 32 * i, kk);
+    }
+  };
+  auto multiply = [&](int kk) {
 #pragma unroll
-        for (int p = 0; p < RP; ++p) b[p][i] = SR::frag(sr + p * SR::kBytes, wc + 32 * i, kk);
-      }
+    for (int p = 0; p < LP; ++p)
 #pragma unroll
-      for (int p = 0; p < LP; ++p)
-#pragma unroll
-        for (int q = 0; q + p < (LP > RP ? LP : RP); ++q)  // not lo lo
+      for (int q = 0; q < RP; ++q)
+        if (p + q < (LP > RP ? LP : RP))  // not lo lo
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
-            for (int j = 0; j < kBlocks; ++j)
-              if (q < RP) acc[i][j] = mma(b[q][j], a[p][i], acc[i][j]);
+            for (int j = 0; j < kBlocks; ++j) s.acc[i][j] = mma(b[kk][q][j], a[kk][p][i], s.acc[i][j]);
+  };
+  constexpr int kReads = (LP + RP) * kBlocks, kProducts = (LP + RP - 1) * kBlocks * kBlocks;
+#pragma unroll
+  for (int i = 0; i < kCount; ++i) start(min(uint64_t(i) * kDeep, deep - kDeep), i);
+  tile_barrier<(kCount - 1) * kCopies>();
+  read(lds, 0);
+  int now = 0;
+  for (uint64_t k = 0; k < deep; k += kDeep) {
+    read(lds + now * kStage, 1);
+    multiply(0);
+    spread<0, kProducts, kReads, 0>(std::make_integer_sequence<int, kProducts>());
+    __builtin_amdgcn_sched_barrier(0);
+    tile_barrier<(kCount - 2) * kCopies>();
+    __builtin_amdgcn_sched_barrier(0);
+    const int done = now;
+    now = now + 1 == kCount ? 0 : now + 1;
+    read(lds + now * kStage, 0);
+    start(min(k + kCount * kDeep, deep - kDeep), done);
+    multiply(1);
+    spread<1, kProducts, kReads, kCopies>(std::make_integer_sequence<int, kProducts>());
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  tile_barrier<0>();
+}
+
+// Orders a wave's LDS writes before its reads of what other lanes wrote.
+__device__ __forceinline__ void wave_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// 32 rows of kTile / 2 float16 values in a wave's part of LDS, by which a wave turns its sums into whole lines: rows lie 16
+// bytes more than their length apart, so that lanes of adjacent rows meet different banks.
+template <int kTile>
+struct Turn {
+  static constexpr int kCols = kTile / 2, kStride = kCols * 2 + 16, kBytes = 32 * kStride;
+
+  static constexpr int kChunks = kCols / 8, kTurns = 32 * kChunks / 64;
+
+  // The lane's four values from column col of its row on.
+  __device__ static __forceinline__ Vec<half, 4>& at(char* s, int col) {
+    return *reinterpret_cast<Vec<half, 4>*>(s + (threadIdx.x & 31) * kStride + col * 2);
+  }
+  // Loads rows row .. and columns col .. of in, [size_r][ld], 16 bytes a lane at a time (what lies beyond repeats the last
+  // ones), and lays them into LDS.
+  __device__ static __forceinline__ void fetch(const half* in, uint64_t ld, uint64_t row, uint64_t col, uint64_t size_r,
+                                               u32x4* v) {
+#pragma unroll
+    for (int t = 0; t < kTurns; ++t) {
+      const int e = t * 64 + int(threadIdx.x & 63), r = e / kChunks, c = e % kChunks;
+      v[t] = *reinterpret_cast<const u32x4*>(in + min(row + r, size_r - 1) * ld + min(col + 8 * c, ld - 8));
     }
   }
+  __device__ static __forceinline__ void lay(const u32x4* v, char* s) {
 #pragma unroll
-  for (int i = 0; i < kBlocks; ++i)
-#pragma unroll
-    for (int j = 0; j < kBlocks; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        f(row + wr + 32 * i + (l & 31), col + wc + 32 * j + 8 * q + 4 * (l >> 5),
-          Vec<float, 4>{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
-}
-
-template <int PLANES>
-__device__ __forceinline__ Vec<float, 4> load_split(const half* p, uint64_t plane) {
-  const Vec<half, 4> h = *reinterpret_cast<const Vec<half, 4>*>(p);
-  Vec<float, 4> v = {float(h[0]), float(h[1]), float(h[2]), float(h[3])};
-  if constexpr (PLANES == 2) {
-    const Vec<half, 4> l = *reinterpret_cast<const Vec<half, 4>*>(p + plane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += float(l[i]);
+    for (int t = 0; t < kTurns; ++t) {
+      const int e = t * 64 + int(threadIdx.x & 63);
+      *reinterpret_cast<u32x4*>(s + e / kChunks * kStride + e % kChunks * 16) = v[t];
+    }
   }
-  return v;
-}
-
-template <int PLANES>
-__device__ __forceinline__ void store_split(half* p, uint64_t plane, Vec<float, 4> v) {
-  Vec<half, 4> hi, lo;
+  // Rows row .. and columns col .. of out, [size_r][ld], in 16-byte stores.
+  __device__ static __forceinline__ void rows(const char* s, half* out, uint64_t ld, uint64_t row, uint64_t col,
+                                              uint64_t size_r) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    half h, l;
-    split(v[i], &h, &l);
-    hi[i] = h;
-    lo[i] = l;
+    for (int t = 0; t < kTurns; ++t) {
+      const int e = t * 64 + int(threadIdx.x & 63), r = e / kChunks, c = e % kChunks;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(s + r * kStride + c * 16);
+      if (row + r < size_r && col + 8 * c < ld) *reinterpret_cast<u32x4*>(out + (row + r) * ld + col + 8 * c) = v;
+    }
   }
-  *reinterpret_cast<Vec<half, 4>*>(p) = hi;
-  if constexpr (PLANES == 2) *reinterpret_cast<Vec<half, 4>*>(p + plane) = lo;
-}
+  // The transposed 32 columns: rows col .. and columns row .. of out, 64 bytes of a row together.
+  __device__ static __forceinline__ void columns(const char* s, half* out, uint64_t ld, uint64_t row, uint64_t col,
+                                                 uint64_t size_r) {
+    const int l = threadIdx.x & 63, g = l >> 4, j = l & 15;
+    using s16x4 = Vec<short, 4>;
+    using P = __attribute__((address_space(3))) s16x4*;
+#pragma unroll
+    for (int c = 0; c < kCols; c += 16) {
+      // sixteen lanes read four rows of sixteen columns; lane j of them receives column j
+      const char* at = s + (8 * g + (j >> 2)) * kStride + (c + (j & 3) * 4) * 2;
+      const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)at);
+      const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(at + 4 * kStride));
+      using s16x8 = Vec<short, 8>;
+      const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      if (col + c + j < size_r && row + 8 * g < ld)
+        *reinterpret_cast<s16x8*>(out + (col + c + j) * ld + row + 8 * g) = v;
+    }
+  }
+};
 
 // Which tile a workgroup computes: workgroups are dealt to the dies round-robin, so consecutive tiles go to one die.
 struct Works {
@@ -310,12 +381,46 @@ __device__ __forceinline__ void triangle(uint32_t t, uint32_t* i, uint32_t* j) {
   *j = t - uint32_t(uint64_t(r) * (r + 1) / 2);
 }
 
-// out = alpha in + beta (x x^T) [r, r], PLANES planes each of x (XP read), in (none if alpha is 0) and out, symmetric.
+// A wave's 32 rows of sums, beta times, as numbers of PLANES planes in its part of LDS; with ADD plus alpha times the
+// numbers of two planes (or one, if PLANES is 1) that lie there.
 template <int kTile, int PLANES, bool ADD>
-__global__ __launch_bounds__(kThreads) void k_orth_symmetric(Works w, uint32_t tiles, Operand x, uint64_t x_matrix,
-                                                             uint64_t deep, const half* __restrict__ in,
-                                                             half* __restrict__ out, uint64_t rp, float alpha,
-                                                             float beta) {
+__device__ __forceinline__ void finish_rows(char* mine, const f32x16* acc, float alpha, float beta) {
+  using L = Turn<kTile>;
+#pragma unroll
+  for (int j = 0; j < kTile / 64; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = 32 * j + 8 * q + 4 * int((threadIdx.x & 63) >> 5);
+      Vec<half, 4> &hi = L::at(mine, col), &lo = L::at(mine + (PLANES - 1) * L::kBytes, col);
+      Vec<float, 4> v = {acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+      v *= beta;
+      if constexpr (ADD) {
+        const Vec<half, 4> h = hi, w = lo;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = fmaf(alpha, PLANES == 2 ? float(h[k]) + float(w[k]) : float(h[k]), v[k]);
+      }
+      Vec<half, 4> h, w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        half a, b;
+        split(v[k], &a, &b);
+        h[k] = a;
+        w[k] = b;
+      }
+      if constexpr (PLANES == 2) lo = w;
+      hi = h;
+    }
+}
+
+// out = alpha in + beta (x x^T) [rp, rp], symmetric, PLANES planes each of x, in (read if ADD) and out.
+template <int kTile, int PLANES, bool ADD>
+__global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_symmetric(
+    Works w, uint32_t tiles, Operand x, uint64_t x_matrix, uint64_t deep, const half* __restrict__ in,
+    half* __restrict__ out, uint64_t rp, float alpha, float beta) {
+  using Mem = Lds<kTile, PLANES, PLANES>;
+  using L = Turn<kTile>;
+  static_assert(4 * PLANES * L::kBytes <= Mem::kBytes, "the results pass through the stages' LDS");
+  __shared__ alignas(16) char lds[Mem::kBytes];
   uint64_t id;
   if (!w.mine(&id)) return;
   const uint64_t b = id / tiles;
@@ -325,23 +430,37 @@ __global__ __launch_bounds__(kThreads) void k_orth_symmetric(Works w, uint32_t t
   x.base += b * x_matrix;
   in += b * PLANES * plane;
   out += b * PLANES * plane;
-  product<kTile, PLANES, PLANES, false>(
-      x, x, uint64_t(ti) * kTile, uint64_t(tj) * kTile, deep, [&](uint64_t row, uint64_t col, Vec<float, 4> v) {
-        v *= beta;
-        if constexpr (ADD) v += alpha * load_split<PLANES>(in + row * rp + col, plane);
-        store_split<PLANES>(out + row * rp + col, plane, v);
-        if (ti != tj)
+  Sums<kTile> s;
+  product<kTile, PLANES, PLANES>(x, x, uint64_t(ti) * kTile, uint64_t(tj) * kTile, deep, lds, s);
+  char* mine = lds + (threadIdx.x >> 6) * PLANES * L::kBytes;
+  u32x4 have[PLANES][L::kTurns];
+  auto fetch = [&](uint64_t row) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            half h, l;
-            split(v[k], &h, &l);
-            out[(col + k) * rp + row] = h;
-            if constexpr (PLANES == 2) out[plane + (col + k) * rp + row] = l;
-          }
-      });
+    for (int p = 0; p < PLANES; ++p) L::fetch(in + p * plane, rp, row, s.col, rp, have[p]);
+  };
+  if constexpr (ADD) fetch(s.row);
+#pragma unroll
+  for (int i = 0; i < kTile / 64; ++i) {
+    const uint64_t row = s.row + 32 * i;
+    if (row >= rp) break;
+    wave_sync();  // the last rows' reads
+    if constexpr (ADD) {
+#pragma unroll
+      for (int p = 0; p < PLANES; ++p) L::lay(have[p], mine + p * L::kBytes);
+      if (i + 1 < kTile / 64) fetch(row + 32);  // on their way while these rows are stored
+      wave_sync();
+    }
+    finish_rows<kTile, PLANES, ADD>(mine, s.acc[i], alpha, beta);
+    wave_sync();
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p) {
+      L::rows(mine + p * L::kBytes, out + p * plane, rp, row, s.col, rp);
+      if (ti != tj) L::columns(mine + p * L::kBytes, out + p * plane, rp, row, s.col, rp);
+    }
+  }
 }
 
-// What the last product is for: nothing (X' = its planes are written), a result in type T, or a parameter's update.
+// What the last product is for: the next step (X' is written in two planes), a result in type T, or a parameter's update.
 template <typename T>
 struct Result {
   T* p;
@@ -351,11 +470,17 @@ struct Result {
 
 enum { kNext = 0, kWrite = 1, kUpdate = 2 };
 
-// X' = alpha X + beta (P X), PP planes of P.
+// X' = alpha X + beta (P X), PP planes of P, from X (written in place: only its own tile is read) and its transpose xt; the
+// transpose goes to next.
 template <int kTile, int PP, int WHAT, typename T>
-__global__ __launch_bounds__(kThreads) void k_orth_apply(Works w, OrthShape g, uint32_t tiles_r, uint32_t tiles_c,
-                                                         Operand p, const half* x, half* next, float alpha, float beta,
-                                                         Result<T> res) {
+__global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_apply(
+    Works w, OrthShape g, uint32_t tiles_r, uint32_t tiles_c, Operand p, half* x,
+    const half* __restrict__ xt, half* __restrict__ next, float alpha, float beta, Result<T> res) {
+  using Mem = Lds<kTile, PP, 2>;
+  using L = Turn<kTile>;
+  constexpr int kStride = kTile / 2 * 4 + 16;  // of rows of float32, as L's
+  static_assert(4 * 2 * L::kBytes <= Mem::kBytes && 2 * L::kBytes >= 32 * kStride, "the results pass through the stages' LDS");
+  __shared__ alignas(16) char lds[Mem::kBytes];
   uint64_t id;
   if (!w.mine(&id)) return;
   const uint32_t tr = uint32_t(id % tiles_r);
@@ -364,25 +489,110 @@ __global__ __launch_bounds__(kThreads) void k_orth_apply(Works w, OrthShape g, u
   const uint64_t b = id / tiles_c, plane = g.rp * g.cp;
   p.base += b * PP * p.plane;
   x += b * 2 * plane;
-  const Operand right{x, plane, g.cp};
-  product<kTile, PP, 2, true>(
-      p, right, uint64_t(tr) * kTile, uint64_t(tc) * kTile, g.rp, [&](uint64_t row, uint64_t col, Vec<float, 4> v) {
-        v = v * beta + alpha * load_split<2>(x + row * g.cp + col, plane);
-        if constexpr (WHAT == kNext) {
-          store_split<2>(next + b * 2 * plane + row * g.cp + col, plane, v);
-        } else {
+  const Operand right{xt + b * 2 * plane, plane, g.rp, g.cp};
+  Sums<kTile> s;
+  product<kTile, PP, 2>(p, right, uint64_t(tr) * kTile, uint64_t(tc) * kTile, g.rp, lds, s);
+  const int l = threadIdx.x & 63;
+  char* mine = lds + (threadIdx.x >> 6) * 2 * L::kBytes;
+  const T* const from = res.p + int64_t(b) * res.mat;
+  T* const to = res.p + int64_t(b) * res.mat;
+  u32x4 have[2][L::kTurns];
+  auto fetch = [&](uint64_t row) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (row >= g.r || col + k >= g.c) continue;
-            T* o = res.p + int64_t(b) * res.mat +
-                   (g.tall ? int64_t(col + k) * res.row + int64_t(row) : int64_t(row) * res.row + int64_t(col + k));
-            if constexpr (WHAT == kUpdate)
-              *o = res.decay * *o - res.lr * v[k];
-            else
-              *o = T(v[k]);
-          }
+    for (int q = 0; q < 2; ++q) L::fetch(x + q * plane, g.cp, row, s.col, g.rp, have[q]);
+  };
+  fetch(s.row);
+#pragma unroll
+  for (int i = 0; i < kTile / 64; ++i) {
+    const uint64_t row = s.row + 32 * i;
+    if (row >= g.rp) break;
+    wave_sync();  // the last rows' reads
+#pragma unroll
+    for (int q = 0; q < 2; ++q) L::lay(have[q], mine + q * L::kBytes);
+    if (i + 1 < kTile / 64) fetch(row + 32);  // on their way while these rows are stored
+    wave_sync();
+    if constexpr (WHAT == kNext) {
+      finish_rows<kTile, 2, true>(mine, s.acc[i], alpha, beta);
+      wave_sync();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        L::rows(mine + q * L::kBytes, x + q * plane, g.cp, row, s.col, g.rp);
+        L::columns(mine + q * L::kBytes, next + (b * 2 + q) * plane, g.rp, row, s.col, g.cp);
+      }
+      continue;
+    }
+    f32x16 v[kTile / 64];
+#pragma unroll
+    for (int j = 0; j < kTile / 64; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = 32 * j + 8 * q + 4 * (l >> 5);
+        const Vec<half, 4> hi = L::at(mine, col), lo = L::at(mine + L::kBytes, col);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          v[j][4 * q + k] = fmaf(alpha, float(hi[k]) + float(lo[k]), s.acc[i][j][4 * q + k] * beta);
+      }
+    if (g.tall) {  // a lane's row is a column of the result: sixteen columns of it at a time
+      const bool live = row + (l & 31) < g.r;
+#pragma unroll
+      for (int j = 0; j < kTile / 64; ++j) {
+        const uint64_t col = s.col + 32 * j + 4 * (l >> 5);
+        float old[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint64_t at = col + 8 * (e / 4) + e % 4;
+          old[e] = WHAT == kUpdate && live && at < g.c
+                       ? float(from[int64_t(at) * res.row + int64_t(row) + (l & 31)])
+                       : 0.0f;
         }
-      });
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint64_t at = col + 8 * (e / 4) + e % 4;
+          if (live && at < g.c)
+            to[int64_t(at) * res.row + int64_t(row) + (l & 31)] =
+                T(WHAT == kUpdate ? res.decay * old[e] - res.lr * v[j][e] : v[j][e]);
+        }
+      }
+    } else {
+      wave_sync();
+#pragma unroll
+      for (int j = 0; j < kTile / 64; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<Vec<float, 4>*>(mine + (l & 31) * kStride + (32 * j + 8 * q + 4 * (l >> 5)) * 4) =
+              Vec<float, 4>{v[j][4 * q], v[j][4 * q + 1], v[j][4 * q + 2], v[j][4 * q + 3]};
+      wave_sync();
+      constexpr int kLanes = kTile / 8, kTurns = 32 * kLanes / 64, kAtOnce = kTurns < 4 ? kTurns : 4;
+#pragma unroll
+      for (int t0 = 0; t0 < kTurns; t0 += kAtOnce) {
+        float old[kAtOnce][4];
+        auto place = [&](int t, int* r, int* c, int* n) {
+          const int e = (t0 + t) * 64 + l;
+          *r = e / kLanes;
+          *c = e % kLanes * 4;
+          const int64_t left = int64_t(g.c) - int64_t(s.col) - *c;
+          *n = row + *r < g.r ? int(left < 0 ? 0 : (left > 4 ? 4 : left)) : 0;
+        };
+        if constexpr (WHAT == kUpdate)
+#pragma unroll
+          for (int t = 0; t < kAtOnce; ++t) {
+            int r, c, n;
+            place(t, &r, &c, &n);
+            load_f32<4>(from + int64_t(row + r) * res.row + int64_t(s.col) + c, n, old[t]);
+          }
+#pragma unroll
+        for (int t = 0; t < kAtOnce; ++t) {
+          int r, c, n;
+          place(t, &r, &c, &n);
+          const Vec<float, 4> x4 = *reinterpret_cast<const Vec<float, 4>*>(mine + r * kStride + c * 4);
+          float o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = WHAT == kUpdate ? res.decay * old[t][k] - res.lr * x4[k] : x4[k];
+          store_f32<4>(to + int64_t(row + r) * res.row + int64_t(s.col) + c, n, o);
+        }
+      }
+    }
+  }
 }
 
 struct Step {
@@ -426,35 +636,82 @@ bool plan_of(const gsr_newton_schulz* d, Plan* p) {
 
 uint64_t round_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
-template <int kTile, int PLANES, typename T, bool MUON, typename R>
-void launch_steps(hipStream_t s, const OrthShape& g, const Plan& plan, const Source<T, MUON>& src, double* part, half* x0,
-                  half* x1, half* am, half* pm, const Result<R>& res) {
+// The side of the square tiles of a product: the one whose rounds of workgroups take least. `tiles(side)` counts them.
+// Measured for tiles of depth 1,024 in two planes, one workgroup after the other on a compute unit: 12.8, 31, 56 and 95
+// us; small tiles overlap, so that part of a round of them counts as part. 8 x 1,024 x 4,096: P X 243 us with tiles of
+// 256, 278 with 128, 416 with 64; 4,096 x 1,024: X X^T 36 us with tiles of 64, 91 with 128; 4,096 x 4,096: A A^T 205 us
+// with 253 tiles of 192, 250 with 136 of 256, 276 with 528 of 128.
+template <typename F>
+int tile_side(F tiles) {
+  int best = 0;
+  double least = 1e300;
+  for (const auto& [side, us] : {std::pair(64, 12.8), std::pair(128, 31.0), std::pair(192, 56.0), std::pair(256, 95.0)}) {
+    const double rounds = double(tiles(uint64_t(side))) / 256;
+    const double time = us * (side == 64 ? std::max(1.0, rounds) : std::ceil(rounds));
+    if (time < least) {
+      least = time;
+      best = side;
+    }
+  }
+  return best;
+}
+
+// Calls f(tile side) with a compile-time value.
+template <typename F>
+void by_side(int side, F f) {
+  if (side == 64)
+    f(std::integral_constant<int, 64>());
+  else if (side == 128)
+    f(std::integral_constant<int, 128>());
+  else if (side == 192)
+    f(std::integral_constant<int, 192>());
+  else
+    f(std::integral_constant<int, 256>());
+}
+
+template <int PLANES, typename T, bool MUON, typename R>
+void launch_steps(hipStream_t s, const OrthShape& g, const Plan& plan, const Source<T, MUON>& src, double* part, half* x,
+                  half* xt, half* next, half* am, half* pm, const Result<R>& res) {
   hipLaunchKernelGGL((k_orth_norm<T, MUON>), dim3(g.parts, g.batch), dim3(kThreads), 0, s, g, src, part);
   hipLaunchKernelGGL((k_orth_start<T, MUON>), dim3(uint32_t(g.cp / 64), uint32_t(g.rp / 64), g.batch), dim3(kThreads), 0,
-                     s, g, src, part, x0);
+                     s, g, src, part, x, xt);
   const uint64_t plane = g.rp * g.cp, square = g.rp * g.rp;
-  const uint32_t tr = uint32_t(g.rp / kTile), tc = uint32_t(g.cp / kTile), tri = uint32_t(uint64_t(tr) * (tr + 1) / 2);
+  auto across = [](uint64_t n, uint64_t side) { return (n + side - 1) / side; };
+  auto triangle = [&](uint64_t side) { return across(g.rp, side) * (across(g.rp, side) + 1) / 2; };
+  auto whole = [&](uint64_t side) { return across(g.rp, side) * across(g.cp, side); };
   auto works = [](uint64_t n) { return Works{n, (n + kFeatXcds - 1) / kFeatXcds}; };
-  const Works half_square = works(uint64_t(tri) * g.batch), whole = works(uint64_t(tr) * tc * g.batch);
   auto grid = [](const Works& w) { return grid_rows(w.per_xcd * kFeatXcds); };
+  const int side_s = tile_side([&](uint64_t side) { return triangle(side) * g.batch; });
+  const int side_w = tile_side([&](uint64_t side) { return whole(side) * g.batch; });
   for (int k = 0; k < plan.steps; ++k) {
     const Step& c = plan.step[k];
     const int ex = plan.x_exp[k], ea = plan.a_exp[k], ep = plan.p_exp[k], en = plan.x_exp[k + 1];
-    hipLaunchKernelGGL((k_orth_symmetric<kTile, PLANES, false>), grid(half_square), dim3(kThreads), 0, s, half_square,
-                       tri, Operand{x0, plane, g.cp}, 2 * plane, g.cp, am, am, g.rp, 0.0f,
-                       std::ldexp(1.0f, ea - 2 * ex));
-    hipLaunchKernelGGL((k_orth_symmetric<kTile, PLANES, true>), grid(half_square), dim3(kThreads), 0, s, half_square,
-                       tri, Operand{am, square, g.rp}, PLANES * square, g.rp, am, pm, g.rp, std::ldexp(c.b, ep - ea),
-                       std::ldexp(c.c, ep - 2 * ea));
+    by_side(side_s, [&](auto side) {
+      constexpr int kTile = decltype(side)::value;
+      const uint32_t tiles = uint32_t(triangle(kTile));
+      const Works w = works(uint64_t(tiles) * g.batch);
+      hipLaunchKernelGGL((k_orth_symmetric<kTile, PLANES, false>), grid(w), dim3(kThreads), 0, s, w, tiles,
+                         Operand{x, plane, g.cp, g.rp}, 2 * plane, g.cp, am, am, g.rp, 0.0f,
+                         std::ldexp(1.0f, ea - 2 * ex));
+      hipLaunchKernelGGL((k_orth_symmetric<kTile, PLANES, true>), grid(w), dim3(kThreads), 0, s, w, tiles,
+                         Operand{am, square, g.rp, g.rp}, PLANES * square, g.rp, am, pm, g.rp, std::ldexp(c.b, ep - ea),
+                         std::ldexp(c.c, ep - 2 * ea));
+    });
     const float alpha = std::ldexp(c.a, en - ex), beta = std::ldexp(1.0f, en - ep - ex);
-    const Operand p{pm, square, g.rp};
-    if (k + 1 < plan.steps)
-      hipLaunchKernelGGL((k_orth_apply<kTile, PLANES, kNext, R>), grid(whole), dim3(kThreads), 0, s, whole, g, tr, tc, p,
-                         x0, x1, alpha, beta, res);
-    else
-      hipLaunchKernelGGL((k_orth_apply<kTile, PLANES, MUON ? kUpdate : kWrite, R>), grid(whole), dim3(kThreads), 0, s,
-                         whole, g, tr, tc, p, x0, x1, alpha, beta, res);
-    std::swap(x0, x1);
+    const Operand p{pm, square, g.rp, g.rp};
+    by_side(side_w, [&](auto side) {
+      constexpr int kTile = decltype(side)::value;
+      const uint32_t tr = uint32_t(across(g.rp, kTile)), tc = uint32_t(across(g.cp, kTile));
+      const Works w = works(uint64_t(tr) * tc * g.batch);
+      auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid(w), dim3(kThreads), 0, s, w, g, tr, tc, p, x, xt, next, alpha, beta, res);
+      };
+      if (k + 1 < plan.steps)
+        launch(k_orth_apply<kTile, PLANES, kNext, R>);
+      else
+        launch(k_orth_apply<kTile, PLANES, MUON ? kUpdate : kWrite, R>);
+    });
+    std::swap(xt, next);
   }
 }
 
@@ -476,7 +733,8 @@ gsr_status check_desc(gsr_ctx* ctx, const gsr_newton_schulz* d, const char* who,
 template <typename T, bool MUON, typename R>
 gsr_status run(gsr_ctx* ctx, hipStream_t s, const gsr_newton_schulz* d, const Plan& plan,
                const Source<T, MUON>& src, const Result<R>& res, int stage, const char* who) {
-  constexpr int kPlanes = std::is_same_v<R, __bf16> ? 1 : 2;
+  // bfloat16: the left factors in one number where the products take the time
+  const int planes = std::is_same_v<R, __bf16> && std::min(d->rows, d->cols) > 256 ? 1 : 2;
   OrthShape g{};
   g.batch = d->batch;
   g.rows = d->rows;
@@ -488,23 +746,24 @@ gsr_status run(gsr_ctx* ctx, hipStream_t s, const gsr_newton_schulz* d, const Pl
   g.first = std::ldexp(1.0f, plan.x_exp[0]);
   g.by_vec.set((d->cols + kNormVec - 1) / kNormVec);
   g.parts = uint32_t(std::min<uint64_t>(256, (uint64_t(g.by_vec.d) * g.rows + 4 * kThreads - 1) / (4 * kThreads)));
-  const int tile = g.r <= 512 ? 64 : 128;
-  g.rp = round_up(g.r, tile);
-  g.cp = round_up(g.c, tile);
+  g.rp = round_up(g.r, 64);
+  g.cp = round_up(g.c, 64);
   const size_t plane = g.rp * g.cp, square = g.rp * g.rp, parts = round_up(size_t(g.batch) * g.parts, 2);
   gsr_status st = grow(ctx, ctx->arena.feat_part,
-                       parts * sizeof(double) + g.batch * (4 * plane + 2 * kPlanes * square) * sizeof(half));
+                       parts * sizeof(double) + g.batch * (6 * plane + 2 * planes * square) * sizeof(half));
   if (st) return st;
   double* part = static_cast<double*>(ctx->arena.feat_part.ptr);
-  half* x0 = reinterpret_cast<half*>(part + parts);
-  half* x1 = x0 + 2 * plane * g.batch;
-  half* am = x1 + 2 * plane * g.batch;
-  half* pm = am + kPlanes * square * g.batch;
+  half* x = reinterpret_cast<half*>(part + parts);
+  half* xt = x + 2 * plane * g.batch;
+  half* next = xt + 2 * plane * g.batch;
+  half* am = next + 2 * plane * g.batch;
+  half* pm = am + planes * square * g.batch;
   timing_mark(ctx, stage, s, false);
-  if (tile == 64)
-    launch_steps<64, kPlanes>(s, g, plan, src, part, x0, x1, am, pm, res);
-  else
-    launch_steps<128, kPlanes>(s, g, plan, src, part, x0, x1, am, pm, res);
+  if constexpr (std::is_same_v<R, __bf16>) {
+    if (planes == 1)
+      launch_steps<1>(s, g, plan, src, part, x, xt, next, am, pm, res);
+  }
+  if (planes == 2) launch_steps<2>(s, g, plan, src, part, x, xt, next, am, pm, res);
   timing_mark(ctx, stage, s, true);
   return check_launch(ctx, who);
 }
