@@ -68,6 +68,19 @@ __device__ __forceinline__ void take_new(const Source<T, MUON>& s, uint32_t b, u
   }
 }
 
+// One element, read once: the momentum is updated here.
+template <typename T, bool MUON>
+__device__ __forceinline__ float take_one(const Source<T, MUON>& s, uint32_t b, uint32_t row, uint32_t col) {
+  const float u = float(s.grad[int64_t(b) * s.gb + int64_t(row) * s.gr + col]);
+  if constexpr (MUON) {
+    float* p = s.momentum + int64_t(b) * s.mb + int64_t(row) * s.mr + col;
+    const float m = fmaf(s.mu, *p, u);
+    *p = m;
+    return s.nesterov ? fmaf(s.mu, m, u) : m;
+  }
+  return u;
+}
+
 // The same elements again, the momentum as take_new left it.
 template <typename T, bool MUON>
 __device__ __forceinline__ float take_again(const Source<T, MUON>& s, uint32_t b, uint32_t row, uint32_t col) {
@@ -99,6 +112,13 @@ __global__ __launch_bounds__(kThreads) void k_orth_norm(OrthShape g, Source<T, M
   if (threadIdx.x == 0) part[size_t(b) * g.parts + blockIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
+// The scale of X_0 from the sum of squares; a matrix of zeros stays one, one that holds an infinity or NaN gives NaN
+// throughout.
+__device__ __forceinline__ double first_scale(const OrthShape& g, double sum) {
+  const double norm = sqrt(sum) + double(g.eps);
+  return norm - norm == 0.0 ? (norm > 0.0 ? double(g.first) / norm : 0.0) : norm - norm;
+}
+
 // X_0 and its transpose in two planes each, zeros in the padding. A workgroup takes a 64 x 64 tile.
 template <typename T, bool MUON>
 __global__ __launch_bounds__(kThreads) void k_orth_start(OrthShape g, Source<T, MUON> src,
@@ -111,11 +131,7 @@ __global__ __launch_bounds__(kThreads) void k_orth_start(OrthShape g, Source<T, 
     double sum = 0.0;
     for (uint32_t i = threadIdx.x; i < g.parts; i += 64) sum += part[size_t(b) * g.parts + i];
     for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
-    if (threadIdx.x == 0) {
-      const double norm = sqrt(sum) + double(g.eps);
-      // a matrix of zeros stays one; one that holds an infinity or NaN gives NaN throughout
-      scale_s = norm - norm == 0.0 ? (norm > 0.0 ? double(g.first) / norm : 0.0) : norm - norm;
-    }
+    if (threadIdx.x == 0) scale_s = first_scale(g, sum);
   }
   __syncthreads();
   const double scale = scale_s;
@@ -595,6 +611,407 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_apply(
   }
 }
 
+// ---- matrices of at most 128 rows (or columns) --------------------------------------------------------------------------
+//
+// Where r is at most 128, A and P fit into one compute unit's LDS beside a strip of X's columns, and all three products of
+// a step can be done there: a workgroup keeps P, applies it to its strips and adds what they give to the next step's A.
+// With one workgroup to a matrix (c within one strip) a launch does all steps and the norm too; with several, each step is
+// a launch that adds the workgroups' parts of A first (in their order), finds P from them again in every workgroup and
+// leaves its own part for the next. All numbers are in two float16.
+
+// R: r padded to 64 or 128; S: the strip's columns. R / 32 x 2 waves: wave (w / 2, w % 2) has rows 32 (w / 2) .. of each
+// product and half of its columns.
+template <int R, int S>
+struct Small {
+  static constexpr int kT = 4 * R, kWaves = R / 16;
+  using LX = Tile<half, S>;
+  using LA = Tile<half, R>;
+  static constexpr int kX = R * LX::kRowBytes, kA = R * LA::kRowBytes;  // bytes of a plane
+  static constexpr int kLds = 2 * kX + 2 * kA;
+  static constexpr int kXBlocks = S / 64, kABlocks = R / 64;            // 32-column blocks of a wave
+  static constexpr int kEach = R * S / kT;                              // a strip's elements by each thread
+};
+
+// Depths 16 kk + 8 h .. + 7 of column at + l % 32 of a tile whose rows are the depths.
+template <typename L>
+__device__ __forceinline__ Vec<half, 8> frag_of_columns(const char* s, int at, int kk) {
+  // sixteen lanes read four rows of sixteen columns; lane j of them receives column j
+  const int l = threadIdx.x & 63, r = 16 * kk + 8 * (l >> 5) + ((l & 15) >> 2);
+  const int chunk = at / 8 + ((l >> 4) & 1) * 2 + ((l & 3) >> 1);
+  using s16x4 = Vec<short, 4>;
+  using P = __attribute__((address_space(3))) s16x4*;
+  const Vec<half, 4> a = __builtin_bit_cast(
+      Vec<half, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(s + L::at(r, chunk) + (l & 1) * 8)));
+  const Vec<half, 4> b = __builtin_bit_cast(
+      Vec<half, 4>, __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(s + L::at(r + 4, chunk) + (l & 1) * 8)));
+  return Vec<half, 8>{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+// acc[j] += rows row .. of `left` by rows (or, with COLUMNS, columns) col + 32 j .. of `right`, both in two planes, transposed
+// as the large products' blocks are. hi hi has a chain of sums of its own: a wave has one or two blocks, and the next
+// product on the same sums waits for the last.
+template <typename LL, int LP, typename LR, int RP, bool COLUMNS, int BLOCKS>
+__device__ __forceinline__ void small_product(const char* left, int row, const char* right, int col, int deep,
+                                              f32x16* acc) {
+  f32x16 rest[BLOCKS];
+#pragma unroll
+  for (int j = 0; j < BLOCKS; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) rest[j][e] = 0.0f;
+#pragma unroll 2
+  for (int kk = 0; kk < deep / 16; ++kk) {
+    const Vec<half, 8> ah = LL::frag(left, row, kk), al = LL::frag(left + LP, row, kk);
+#pragma unroll
+    for (int j = 0; j < BLOCKS; ++j) {
+      Vec<half, 8> bh, bl;
+      if constexpr (COLUMNS) {
+        bh = frag_of_columns<LR>(right, col + 32 * j, kk);
+        bl = frag_of_columns<LR>(right + RP, col + 32 * j, kk);
+      } else {
+        bh = LR::frag(right, col + 32 * j, kk);
+        bl = LR::frag(right + RP, col + 32 * j, kk);
+      }
+      acc[j] = mma(bh, ah, acc[j]);
+      rest[j] = mma(bl, ah, rest[j]);
+      rest[j] = mma(bh, al, rest[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < BLOCKS; ++j) acc[j] += rest[j];
+}
+
+// The lane's place in a tile of two planes: row row + l % 32, the four columns col + 8 q + 4 (l / 32) .. .
+template <typename L>
+__device__ __forceinline__ Vec<half, 4>& at_four(char* s, int row, int col, int q) {
+  const int l = threadIdx.x & 63, c = col + 8 * q + 4 * (l >> 5);
+  return *reinterpret_cast<Vec<half, 4>*>(s + L::at(row + (l & 31), c / 8) + (c % 8) * 2);
+}
+
+template <typename L, int PLANE>
+__device__ __forceinline__ void put_four(char* s, int row, int col, int q, Vec<float, 4> v) {
+  Vec<half, 4> hi, lo;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    half h, w;
+    split(v[k], &h, &w);
+    hi[k] = h;
+    lo[k] = w;
+  }
+  at_four<L>(s, row, col, q) = hi;
+  at_four<L>(s + PLANE, row, col, q) = lo;
+}
+
+template <typename L, int PLANE>
+__device__ __forceinline__ Vec<float, 4> get_four(char* s, int row, int col, int q) {
+  const Vec<half, 4> hi = at_four<L>(s, row, col, q), lo = at_four<L>(s + PLANE, row, col, q);
+  Vec<float, 4> v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = float(hi[k]) + float(lo[k]);
+  return v;
+}
+
+__device__ __forceinline__ Vec<float, 4> four_of(const f32x16& a, int q) {
+  return Vec<float, 4>{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+}
+
+// The factors of one step (see launch_steps): A = sums times a_scale; P = p_in A + p_sum A A^T; X' = x_in X + x_sum P X.
+struct SmallStep {
+  float a_scale, p_in, p_sum, x_in, x_sum;
+};
+
+struct SmallPlan {
+  int steps;
+  SmallStep step[GSR_ORTHOGONALIZE_MAX_STEPS];
+};
+
+template <int N>
+__device__ __forceinline__ void clear(f32x16 (&a)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) a[j][e] = 0.0f;
+}
+
+// From the wave's sums of A: A to LDS, P = p_in A + p_sum A A^T in its place.
+template <typename C>
+__device__ __forceinline__ void small_to_p(char* as, int row, int col, f32x16 (&a)[C::kABlocks], const SmallStep& st) {
+  using L = typename C::LA;
+#pragma unroll
+  for (int j = 0; j < C::kABlocks; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) put_four<L, C::kA>(as, row, col + 32 * j, q, four_of(a[j], q) * st.a_scale);
+  __syncthreads();
+  f32x16 s[C::kABlocks];
+  clear(s);
+  small_product<L, C::kA, L, C::kA, false, C::kABlocks>(as, row, as, col, C::kWaves * 16, s);
+#pragma unroll
+  for (int j = 0; j < C::kABlocks; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const Vec<float, 4> v = get_four<L, C::kA>(as, row, col + 32 * j, q);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[j][4 * q + k] = fmaf(st.p_in, v[k], s[j][4 * q + k] * st.p_sum);
+    }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < C::kABlocks; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) put_four<L, C::kA>(as, row, col + 32 * j, q, four_of(s[j], q));
+  __syncthreads();
+}
+
+// The wave's sums of P X to X' = x_in X + x_sum P X, X from LDS.
+template <typename C>
+__device__ __forceinline__ void small_next(char* xs, int row, int col, f32x16 (&x)[C::kXBlocks], const SmallStep& st) {
+#pragma unroll
+  for (int j = 0; j < C::kXBlocks; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const Vec<float, 4> v = get_four<typename C::LX, C::kX>(xs, row, col + 32 * j, q);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[j][4 * q + k] = fmaf(st.x_in, v[k], x[j][4 * q + k] * st.x_sum);
+    }
+}
+
+// The wave's part of the result, from row `row` and column `col` of X on.
+template <bool UPDATE, typename T, int N>
+__device__ __forceinline__ void small_result(const OrthShape& g, const Result<T>& res, uint64_t b, uint32_t row,
+                                             uint64_t col, const f32x16 (&x)[N]) {
+  const int l = threadIdx.x & 63;
+  T* to = res.p + int64_t(b) * res.mat;
+  const uint32_t i = row + (l & 31);
+  if (i >= g.r) return;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    float old[16];
+    T* at[4];
+    int n[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint64_t c = col + 32 * j + 8 * q + 4 * (l >> 5);
+      n[q] = c < g.c ? int(min(uint64_t(4), g.c - c)) : 0;
+      at[q] = to + (g.tall ? int64_t(c) * res.row + i : int64_t(i) * res.row + int64_t(c));
+    }
+    if constexpr (UPDATE)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (!g.tall)
+          load_f32<4>(at[q], n[q], old + 4 * q);
+        else
+#pragma unroll
+          for (int k = 0; k < 4; ++k) old[4 * q + k] = k < n[q] ? float(at[q][k * res.row]) : 0.0f;
+      }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = UPDATE ? res.decay * old[4 * q + k] - res.lr * x[j][4 * q + k] : x[j][4 * q + k];
+      if (!g.tall)
+        store_f32<4>(at[q], n[q], o);
+      else
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < n[q]) at[q][k * res.row] = T(o[k]);
+    }
+  }
+}
+
+// Where element e of a strip's thread lies in X: threads walk along the source's rows.
+template <typename C>
+__device__ __forceinline__ void strip_place(bool tall, int e, int* i, int* j) {
+  const int at = e * C::kT + int(threadIdx.x);
+  constexpr int kRows = C::kWaves * 16, kCols = C::kEach * C::kT / kRows;
+  if (tall) {
+    *j = at / kRows;
+    *i = at % kRows;
+  } else {
+    *i = at / kCols;
+    *j = at % kCols;
+  }
+}
+
+// A matrix in one launch.
+template <int R, int S, typename T, bool MUON, typename RT>
+__global__ __launch_bounds__(4 * R) void k_orth_one(OrthShape g, SmallPlan plan, Source<T, MUON> src,
+                                                              Result<RT> res) {
+  using C = Small<R, S>;
+  __shared__ alignas(16) char xs[2 * C::kX];
+  __shared__ alignas(16) char as[2 * C::kA];
+  __shared__ double sums[C::kWaves];
+  const uint32_t b = blockIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  const int row = 32 * (wave / 2), xcol = (wave % 2) * (S / 2), acol = (wave % 2) * (R / 2);
+  {
+    float u[C::kEach];
+    double sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < C::kEach; ++e) {
+      int i, j;
+      strip_place<C>(g.tall, e, &i, &j);
+      const uint32_t sr = g.tall ? j : i, sc = g.tall ? i : j;
+      u[e] = sr < g.rows && sc < g.cols ? take_one(src, b, sr, sc) : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < C::kEach; ++e) sum = fma(double(u[e]), double(u[e]), sum);
+    for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
+    if ((threadIdx.x & 63) == 0) sums[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < C::kWaves; ++k) sum += sums[k];
+    const double scale = first_scale(g, sum);
+#pragma unroll
+    for (int e = 0; e < C::kEach; ++e) {
+      int i, j;
+      strip_place<C>(g.tall, e, &i, &j);
+      half hi, lo;
+      split(float(double(u[e]) * scale), &hi, &lo);
+      const int at = C::LX::at(i, j / 8) + (j % 8) * 2;
+      *reinterpret_cast<half*>(xs + at) = hi;
+      *reinterpret_cast<half*>(xs + C::kX + at) = lo;
+    }
+    __syncthreads();
+  }
+  for (int k = 0; k < plan.steps; ++k) {
+    const SmallStep st = plan.step[k];
+    f32x16 a[C::kABlocks];
+    clear(a);
+    small_product<typename C::LX, C::kX, typename C::LX, C::kX, false, C::kABlocks>(xs, row, xs, acol, S, a);
+    small_to_p<C>(as, row, acol, a, st);
+    f32x16 x[C::kXBlocks];
+    clear(x);
+    small_product<typename C::LA, C::kA, typename C::LX, C::kX, true, C::kXBlocks>(as, row, xs, xcol, R, x);
+    small_next<C>(xs, row, xcol, x, st);
+    if (k + 1 == plan.steps) {
+      small_result<MUON>(g, res, b, row, xcol, x);
+      return;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < C::kXBlocks; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) put_four<typename C::LX, C::kX>(xs, row, xcol + 32 * j, q, four_of(x[j], q));
+    __syncthreads();
+  }
+}
+
+// X_0's strips (FIRST), or one step on them, and the next step's part of A. Workgroup w of a matrix has strips w, w + ways,
+// ...; x: [batch][2][R][cp]; parts_in, parts_out: [batch][ways][R][R] float32.
+template <int R, int S, bool FIRST, bool LAST, typename T, bool MUON, typename RT>
+__global__ __launch_bounds__(4 * R) void k_orth_strips(OrthShape g, SmallStep st, Source<T, MUON> src,
+                                                                 Result<RT> res, const double* __restrict__ norm,
+                                                                 half* __restrict__ x, uint32_t ways,
+                                                                 const float* __restrict__ parts_in,
+                                                                 float* __restrict__ parts_out) {
+  using C = Small<R, S>;
+  __shared__ alignas(16) char xs[2 * C::kX];
+  __shared__ alignas(16) char as[2 * C::kA];
+  const uint32_t b = blockIdx.y;
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), l = threadIdx.x & 63;
+  const int row = 32 * (wave / 2), xcol = (wave % 2) * (S / 2), acol = (wave % 2) * (R / 2);
+  const uint32_t strips = uint32_t(g.cp / S);
+  const uint64_t plane = uint64_t(R) * g.cp;
+  x += b * 2 * plane;
+  double scale = 0.0;
+  if constexpr (FIRST) {
+    double sum = 0.0;  // every wave for itself, in the same order
+    for (uint32_t i = l; i < g.parts; i += 64) sum += norm[size_t(b) * g.parts + i];
+    for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
+    scale = first_scale(g, sum);
+  } else {
+    f32x16 a[C::kABlocks];
+    clear(a);
+    for (uint32_t w = 0; w < ways; ++w) {
+      const float* in = parts_in + (size_t(b) * ways + w) * R * R + (row + (l & 31)) * R + acol + 4 * (l >> 5);
+#pragma unroll
+      for (int j = 0; j < C::kABlocks; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const Vec<float, 4> v = *reinterpret_cast<const Vec<float, 4>*>(in + 32 * j + 8 * q);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) a[j][4 * q + k] += v[k];
+        }
+    }
+    small_to_p<C>(as, row, acol, a, st);
+  }
+  f32x16 next[C::kABlocks];
+  clear(next);
+  for (uint32_t strip = blockIdx.x; strip < strips; strip += ways) {
+    const uint64_t c0 = uint64_t(strip) * S;
+    if constexpr (FIRST) {
+      float u[C::kEach];
+#pragma unroll
+      for (int e = 0; e < C::kEach; ++e) {
+        int i, j;
+        strip_place<C>(g.tall, e, &i, &j);
+        const uint32_t sr = g.tall ? uint32_t(c0) + j : i, sc = g.tall ? i : uint32_t(c0) + j;
+        u[e] = sr < g.rows && sc < g.cols ? take_again(src, b, sr, sc) : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < C::kEach; ++e) {
+        int i, j;
+        strip_place<C>(g.tall, e, &i, &j);
+        half hi, lo;
+        split(float(double(u[e]) * scale), &hi, &lo);
+        const int at = C::LX::at(i, j / 8) + (j % 8) * 2;
+        *reinterpret_cast<half*>(xs + at) = hi;
+        *reinterpret_cast<half*>(xs + C::kX + at) = lo;
+      }
+      __syncthreads();
+      constexpr int kChunks = R * S / 8;
+      for (int e = threadIdx.x; e < kChunks; e += C::kT) {
+        const int i = e / (S / 8), c = e % (S / 8), at = C::LX::at(i, c);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          *reinterpret_cast<u32x4*>(x + p * plane + i * g.cp + c0 + 8 * c) =
+              *reinterpret_cast<const u32x4*>(xs + p * C::kX + at);
+      }
+    } else {
+      constexpr int kChunks = R * S / 8;
+#pragma unroll
+      for (int e = threadIdx.x; e < kChunks; e += C::kT) {
+        const int i = e / (S / 8), c = e % (S / 8), at = C::LX::at(i, c);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          *reinterpret_cast<u32x4*>(xs + p * C::kX + at) =
+              *reinterpret_cast<const u32x4*>(x + p * plane + i * g.cp + c0 + 8 * c);
+      }
+      __syncthreads();
+      f32x16 v[C::kXBlocks];
+      clear(v);
+      small_product<typename C::LA, C::kA, typename C::LX, C::kX, true, C::kXBlocks>(as, row, xs, xcol, R, v);
+      small_next<C>(xs, row, xcol, v, st);
+      if constexpr (LAST) {
+        small_result<MUON>(g, res, b, row, c0 + xcol, v);
+      } else {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < C::kXBlocks; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) put_four<typename C::LX, C::kX>(xs, row, xcol + 32 * j, q, four_of(v[j], q));
+        __syncthreads();
+        for (int e = threadIdx.x; e < kChunks; e += C::kT) {
+          const int i = e / (S / 8), c = e % (S / 8), at = C::LX::at(i, c);
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            *reinterpret_cast<u32x4*>(x + p * plane + i * g.cp + c0 + 8 * c) =
+                *reinterpret_cast<const u32x4*>(xs + p * C::kX + at);
+        }
+      }
+    }
+    if constexpr (!LAST)
+      small_product<typename C::LX, C::kX, typename C::LX, C::kX, false, C::kABlocks>(xs, row, xs, acol, S, next);
+    __syncthreads();
+  }
+  if constexpr (!LAST) {
+    float* out = parts_out + (size_t(b) * ways + blockIdx.x) * R * R + (row + (l & 31)) * R + acol + 4 * (l >> 5);
+#pragma unroll
+    for (int j = 0; j < C::kABlocks; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *reinterpret_cast<Vec<float, 4>*>(out + 32 * j + 8 * q) = four_of(next[j], q);
+  }
+}
+
 struct Step {
   float a, b, c;
 };
@@ -715,6 +1132,28 @@ void launch_steps(hipStream_t s, const OrthShape& g, const Plan& plan, const Sou
   }
 }
 
+template <int R, int S, typename T, bool MUON, typename RT>
+void launch_one(hipStream_t s, const OrthShape& g, const SmallPlan& plan, const Source<T, MUON>& src,
+                const Result<RT>& res) {
+  hipLaunchKernelGGL((k_orth_one<R, S, T, MUON, RT>), dim3(g.batch), dim3(Small<R, S>::kT), 0, s, g, plan, src, res);
+}
+
+template <int R, int S, typename T, bool MUON, typename RT>
+void launch_strips(hipStream_t s, const OrthShape& g, const SmallPlan& plan, const Source<T, MUON>& src, double* norm,
+                   half* x, uint32_t ways, float* parts, const Result<RT>& res) {
+  constexpr int kT = Small<R, S>::kT;
+  hipLaunchKernelGGL((k_orth_norm<T, MUON>), dim3(g.parts, g.batch), dim3(kThreads), 0, s, g, src, norm);
+  float* other = parts + size_t(g.batch) * ways * R * R;
+  const dim3 grid(ways, g.batch);
+  auto launch = [&](auto kernel, const SmallStep& st) {
+    hipLaunchKernelGGL(kernel, grid, dim3(kT), 0, s, g, st, src, res, norm, x, ways, other, parts);
+    std::swap(parts, other);
+  };
+  launch(k_orth_strips<R, S, true, false, T, MUON, RT>, SmallStep{});
+  for (int k = 0; k + 1 < plan.steps; ++k) launch(k_orth_strips<R, S, false, false, T, MUON, RT>, plan.step[k]);
+  launch(k_orth_strips<R, S, false, true, T, MUON, RT>, plan.step[plan.steps - 1]);
+}
+
 // The checks that both entry points share, and the shape of the work; an empty call leaves g->batch 0.
 gsr_status check_desc(gsr_ctx* ctx, const gsr_newton_schulz* d, const char* who, Plan* plan) {
   if (!d) return fail(ctx, GSR_EINVAL, "%s: null descriptor", who);
@@ -728,6 +1167,49 @@ gsr_status check_desc(gsr_ctx* ctx, const gsr_newton_schulz* d, const char* who,
   if (d->rows >= (1u << 20) || d->cols >= (1u << 20) || uint64_t(d->rows) * d->cols >= (uint64_t(1) << 31))
     return fail(ctx, GSR_EOVERFLOW, "%s: rows or cols >= 2^20 or rows * cols >= 2^31", who);
   return GSR_OK;
+}
+
+// Matrices of at most 128 rows (or columns). Up to 128 columns are one strip: one launch. More are dealt to at most 8 (of
+// 128 rows) or 16 workgroups a matrix, whose parts of A every workgroup adds.
+template <typename T, bool MUON, typename RT>
+gsr_status run_small(gsr_ctx* ctx, hipStream_t s, OrthShape g, const Plan& plan, const Source<T, MUON>& src,
+                     const Result<RT>& res, int stage, const char* who) {
+  SmallPlan sp;
+  sp.steps = plan.steps;
+  for (int k = 0; k < plan.steps; ++k) {
+    const Step& c = plan.step[k];
+    const int ex = plan.x_exp[k], ea = plan.a_exp[k], ep = plan.p_exp[k], en = plan.x_exp[k + 1];
+    sp.step[k] = SmallStep{std::ldexp(1.0f, ea - 2 * ex), std::ldexp(c.b, ep - ea), std::ldexp(c.c, ep - 2 * ea),
+                           std::ldexp(c.a, en - ex), std::ldexp(1.0f, en - ep - ex)};
+  }
+  const bool narrow = g.r <= 64;
+  if (g.c <= 128) {
+    timing_mark(ctx, stage, s, false);
+    if (g.c <= 64)
+      launch_one<64, 64>(s, g, sp, src, res);
+    else if (narrow)
+      launch_one<64, 128>(s, g, sp, src, res);
+    else
+      launch_one<128, 128>(s, g, sp, src, res);
+    timing_mark(ctx, stage, s, true);
+    return check_launch(ctx, who);
+  }
+  g.cp = round_up(g.c, 128);
+  const uint32_t R = narrow ? 64 : 128, ways = uint32_t(std::min<uint64_t>(g.cp / 128, narrow ? 16 : 8));
+  const size_t norms = round_up(size_t(g.batch) * g.parts, 2), plane = size_t(R) * g.cp;
+  gsr_status st = grow(ctx, ctx->arena.feat_part,
+                       norms * sizeof(double) + g.batch * (2 * plane * sizeof(half) + 2 * size_t(ways) * R * R * sizeof(float)));
+  if (st) return st;
+  double* norm = static_cast<double*>(ctx->arena.feat_part.ptr);
+  half* x = reinterpret_cast<half*>(norm + norms);
+  float* parts = reinterpret_cast<float*>(x + 2 * plane * g.batch);
+  timing_mark(ctx, stage, s, false);
+  if (narrow)
+    launch_strips<64, 128>(s, g, sp, src, norm, x, ways, parts, res);
+  else
+    launch_strips<128, 128>(s, g, sp, src, norm, x, ways, parts, res);
+  timing_mark(ctx, stage, s, true);
+  return check_launch(ctx, who);
 }
 
 template <typename T, bool MUON, typename R>
@@ -746,6 +1228,7 @@ gsr_status run(gsr_ctx* ctx, hipStream_t s, const gsr_newton_schulz* d, const Pl
   g.first = std::ldexp(1.0f, plan.x_exp[0]);
   g.by_vec.set((d->cols + kNormVec - 1) / kNormVec);
   g.parts = uint32_t(std::min<uint64_t>(256, (uint64_t(g.by_vec.d) * g.rows + 4 * kThreads - 1) / (4 * kThreads)));
+  if (g.r <= 128) return run_small(ctx, s, g, plan, src, res, stage, who);
   g.rp = round_up(g.r, 64);
   g.cp = round_up(g.c, 64);
   const size_t plane = g.rp * g.cp, square = g.rp * g.rp, parts = round_up(size_t(g.batch) * g.parts, 2);
