@@ -619,14 +619,29 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_apply(
 // a launch that adds the workgroups' parts of A first (in their order), finds P from them again in every workgroup and
 // leaves its own part for the next. All numbers are in two float16.
 
+// An LDS tile of R rows of S values, in panels of at most 128 columns.
+template <int R, int S>
+struct Panels {
+  using L = Tile<half, (S < 128 ? S : 128)>;
+  static constexpr int kRowChunks = L::kChunks;
+  __device__ static __forceinline__ int at(int r, int chunk) {
+    return chunk / kRowChunks * (R * L::kRowBytes) + L::at(r, chunk % kRowChunks);
+  }
+  // Depths 16 kk + 8 h .. + 7 of row r0 + l % 32.
+  __device__ static __forceinline__ Vec<half, 8> frag(const char* s, int r0, int kk) {
+    const int l = threadIdx.x & 63;
+    return *reinterpret_cast<const Vec<half, 8>*>(s + at(r0 + (l & 31), 2 * kk + (l >> 5)));
+  }
+};
+
 // R: r padded to 64 or 128; S: the strip's columns. R / 32 x 2 waves: wave (w / 2, w % 2) has rows 32 (w / 2) .. of each
 // product and half of its columns.
 template <int R, int S>
 struct Small {
   static constexpr int kT = 4 * R, kWaves = R / 16;
-  using LX = Tile<half, S>;
+  using LX = Panels<R, S>;
   using LA = Tile<half, R>;
-  static constexpr int kX = R * LX::kRowBytes, kA = R * LA::kRowBytes;  // bytes of a plane
+  static constexpr int kX = R * S * 2, kA = R * LA::kRowBytes;  // bytes of a plane
   static constexpr int kLds = 2 * kX + 2 * kA;
   static constexpr int kXBlocks = S / 64, kABlocks = R / 64;            // 32-column blocks of a wave
   static constexpr int kEach = R * S / kT;                              // a strip's elements by each thread
@@ -648,18 +663,18 @@ __device__ __forceinline__ Vec<half, 8> frag_of_columns(const char* s, int at, i
 }
 
 // acc[j] += rows row .. of `left` by rows (or, with COLUMNS, columns) col + 32 j .. of `right`, both in two planes, transposed
-// as the large products' blocks are. hi hi has a chain of sums of its own: a wave has one or two blocks, and the next
-// product on the same sums waits for the last.
-template <typename LL, int LP, typename LR, int RP, bool COLUMNS, int BLOCKS>
-__device__ __forceinline__ void small_product(const char* left, int row, const char* right, int col, int deep,
-                                              f32x16* acc) {
-  f32x16 rest[BLOCKS];
+// as the large products' blocks are. With few blocks hi hi has a chain of sums of its own: the next product on the same
+// sums waits for the last.
+template <typename LL, int LP, typename LR, int RP, bool COLUMNS, int BLOCKS, int DEEP>
+__device__ __forceinline__ void small_product(const char* left, int row, const char* right, int col, f32x16* acc) {
+  constexpr int kRest = BLOCKS <= 2 ? BLOCKS : 0;
+  f32x16 rest[kRest + 1];
 #pragma unroll
-  for (int j = 0; j < BLOCKS; ++j)
+  for (int j = 0; j < kRest; ++j)
 #pragma unroll
     for (int e = 0; e < 16; ++e) rest[j][e] = 0.0f;
-#pragma unroll 2
-  for (int kk = 0; kk < deep / 16; ++kk) {
+#pragma unroll
+  for (int kk = 0; kk < DEEP / 16; ++kk) {
     const Vec<half, 8> ah = LL::frag(left, row, kk), al = LL::frag(left + LP, row, kk);
 #pragma unroll
     for (int j = 0; j < BLOCKS; ++j) {
@@ -671,13 +686,14 @@ __device__ __forceinline__ void small_product(const char* left, int row, const c
         bh = LR::frag(right, col + 32 * j, kk);
         bl = LR::frag(right + RP, col + 32 * j, kk);
       }
+      f32x16& low = kRest ? rest[kRest ? j : 0] : acc[j];
       acc[j] = mma(bh, ah, acc[j]);
-      rest[j] = mma(bl, ah, rest[j]);
-      rest[j] = mma(bh, al, rest[j]);
+      low = mma(bl, ah, low);
+      low = mma(bh, al, low);
     }
   }
 #pragma unroll
-  for (int j = 0; j < BLOCKS; ++j) acc[j] += rest[j];
+  for (int j = 0; j < kRest; ++j) acc[j] += rest[j];
 }
 
 // The lane's place in a tile of two planes: row row + l % 32, the four columns col + 8 q + 4 (l / 32) .. .
@@ -743,7 +759,7 @@ __device__ __forceinline__ void small_to_p(char* as, int row, int col, f32x16 (&
   __syncthreads();
   f32x16 s[C::kABlocks];
   clear(s);
-  small_product<L, C::kA, L, C::kA, false, C::kABlocks>(as, row, as, col, C::kWaves * 16, s);
+  small_product<L, C::kA, L, C::kA, false, C::kABlocks, C::kWaves * 16>(as, row, as, col, s);
 #pragma unroll
   for (int j = 0; j < C::kABlocks; ++j)
 #pragma unroll
@@ -830,6 +846,18 @@ __device__ __forceinline__ void strip_place(bool tall, int e, int* i, int* j) {
   }
 }
 
+// The parts of A added: a thread's four adjacent elements, eight loads in flight. parts: [batch][ways][R R], its first part
+// replaced.
+template <int R>
+__global__ __launch_bounds__(256) void k_orth_sum(float* parts, uint32_t ways) {
+  using F4 = Vec<float, 4>;
+  F4* at = reinterpret_cast<F4*>(parts + size_t(blockIdx.y) * ways * R * R) + blockIdx.x * 256 + threadIdx.x;
+  F4 sum = *at;
+#pragma unroll 8
+  for (uint32_t w = 1; w < ways; ++w) sum += at[size_t(w) * (R * R / 4)];
+  *at = sum;
+}
+
 // A matrix in one launch.
 template <int R, int S, typename T, bool MUON, typename RT>
 __global__ __launch_bounds__(4 * R) void k_orth_one(OrthShape g, SmallPlan plan, Source<T, MUON> src,
@@ -876,11 +904,11 @@ __global__ __launch_bounds__(4 * R) void k_orth_one(OrthShape g, SmallPlan plan,
     const SmallStep st = plan.step[k];
     f32x16 a[C::kABlocks];
     clear(a);
-    small_product<typename C::LX, C::kX, typename C::LX, C::kX, false, C::kABlocks>(xs, row, xs, acol, S, a);
+    small_product<typename C::LX, C::kX, typename C::LX, C::kX, false, C::kABlocks, S>(xs, row, xs, acol, a);
     small_to_p<C>(as, row, acol, a, st);
     f32x16 x[C::kXBlocks];
     clear(x);
-    small_product<typename C::LA, C::kA, typename C::LX, C::kX, true, C::kXBlocks>(as, row, xs, xcol, R, x);
+    small_product<typename C::LA, C::kA, typename C::LX, C::kX, true, C::kXBlocks, R>(as, row, xs, xcol, x);
     small_next<C>(xs, row, xcol, x, st);
     if (k + 1 == plan.steps) {
       small_result<MUON>(g, res, b, row, xcol, x);
@@ -895,13 +923,14 @@ __global__ __launch_bounds__(4 * R) void k_orth_one(OrthShape g, SmallPlan plan,
   }
 }
 
-// X_0's strips (FIRST), or one step on them, and the next step's part of A. Workgroup w of a matrix has strips w, w + ways,
-// ...; x: [batch][2][R][cp]; parts_in, parts_out: [batch][ways][R][R] float32.
+// X_0's strips (FIRST), or one step on them, and the next step's part of A. Workgroup w of a matrix has every gridDim.x-th
+// strip from w on. x: [batch][2][R][cp]; parts_in: `parts` parts of A to be added, [R][R] float32, part_stride from matrix to
+// matrix; parts_out: [batch][gridDim.x][R][R].
 template <int R, int S, bool FIRST, bool LAST, typename T, bool MUON, typename RT>
 __global__ __launch_bounds__(4 * R) void k_orth_strips(OrthShape g, SmallStep st, Source<T, MUON> src,
                                                                  Result<RT> res, const double* __restrict__ norm,
-                                                                 half* __restrict__ x, uint32_t ways,
-                                                                 const float* __restrict__ parts_in,
+                                                                 half* x, const float* __restrict__ parts_in,
+                                                                 uint32_t parts, size_t part_stride,
                                                                  float* __restrict__ parts_out) {
   using C = Small<R, S>;
   __shared__ alignas(16) char xs[2 * C::kX];
@@ -913,16 +942,46 @@ __global__ __launch_bounds__(4 * R) void k_orth_strips(OrthShape g, SmallStep st
   const uint64_t plane = uint64_t(R) * g.cp;
   x += b * 2 * plane;
   double scale = 0.0;
+  // a strip's chunks of 16 bytes, in both planes
+  constexpr int kChunks = R * S / 8 / C::kT;
+  u32x4 strip_of[2][kChunks];
+  auto chunk = [&](int e, int* i, int* c) {
+    const int at = e * C::kT + int(threadIdx.x);
+    *i = at / (S / 8);
+    *c = at % (S / 8);
+  };
+  auto fetch = [&](uint64_t c0) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int e = 0; e < kChunks; ++e) {
+        int i, c;
+        chunk(e, &i, &c);
+        strip_of[p][e] = *reinterpret_cast<const u32x4*>(x + p * plane + i * g.cp + c0 + 8 * c);
+      }
+  };
+  auto store = [&](uint64_t c0) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int e = 0; e < kChunks; ++e) {
+        int i, c;
+        chunk(e, &i, &c);
+        *reinterpret_cast<u32x4*>(x + p * plane + i * g.cp + c0 + 8 * c) =
+            *reinterpret_cast<const u32x4*>(xs + p * C::kX + C::LX::at(i, c));
+      }
+  };
   if constexpr (FIRST) {
     double sum = 0.0;  // every wave for itself, in the same order
     for (uint32_t i = l; i < g.parts; i += 64) sum += norm[size_t(b) * g.parts + i];
     for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
     scale = first_scale(g, sum);
   } else {
+    fetch(uint64_t(blockIdx.x) * S);
     f32x16 a[C::kABlocks];
     clear(a);
-    for (uint32_t w = 0; w < ways; ++w) {
-      const float* in = parts_in + (size_t(b) * ways + w) * R * R + (row + (l & 31)) * R + acol + 4 * (l >> 5);
+    const float* in = parts_in + size_t(b) * part_stride + (row + (l & 31)) * R + acol + 4 * (l >> 5);
+    for (uint32_t w = 0; w < parts; ++w, in += R * R) {
 #pragma unroll
       for (int j = 0; j < C::kABlocks; ++j)
 #pragma unroll
@@ -936,7 +995,7 @@ __global__ __launch_bounds__(4 * R) void k_orth_strips(OrthShape g, SmallStep st
   }
   f32x16 next[C::kABlocks];
   clear(next);
-  for (uint32_t strip = blockIdx.x; strip < strips; strip += ways) {
+  for (uint32_t strip = blockIdx.x; strip < strips; strip += gridDim.x) {
     const uint64_t c0 = uint64_t(strip) * S;
     if constexpr (FIRST) {
       float u[C::kEach];
@@ -958,28 +1017,21 @@ __global__ __launch_bounds__(4 * R) void k_orth_strips(OrthShape g, SmallStep st
         *reinterpret_cast<half*>(xs + C::kX + at) = lo;
       }
       __syncthreads();
-      constexpr int kChunks = R * S / 8;
-      for (int e = threadIdx.x; e < kChunks; e += C::kT) {
-        const int i = e / (S / 8), c = e % (S / 8), at = C::LX::at(i, c);
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-          *reinterpret_cast<u32x4*>(x + p * plane + i * g.cp + c0 + 8 * c) =
-              *reinterpret_cast<const u32x4*>(xs + p * C::kX + at);
-      }
+      store(c0);
     } else {
-      constexpr int kChunks = R * S / 8;
 #pragma unroll
-      for (int e = threadIdx.x; e < kChunks; e += C::kT) {
-        const int i = e / (S / 8), c = e % (S / 8), at = C::LX::at(i, c);
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-          *reinterpret_cast<u32x4*>(xs + p * C::kX + at) =
-              *reinterpret_cast<const u32x4*>(x + p * plane + i * g.cp + c0 + 8 * c);
-      }
+        for (int e = 0; e < kChunks; ++e) {
+          int i, c;
+          chunk(e, &i, &c);
+          *reinterpret_cast<u32x4*>(xs + p * C::kX + C::LX::at(i, c)) = strip_of[p][e];
+        }
+      if (strip + gridDim.x < strips) fetch(c0 + uint64_t(gridDim.x) * S);  // on its way while this one is multiplied
       __syncthreads();
       f32x16 v[C::kXBlocks];
       clear(v);
-      small_product<typename C::LA, C::kA, typename C::LX, C::kX, true, C::kXBlocks>(as, row, xs, xcol, R, v);
+      small_product<typename C::LA, C::kA, typename C::LX, C::kX, true, C::kXBlocks, R>(as, row, xs, xcol, v);
       small_next<C>(xs, row, xcol, v, st);
       if constexpr (LAST) {
         small_result<MUON>(g, res, b, row, c0 + xcol, v);
@@ -990,21 +1042,15 @@ __global__ __launch_bounds__(4 * R) void k_orth_strips(OrthShape g, SmallStep st
 #pragma unroll
           for (int q = 0; q < 4; ++q) put_four<typename C::LX, C::kX>(xs, row, xcol + 32 * j, q, four_of(v[j], q));
         __syncthreads();
-        for (int e = threadIdx.x; e < kChunks; e += C::kT) {
-          const int i = e / (S / 8), c = e % (S / 8), at = C::LX::at(i, c);
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-            *reinterpret_cast<u32x4*>(x + p * plane + i * g.cp + c0 + 8 * c) =
-                *reinterpret_cast<const u32x4*>(xs + p * C::kX + at);
-        }
+        store(c0);
       }
     }
     if constexpr (!LAST)
-      small_product<typename C::LX, C::kX, typename C::LX, C::kX, false, C::kABlocks>(xs, row, xs, acol, S, next);
+      small_product<typename C::LX, C::kX, typename C::LX, C::kX, false, C::kABlocks, S>(xs, row, xs, acol, next);
     __syncthreads();
   }
   if constexpr (!LAST) {
-    float* out = parts_out + (size_t(b) * ways + blockIdx.x) * R * R + (row + (l & 31)) * R + acol + 4 * (l >> 5);
+    float* out = parts_out + (size_t(b) * gridDim.x + blockIdx.x) * R * R + (row + (l & 31)) * R + acol + 4 * (l >> 5);
 #pragma unroll
     for (int j = 0; j < C::kABlocks; ++j)
 #pragma unroll
@@ -1145,13 +1191,18 @@ void launch_strips(hipStream_t s, const OrthShape& g, const SmallPlan& plan, con
   hipLaunchKernelGGL((k_orth_norm<T, MUON>), dim3(g.parts, g.batch), dim3(kThreads), 0, s, g, src, norm);
   float* other = parts + size_t(g.batch) * ways * R * R;
   const dim3 grid(ways, g.batch);
+  // every workgroup adds up to four parts itself; more are added by a launch of their own
+  const bool sum = ways > 4;
   auto launch = [&](auto kernel, const SmallStep& st) {
-    hipLaunchKernelGGL(kernel, grid, dim3(kT), 0, s, g, st, src, res, norm, x, ways, other, parts);
+    hipLaunchKernelGGL(kernel, grid, dim3(kT), 0, s, g, st, src, res, norm, x, other, sum ? 1 : ways,
+                       size_t(ways) * R * R, parts);
+    if (sum) hipLaunchKernelGGL((k_orth_sum<R>), dim3(R * R / 1024, g.batch), dim3(256), 0, s, parts, ways);
     std::swap(parts, other);
   };
   launch(k_orth_strips<R, S, true, false, T, MUON, RT>, SmallStep{});
   for (int k = 0; k + 1 < plan.steps; ++k) launch(k_orth_strips<R, S, false, false, T, MUON, RT>, plan.step[k]);
-  launch(k_orth_strips<R, S, false, true, T, MUON, RT>, plan.step[plan.steps - 1]);
+  hipLaunchKernelGGL((k_orth_strips<R, S, false, true, T, MUON, RT>), grid, dim3(kT), 0, s, g, plan.step[plan.steps - 1],
+                     src, res, norm, x, other, sum ? 1 : ways, size_t(ways) * R * R, parts);
 }
 
 // The checks that both entry points share, and the shape of the work; an empty call leaves g->batch 0.
@@ -1169,8 +1220,8 @@ gsr_status check_desc(gsr_ctx* ctx, const gsr_newton_schulz* d, const char* who,
   return GSR_OK;
 }
 
-// Matrices of at most 128 rows (or columns). Up to 128 columns are one strip: one launch. More are dealt to at most 8 (of
-// 128 rows) or 16 workgroups a matrix, whose parts of A every workgroup adds.
+// Matrices of at most 128 rows (or columns). What one workgroup's LDS holds (128 columns, or 256 of at most 64 rows) is done
+// in one launch; more columns are dealt to at most 64 workgroups a matrix by strips of 128.
 template <typename T, bool MUON, typename RT>
 gsr_status run_small(gsr_ctx* ctx, hipStream_t s, OrthShape g, const Plan& plan, const Source<T, MUON>& src,
                      const Result<RT>& res, int stage, const char* who) {
@@ -1183,19 +1234,21 @@ gsr_status run_small(gsr_ctx* ctx, hipStream_t s, OrthShape g, const Plan& plan,
                            std::ldexp(c.a, en - ex), std::ldexp(1.0f, en - ep - ex)};
   }
   const bool narrow = g.r <= 64;
-  if (g.c <= 128) {
+  if (g.c <= 128 || (narrow && g.c <= 256)) {
     timing_mark(ctx, stage, s, false);
     if (g.c <= 64)
       launch_one<64, 64>(s, g, sp, src, res);
-    else if (narrow)
+    else if (!narrow)
+      launch_one<128, 128>(s, g, sp, src, res);
+    else if (g.c <= 128)
       launch_one<64, 128>(s, g, sp, src, res);
     else
-      launch_one<128, 128>(s, g, sp, src, res);
+      launch_one<64, 256>(s, g, sp, src, res);
     timing_mark(ctx, stage, s, true);
     return check_launch(ctx, who);
   }
   g.cp = round_up(g.c, 128);
-  const uint32_t R = narrow ? 64 : 128, ways = uint32_t(std::min<uint64_t>(g.cp / 128, narrow ? 16 : 8));
+  const uint32_t R = narrow ? 64 : 128, ways = uint32_t(std::min<uint64_t>(g.cp / 128, 64));
   const size_t norms = round_up(size_t(g.batch) * g.parts, 2), plane = size_t(R) * g.cp;
   gsr_status st = grow(ctx, ctx->arena.feat_part,
                        norms * sizeof(double) + g.batch * (2 * plane * sizeof(half) + 2 * size_t(ways) * R * R * sizeof(float)));
