@@ -32,12 +32,32 @@ struct LnRows {
   }
 };
 
-// Sum over a team of TEAM adjacent lanes (a power of two up to 64) or over the workgroup's TEAM threads, in a fixed
-// order; every lane of the team gets it. `s` holds TEAM / 64 floats where TEAM > 64; two sums in turn need two of them.
+__device__ __forceinline__ uint32_t bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+
+// The value of the lane that CTRL names, within rows of sixteen lanes.
+template <int CTRL>
+__device__ __forceinline__ float lane_of(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, int(bits(v)), CTRL, 0xf, 0xf, true));
+}
+
+// Sum over a team of TEAM adjacent lanes (a power of two from 8 to 64) or over the workgroup's TEAM threads, in a fixed
+// order; every lane of the team gets it. `s` holds TEAM / 64 floats where TEAM > 64; two sums in turn need two of them. In
+// a wave by moves between lanes that stay in the vector unit: through LDS, twelve steps a token were most of its time.
 template <int TEAM>
 __device__ __forceinline__ float team_sum(float v, float* s) {
-#pragma unroll
-  for (int k = (TEAM < 64 ? TEAM : 64) / 2; k > 0; k >>= 1) v += __shfl_xor(v, k);
+  static_assert(TEAM >= 8);
+  v += lane_of<0xB1>(v);   // the lane's neighbour
+  v += lane_of<0x4E>(v);   // the other pair of four
+  v += lane_of<0x141>(v);  // the other four of eight
+  if constexpr (TEAM >= 16) v += lane_of<0x140>(v);  // the other eight of sixteen
+  if constexpr (TEAM >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
+    v = __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+  }
+  if constexpr (TEAM >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
+    v = __builtin_bit_cast(float, uint32_t(r[0])) + __builtin_bit_cast(float, uint32_t(r[1]));
+  }
   if constexpr (TEAM > 64) {
     __syncthreads();
     if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
@@ -54,7 +74,27 @@ constexpr int threads_of(int team) { return team > 256 ? team : 256; }
 template <typename T>
 constexpr int kVec = 16 / int(sizeof(T));
 
-// A lane's K vectors of V channels: vector k is channels (k * TEAM + lane) * V ...
+// A lane's K vectors of V channels of a token, as they lie in memory (zeros past the last): vector k is channels
+// (k * TEAM + lane) * V and on.
+template <typename T, int TEAM, int K>
+struct Token {
+  static constexpr int V = kVec<T>;
+  Vec<T, V> v[K];
+  __device__ __forceinline__ void load(const T* p, uint32_t lane, int channels) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = int(k * TEAM + lane) * V;
+      if (c + V <= channels) {
+        __builtin_memcpy(&v[k], p + c, sizeof v[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] = c + i < channels ? p[c + i] : T(0.0f);
+      }
+    }
+  }
+};
+
+// Bound by memory: 40,000 x 1,024 bfloat16 (164 MB) 38 us, 4.3 TB/s.
 template <typename T, int TEAM, int K>
 __global__ __launch_bounds__(threads_of(TEAM)) void k_ln(LnShape g, const T* x, LnRows xr,
                                                          const float* __restrict__ gamma,
@@ -66,6 +106,8 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_ln(LnShape g, const T* x, 
   const uint32_t stride = gridDim.x * kTeams;
   const int C = int(g.channels);
   const float n = float(C);
+  Token<T, TEAM, K> next;
+  if (team < g.rows) next.load(x + xr.at(g, team), lane, C);
   float gm[K][V], bt[K][V];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -77,14 +119,16 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_ln(LnShape g, const T* x, 
     }
   }
   for (uint32_t row = team; row < g.rows; row += stride) {
-    const T* xp = x + xr.at(g, row);
+    const Token<T, TEAM, K> now = next;
+    if (row + stride < g.rows) next.load(x + xr.at(g, row + stride), lane, C);  // on its way while this one is summed
     float f[K][V], sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) load_f32<V>(xp + (k * TEAM + lane) * V, C - int(k * TEAM + lane) * V, f[k]);
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += f[k][i];
+      for (int i = 0; i < V; ++i) {
+        f[k][i] = float(now.v[k][i]);
+        sum += f[k][i];
+      }
     const float mean = team_sum<TEAM>(sum, s[0]) / n;
     float sq = 0.0f;
 #pragma unroll
@@ -107,44 +151,55 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_ln(LnShape g, const T* x, 
 }
 
 // dx, and the team's sums of dy xh and dy over its tokens; the workgroup's teams are added through LDS, and `part` gets
-// [workgroup][2][channels].
-template <typename T, int TEAM, int K>
-__global__ __launch_bounds__(threads_of(TEAM)) void k_ln_back(LnShape g, const T* __restrict__ x, LnRows xr,
-                                                              const float* __restrict__ gamma,
-                                                              const LnStats* __restrict__ stats, const T* dy,
-                                                              LnRows dr, T* dx, LnRows or_,
-                                                              float* __restrict__ part) {
-  constexpr int V = kVec<T>, kThreads = threads_of(TEAM), kTeams = kThreads / TEAM;
+// [workgroup][2][channels], or with one workgroup dgamma and dbeta get them.
+// Bound by memory: 40,000 x 1,024 bfloat16 (246 MB) 52 us, 4.7 TB/s.
+template <typename T, int TEAM, int K, int THREADS>
+__global__ __launch_bounds__(THREADS) void k_ln_back(LnShape g, const T* __restrict__ x, LnRows xr,
+                                                     const float* __restrict__ gamma,
+                                                     const LnStats* __restrict__ stats, const T* dy, LnRows dr, T* dx,
+                                                     LnRows or_, float* __restrict__ part, float* __restrict__ dgamma,
+                                                     float* __restrict__ dbeta) {
+  constexpr int V = kVec<T>, kTeams = THREADS / TEAM;
   __shared__ float s[2][TEAM > 64 ? TEAM / 64 : 1];
   const uint32_t lane = threadIdx.x % TEAM, team = blockIdx.x * kTeams + threadIdx.x / TEAM;
   const uint32_t stride = gridDim.x * kTeams;
   const int C = int(g.channels);
   const float n = float(C);
+  Token<T, TEAM, K> next_x, next_dy;
+  LnStats next_stats = {};
+  auto load = [&](uint32_t row) {
+    next_x.load(x + xr.at(g, row), lane, C);
+    next_dy.load(dy + dr.at(g, row), lane, C);
+    next_stats = stats[row];
+  };
+  if (team < g.rows) load(team);
+  constexpr bool kHold = TEAM < 1024;  // gamma in registers, which 1,024 threads of two vectors have none left for
   float gm[K][V], dg[K][V], db[K][V];
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = int(k * TEAM + lane) * V;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      gm[k][i] = gamma && c + i < C ? gamma[c + i] : 1.0f;
-      dg[k][i] = db[k][i] = 0.0f;
-    }
-  }
-  for (uint32_t row = team; row < g.rows; row += stride) {
-    const T *xp = x + xr.at(g, row), *dp = dy + dr.at(g, row);
-    float f[K][V], d[K][V];
+  auto load_gamma = [&] {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      load_f32<V>(xp + (k * TEAM + lane) * V, C - int(k * TEAM + lane) * V, f[k]);
-      load_f32<V>(dp + (k * TEAM + lane) * V, C - int(k * TEAM + lane) * V, d[k]);
+      const int c = int(k * TEAM + lane) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) gm[k][i] = gamma && c + i < C ? gamma[c + i] : 1.0f;
     }
-    const LnStats st = stats[row];
-    float a = 0.0f, b = 0.0f;
+  };
+  if constexpr (kHold) load_gamma();
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) dg[k][i] = db[k][i] = 0.0f;
+  for (uint32_t row = team; row < g.rows; row += stride) {
+    const Token<T, TEAM, K> now_x = next_x, now_dy = next_dy;
+    const LnStats st = next_stats;
+    if (row + stride < g.rows) load(row + stride);  // on its way while this one is summed
+    if constexpr (!kHold) load_gamma();
+    float f[K][V], d[K][V], a = 0.0f, b = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        f[k][i] = (f[k][i] - st.mean) * st.rstd;
+        f[k][i] = (float(now_x.v[k][i]) - st.mean) * st.rstd;
+        d[k][i] = float(now_dy.v[k][i]);
         db[k][i] += d[k][i];
         dg[k][i] = fmaf(d[k][i], f[k][i], dg[k][i]);
         d[k][i] *= gm[k][i];
@@ -164,23 +219,27 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_ln_back(LnShape g, const T
       store_f32<V>(op + (k * TEAM + lane) * V, C - int(k * TEAM + lane) * V, d[k]);
     }
   }
-  if (!part) return;
-  float* out = part + size_t(blockIdx.x) * 2 * g.channels;
+  if (!dgamma && !dbeta) return;
+  if (gridDim.x > 1) {
+    dgamma = part + size_t(blockIdx.x) * 2 * g.channels;
+    dbeta = dgamma + g.channels;
+  }
   if constexpr (kTeams > 1) {
-    __shared__ float sums[kThreads * V];
+    __shared__ float sums[THREADS * V];
 #pragma unroll
     for (int k = 0; k < K; ++k)
       for (int which = 0; which < 2; ++which) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < V; ++i) sums[i * kThreads + threadIdx.x] = which ? db[k][i] : dg[k][i];
+        for (int i = 0; i < V; ++i) sums[i * THREADS + threadIdx.x] = which ? db[k][i] : dg[k][i];
         __syncthreads();
-        for (int e = threadIdx.x; e < TEAM * V; e += kThreads) {
+        for (int e = threadIdx.x; e < TEAM * V; e += THREADS) {
           const int l = e / V, i = e % V, c = (k * TEAM + l) * V + i;
           float t = 0.0f;
 #pragma unroll
-          for (int n = 0; n < kTeams; ++n) t += sums[i * kThreads + n * TEAM + l];
-          if (c < C) out[which * C + c] = t;
+          for (int m = 0; m < kTeams; ++m) t += sums[i * THREADS + m * TEAM + l];
+          float* const out = which ? dbeta : dgamma;
+          if (c < C && out) out[c] = t;
         }
       }
   } else {
@@ -189,10 +248,8 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_ln_back(LnShape g, const T
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = int(k * TEAM + lane) * V + i;
-        if (c < C) {
-          out[c] = dg[k][i];
-          out[C + c] = db[k][i];
-        }
+        if (c < C && dgamma) dgamma[c] = dg[k][i];
+        if (c < C && dbeta) dbeta[c] = db[k][i];
       }
   }
 }
@@ -380,6 +437,22 @@ LnShape shape_of(const gsr_layer_norm* d) {
   return g;
 }
 
+// Workgroups of `teams` teams whose lanes hold `load` vectors (of 256 threads): each reads gamma (and writes its sums) once,
+// so that few long-lived ones cost least, as many as keep memory busy. Forward and backward with 256, 512, 1,024 and 2,048
+// of them: 40,000 x 1,024 bfloat16 (two vectors) 45, 38, 42 and 46 us; 57, 56, 61 and (with 1,024 threads each) 66. 40,000 x
+// 1,024 float32 (four) 60, 64, 65 and 63; 94, 99, 102 and 158. 40,000 x 512 float16 (one) 32, 26, 25 and 26; 43, 34, 34
+// and 34. Each gets as many tokens as the others.
+uint32_t workgroups(uint32_t rows, uint32_t teams, uint32_t load) {
+  const uint64_t most = uint64_t(load >= 4 ? 256 : (load >= 2 ? 512 : 1024)) * teams, per = (rows + most - 1) / most;
+  return uint32_t((rows + teams * per - 1) / (teams * per));
+}
+
+// Threads of the one workgroup that takes few tokens (four to a team; no sums to join): as many as its registers allow.
+template <typename T, int TEAM, int K>
+constexpr int large_threads() {
+  return TEAM >= 256 ? threads_of(TEAM) : (kVec<T> * K <= 16 ? 1024 : 512);
+}
+
 // Calls f(element type, team, vectors) with compile-time values for the smallest team that holds a token, or
 // wide(element type).
 template <typename F, typename W>
@@ -452,7 +525,7 @@ extern "C" gsr_status gsr_layer_norm_forward(gsr_ctx* ctx, void* stream, const g
       [&](auto t, auto team, auto k) {
         using T = decltype(t);
         constexpr int kTeam = decltype(team)::value, kT = threads_of(kTeam), kTeams = kT / kTeam;
-        const uint32_t blocks = std::min<uint32_t>((g.rows + kTeams - 1) / kTeams, 2048);
+        const uint32_t blocks = workgroups(g.rows, kTeams, kT / 256 * decltype(k)::value);
         hipLaunchKernelGGL((k_ln<T, kTeam, decltype(k)::value>), dim3(blocks), dim3(kT), 0, s, g,
                            static_cast<const T*>(x), xr, gamma, beta, static_cast<T*>(y), yr, out);
       },
@@ -495,24 +568,38 @@ extern "C" gsr_status gsr_layer_norm_backward(gsr_ctx* ctx, void* stream, const 
   const bool sums = dgamma || dbeta;
   // the teams' workgroups, or the rows of workgroups of the column sums; each leaves one part
   uint32_t parts = 0;
+  bool one = false, wide = false;
   by_kind(
       d,
-      [&](auto, auto team, auto) {
-        constexpr int kTeam = decltype(team)::value, kTeams = threads_of(kTeam) / kTeam;
-        parts = std::min<uint32_t>((g.rows + kTeams - 1) / kTeams, 512);
+      [&](auto t, auto team, auto k) {
+        constexpr int kTeam = decltype(team)::value, kLarge = large_threads<decltype(t), kTeam, decltype(k)::value>();
+        one = g.rows <= 4 * (kLarge / kTeam);
+        parts = one ? 1 : workgroups(g.rows, threads_of(kTeam) / kTeam, threads_of(kTeam) / 256 * decltype(k)::value);
       },
-      [&](auto) { parts = std::min<uint32_t>(g.rows, 64); });
-  if (sums && (st = grow(ctx, ctx->arena.feat_part, size_t(parts) * 2 * g.channels * sizeof(float)))) return st;
-  float* part = sums ? static_cast<float*>(ctx->arena.feat_part.ptr) : nullptr;
+      [&](auto) {
+        parts = std::min<uint32_t>(g.rows, 64);
+        wide = true;
+      });
+  if (sums && (parts > 1 || wide) && (st = grow(ctx, ctx->arena.feat_part, size_t(parts) * 2 * g.channels * sizeof(float))))
+    return st;
+  float* part = static_cast<float*>(ctx->arena.feat_part.ptr);
+  bool joined = false;
   timing_mark(ctx, GSR_STAGE_LAYER_NORM_BACKWARD, s, false);
   by_kind(
       d,
       [&](auto t, auto team, auto k) {
         using T = decltype(t);
-        constexpr int kTeam = decltype(team)::value;
-        hipLaunchKernelGGL((k_ln_back<T, kTeam, decltype(k)::value>), dim3(parts), dim3(threads_of(kTeam)), 0, s, g,
-                           static_cast<const T*>(x), xr, gamma, in, static_cast<const T*>(dy), dr, static_cast<T*>(dx),
-                           outr, part);
+        constexpr int kTeam = decltype(team)::value, kK = decltype(k)::value;
+        auto launch = [&](auto kernel, int threads) {
+          hipLaunchKernelGGL(kernel, dim3(parts), dim3(threads), 0, s, g, static_cast<const T*>(x), xr, gamma, in,
+                             static_cast<const T*>(dy), dr, static_cast<T*>(dx), outr, part, dgamma, dbeta);
+        };
+        constexpr int kLarge = large_threads<T, kTeam, kK>();
+        if (one)
+          launch(k_ln_back<T, kTeam, kK, kLarge>, kLarge);
+        else
+          launch(k_ln_back<T, kTeam, kK, threads_of(kTeam)>, threads_of(kTeam));
+        joined = parts == 1;
       },
       [&](auto t) {
         using T = decltype(t);
@@ -524,7 +611,7 @@ extern "C" gsr_status gsr_layer_norm_backward(gsr_ctx* ctx, void* stream, const 
           hipLaunchKernelGGL((k_ln_wide_back<T>), dim3(std::min<uint32_t>(g.rows, 512)), dim3(kWide), 0, s, g, xt, xr,
                              gamma, in, dt, dr, static_cast<T*>(dx), outr);
       });
-  if (sums)
+  if (sums && !joined)
     hipLaunchKernelGGL(k_ln_join, dim3((2 * g.channels + 63) / 64), dim3(1024), 0, s, g.channels, parts, part, dgamma,
                        dbeta);
   timing_mark(ctx, GSR_STAGE_LAYER_NORM_BACKWARD, s, true);

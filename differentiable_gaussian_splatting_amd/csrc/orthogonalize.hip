@@ -428,11 +428,29 @@ __device__ __forceinline__ void finish_rows(char* mine, const f32x16* acc, float
     }
 }
 
-// out = alpha in + beta (x x^T) [rp, rp], symmetric, PLANES planes each of x, in (read if ADD) and out.
-template <int kTile, int PLANES, bool ADD>
+// Adds alpha times the numbers that lie in the wave's part of LDS to its 32 rows of sums.
+template <int kTile, int PLANES>
+__device__ __forceinline__ void add_rows(char* mine, f32x16* acc, float alpha) {
+  using L = Turn<kTile>;
+#pragma unroll
+  for (int j = 0; j < kTile / 64; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = 32 * j + 8 * q + 4 * int((threadIdx.x & 63) >> 5);
+      const Vec<half, 4> h = L::at(mine, col), w = L::at(mine + (PLANES - 1) * L::kBytes, col);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        acc[j][4 * q + k] = fmaf(alpha, PLANES == 2 ? float(h[k]) + float(w[k]) : float(h[k]), acc[j][4 * q + k]);
+    }
+}
+
+// out = beta (left right^T) + alpha in + alpha2 in2 [rp, rp], symmetric (left and right are one matrix, or commute), PLANES
+// planes each of left, right, in, in2 and out; ADD of in and in2 are read. Strides from matrix to matrix: of left and right
+// `matrix`, of the others PLANES planes.
+template <int kTile, int PLANES, int ADD>
 __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_symmetric(
-    Works w, uint32_t tiles, Operand x, uint64_t x_matrix, uint64_t deep, const half* __restrict__ in,
-    half* __restrict__ out, uint64_t rp, float alpha, float beta) {
+    Works w, uint32_t tiles, Operand left, Operand right, uint64_t matrix, uint64_t deep, const half* __restrict__ in,
+    const half* __restrict__ in2, half* __restrict__ out, uint64_t rp, float alpha, float alpha2, float beta) {
   using Mem = Lds<kTile, PLANES, PLANES>;
   using L = Turn<kTile>;
   static_assert(4 * PLANES * L::kBytes <= Mem::kBytes, "the results pass through the stages' LDS");
@@ -443,30 +461,42 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_symmetri
   uint32_t ti, tj;
   triangle(uint32_t(id - b * tiles), &ti, &tj);
   const uint64_t plane = rp * rp;
-  x.base += b * x_matrix;
+  left.base += b * matrix;
+  right.base += b * matrix;
   in += b * PLANES * plane;
+  in2 += b * PLANES * plane;
   out += b * PLANES * plane;
   Sums<kTile> s;
-  product<kTile, PLANES, PLANES>(x, x, uint64_t(ti) * kTile, uint64_t(tj) * kTile, deep, lds, s);
+  product<kTile, PLANES, PLANES>(left, right, uint64_t(ti) * kTile, uint64_t(tj) * kTile, deep, lds, s);
   char* mine = lds + (threadIdx.x >> 6) * PLANES * L::kBytes;
   u32x4 have[PLANES][L::kTurns];
-  auto fetch = [&](uint64_t row) {
+  auto fetch = [&](const half* from, uint64_t row) {
 #pragma unroll
-    for (int p = 0; p < PLANES; ++p) L::fetch(in + p * plane, rp, row, s.col, rp, have[p]);
+    for (int p = 0; p < PLANES; ++p) L::fetch(from + p * plane, rp, row, s.col, rp, have[p]);
   };
-  if constexpr (ADD) fetch(s.row);
+  if constexpr (ADD > 0) fetch(in, s.row);
 #pragma unroll
   for (int i = 0; i < kTile / 64; ++i) {
     const uint64_t row = s.row + 32 * i;
     if (row >= rp) break;
     wave_sync();  // the last rows' reads
-    if constexpr (ADD) {
+    auto lay = [&] {
 #pragma unroll
       for (int p = 0; p < PLANES; ++p) L::lay(have[p], mine + p * L::kBytes);
-      if (i + 1 < kTile / 64) fetch(row + 32);  // on their way while these rows are stored
+    };
+    if constexpr (ADD == 2) {
+      lay();
+      fetch(in2, row);
+      wave_sync();
+      add_rows<kTile, PLANES>(mine, s.acc[i], alpha / beta);
       wave_sync();
     }
-    finish_rows<kTile, PLANES, ADD>(mine, s.acc[i], alpha, beta);
+    if constexpr (ADD > 0) {
+      lay();
+      if (i + 1 < kTile / 64) fetch(in, row + 32);  // on their way while these rows are stored
+      wave_sync();
+    }
+    finish_rows<kTile, PLANES, (ADD > 0)>(mine, s.acc[i], ADD == 2 ? alpha2 : alpha, beta);
     wave_sync();
 #pragma unroll
     for (int p = 0; p < PLANES; ++p) {
@@ -1068,20 +1098,27 @@ struct Plan {
   int steps;
   Step step[GSR_ORTHOGONALIZE_MAX_STEPS];
   int x_exp[GSR_ORTHOGONALIZE_MAX_STEPS + 1], a_exp[GSR_ORTHOGONALIZE_MAX_STEPS], p_exp[GSR_ORTHOGONALIZE_MAX_STEPS];
+  // of steps k and k + 1 taken together: T and Q of launch_steps
+  int t_exp[GSR_ORTHOGONALIZE_MAX_STEPS], q_exp[GSR_ORTHOGONALIZE_MAX_STEPS];
 };
 
 int room(double top) { return 14 - std::max(-8, int(std::ceil(std::log2(std::max(top, 1e-30))))); }
 
 bool plan_of(const gsr_newton_schulz* d, Plan* p) {
   p->steps = int(d->steps);
-  double top = 1.0;
+  double top = 1.0, p_last = 0.0, a_last = 0.0;
   for (int k = 0; k < p->steps; ++k) {
     const double a = d->coefficients[k][0], b = d->coefficients[k][1], c = d->coefficients[k][2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
     p->step[k] = Step{float(a), float(b), float(c)};
     p->x_exp[k] = room(top);
     p->a_exp[k] = room(top * top);
-    p->p_exp[k] = room(std::fabs(b) * top * top + std::fabs(c) * top * top * top * top);
+    const double p_top = std::fabs(b) * top * top + std::fabs(c) * top * top * top * top;
+    p->p_exp[k] = room(p_top);
+    p->t_exp[k] = room((std::fabs(a) + p_top) * top * top);
+    if (k) p->q_exp[k - 1] = room(p_top * p_last + std::fabs(a) * p_last + a_last * p_top);
+    p_last = p_top;
+    a_last = std::fabs(a);
     auto value = [&](double u) { return std::sqrt(u) * std::fabs(a + b * u + c * u * u); };
     double next = value(top * top);
     const double disc = 9 * b * b - 20 * a * c;  // slope a + 3 b u + 5 c u^2 in u = s^2
@@ -1099,22 +1136,24 @@ bool plan_of(const gsr_newton_schulz* d, Plan* p) {
 
 uint64_t round_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
-// The side of the square tiles of a product: the one whose rounds of workgroups take least. `tiles(side)` counts them.
-// Measured for tiles of depth 1,024 in two planes, one workgroup after the other on a compute unit: 12.8, 31, 56 and 95
-// us; small tiles overlap, so that part of a round of them counts as part. 8 x 1,024 x 4,096: P X 243 us with tiles of
-// 256, 278 with 128, 416 with 64; 4,096 x 1,024: X X^T 36 us with tiles of 64, 91 with 128; 4,096 x 4,096: A A^T 205 us
-// with 253 tiles of 192, 250 with 136 of 256, 276 with 528 of 128.
+// The side of the square tiles of a product, and its time in us: the one whose rounds of workgroups take least.
+// `tiles(side)` counts them. Measured for tiles of depth 1,024 in two planes, one workgroup after the other on a compute
+// unit: 12.8, 31, 56 and 95 us, and about 4 us of a launch's own; small tiles overlap, so that part of a round of them
+// counts as part. 8 x 1,024 x 4,096: P X 243 us with tiles of 256, 278 with 128, 416 with 64; 4,096 x 1,024: X X^T 36 us
+// with tiles of 64, 91 with 128; 4,096 x 4,096: A A^T 205 us with 253 tiles of 192, 250 with 136 of 256, 276 with 528 of
+// 128.
+struct Side {
+  int side;
+  double us;
+};
+
 template <typename F>
-int tile_side(F tiles) {
-  int best = 0;
-  double least = 1e300;
+Side tile_side(uint64_t deep, F tiles) {
+  Side best{0, 1e300};
   for (const auto& [side, us] : {std::pair(64, 12.8), std::pair(128, 31.0), std::pair(192, 56.0), std::pair(256, 95.0)}) {
     const double rounds = double(tiles(uint64_t(side))) / 256;
-    const double time = us * (side == 64 ? std::max(1.0, rounds) : std::ceil(rounds));
-    if (time < least) {
-      least = time;
-      best = side;
-    }
+    const double time = us * (side == 64 ? std::max(1.0, rounds) : std::ceil(rounds)) * double(deep) / 1024 + 4;
+    if (time < best.us) best = Side{side, time};
   }
   return best;
 }
@@ -1132,9 +1171,14 @@ void by_side(int side, F f) {
     f(std::integral_constant<int, 256>());
 }
 
+// The steps, each by its three products, or, where that is less work, two at a time: with P~ = P + a I, A of the second step
+// is P~ A P~ (all of them are polynomials of one matrix), and both steps are one product with X:
+//   T = A P~;  A' = T P~;  P' from A';  Q = P' P~ + a' P;  X <- a a' X + Q X,
+// five products of r x r instead of a second X X^T and P X. Two steps cost no accuracy (a rounding of A' reaches P' like
+// one of X); more would, because A' loses the small singular values' squares. 8 x 1,024 x 4,096: 2,030 us against 2,540.
 template <int PLANES, typename T, bool MUON, typename R>
 void launch_steps(hipStream_t s, const OrthShape& g, const Plan& plan, const Source<T, MUON>& src, double* part, half* x,
-                  half* xt, half* next, half* am, half* pm, const Result<R>& res) {
+                  half* xt, half* next, half* am, half* pm, half* tm, const Result<R>& res) {
   hipLaunchKernelGGL((k_orth_norm<T, MUON>), dim3(g.parts, g.batch), dim3(kThreads), 0, s, g, src, part);
   hipLaunchKernelGGL((k_orth_start<T, MUON>), dim3(uint32_t(g.cp / 64), uint32_t(g.rp / 64), g.batch), dim3(kThreads), 0,
                      s, g, src, part, x, xt);
@@ -1144,30 +1188,61 @@ void launch_steps(hipStream_t s, const OrthShape& g, const Plan& plan, const Sou
   auto whole = [&](uint64_t side) { return across(g.rp, side) * across(g.cp, side); };
   auto works = [](uint64_t n) { return Works{n, (n + kFeatXcds - 1) / kFeatXcds}; };
   auto grid = [](const Works& w) { return grid_rows(w.per_xcd * kFeatXcds); };
-  const int side_s = tile_side([&](uint64_t side) { return triangle(side) * g.batch; });
-  const int side_w = tile_side([&](uint64_t side) { return whole(side) * g.batch; });
-  for (int k = 0; k < plan.steps; ++k) {
-    const Step& c = plan.step[k];
-    const int ex = plan.x_exp[k], ea = plan.a_exp[k], ep = plan.p_exp[k], en = plan.x_exp[k + 1];
-    by_side(side_s, [&](auto side) {
+  const Side side_g = tile_side(g.cp, [&](uint64_t side) { return triangle(side) * g.batch; });
+  const Side side_s = tile_side(g.rp, [&](uint64_t side) { return triangle(side) * g.batch; });
+  const Side side_w = tile_side(g.rp, [&](uint64_t side) { return whole(side) * g.batch; });
+  const bool pairs = PLANES == 2 && tm;
+  // out = beta left right^T + alpha in + alpha2 in2
+  auto symmetric = [&](auto add, const Side& by, const Operand& left, const Operand& right, uint64_t matrix, uint64_t deep,
+                       float beta, half* out, const half* in, float alpha, const half* in2, float alpha2) {
+    by_side(by.side, [&](auto side) {
       constexpr int kTile = decltype(side)::value;
       const uint32_t tiles = uint32_t(triangle(kTile));
       const Works w = works(uint64_t(tiles) * g.batch);
-      hipLaunchKernelGGL((k_orth_symmetric<kTile, PLANES, false>), grid(w), dim3(kThreads), 0, s, w, tiles,
-                         Operand{x, plane, g.cp, g.rp}, 2 * plane, g.cp, am, am, g.rp, 0.0f,
-                         std::ldexp(1.0f, ea - 2 * ex));
-      hipLaunchKernelGGL((k_orth_symmetric<kTile, PLANES, true>), grid(w), dim3(kThreads), 0, s, w, tiles,
-                         Operand{am, square, g.rp, g.rp}, PLANES * square, g.rp, am, pm, g.rp, std::ldexp(c.b, ep - ea),
-                         std::ldexp(c.c, ep - 2 * ea));
+      hipLaunchKernelGGL((k_orth_symmetric<kTile, PLANES, decltype(add)::value>), grid(w), dim3(kThreads), 0, s, w, tiles,
+                         left, right, matrix, deep, in, in2, out, g.rp, alpha, alpha2, beta);
     });
-    const float alpha = std::ldexp(c.a, en - ex), beta = std::ldexp(1.0f, en - ep - ex);
-    const Operand p{pm, square, g.rp, g.rp};
-    by_side(side_w, [&](auto side) {
+  };
+  using Add0 = std::integral_constant<int, 0>;
+  using Add1 = std::integral_constant<int, 1>;
+  auto pow2 = [](double v, int e) { return float(std::ldexp(v, e)); };
+  auto sq = [&](const half* m) { return Operand{m, square, g.rp, g.rp}; };
+  for (int k = 0; k < plan.steps; ++k) {
+    const Step c = plan.step[k];
+    const int ex = plan.x_exp[k], ea = plan.a_exp[k], ep = plan.p_exp[k];
+    const Operand xo{x, plane, g.cp, g.rp};
+    symmetric(Add0(), side_g, xo, xo, 2 * plane, g.cp, pow2(1, ea - 2 * ex), am, am, 0.0f, am, 0.0f);
+    symmetric(Add1(), side_s, sq(am), sq(am), PLANES * square, g.rp, pow2(c.c, ep - 2 * ea), pm, am, pow2(c.b, ep - ea), am,
+              0.0f);
+    const half* factor = pm;
+    double times_x = c.a;
+    int ef = ep;
+    if constexpr (PLANES == 2) {
+      if (pairs && k + 1 < plan.steps) {
+        using Add2 = std::integral_constant<int, 2>;
+        const Step d = plan.step[++k];
+        const int et = plan.t_exp[k - 1], ea2 = plan.a_exp[k], ep2 = plan.p_exp[k], eq = plan.q_exp[k - 1];
+        symmetric(Add1(), side_s, sq(am), sq(pm), 2 * square, g.rp, pow2(1, et - ea - ep), tm, am, pow2(c.a, et - ea), am,
+                  0.0f);
+        symmetric(Add1(), side_s, sq(tm), sq(pm), 2 * square, g.rp, pow2(1, ea2 - et - ep), am, tm, pow2(c.a, ea2 - et), tm,
+                  0.0f);
+        symmetric(Add1(), side_s, sq(am), sq(am), 2 * square, g.rp, pow2(d.c, ep2 - 2 * ea2), tm, am, pow2(d.b, ep2 - ea2),
+                  am, 0.0f);
+        symmetric(Add2(), side_s, sq(tm), sq(pm), 2 * square, g.rp, pow2(1, eq - ep2 - ep), am, pm, pow2(d.a, eq - ep), tm,
+                  pow2(c.a, eq - ep2));
+        factor = am;
+        times_x = double(c.a) * d.a;
+        ef = eq;
+      }
+    }
+    const int en = plan.x_exp[k + 1];
+    const float alpha = pow2(times_x, en - ex), beta = pow2(1, en - ef - ex);
+    by_side(side_w.side, [&](auto side) {
       constexpr int kTile = decltype(side)::value;
       const uint32_t tr = uint32_t(across(g.rp, kTile)), tc = uint32_t(across(g.cp, kTile));
       const Works w = works(uint64_t(tr) * tc * g.batch);
       auto launch = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, grid(w), dim3(kThreads), 0, s, w, g, tr, tc, p, x, xt, next, alpha, beta, res);
+        hipLaunchKernelGGL(kernel, grid(w), dim3(kThreads), 0, s, w, g, tr, tc, sq(factor), x, xt, next, alpha, beta, res);
       };
       if (k + 1 < plan.steps)
         launch(k_orth_apply<kTile, PLANES, kNext, R>);
@@ -1176,6 +1251,14 @@ void launch_steps(hipStream_t s, const OrthShape& g, const Plan& plan, const Sou
     });
     std::swap(xt, next);
   }
+}
+
+// Whether two steps at a time are less work: X X^T and P X against three more products of r x r.
+bool pairs_pay(const OrthShape& g) {
+  auto across = [](uint64_t n, uint64_t side) { return (n + side - 1) / side; };
+  auto triangle = [&](uint64_t side) { return across(g.rp, side) * (across(g.rp, side) + 1) / 2 * g.batch; };
+  auto whole = [&](uint64_t side) { return across(g.rp, side) * across(g.cp, side) * g.batch; };
+  return tile_side(g.cp, triangle).us + tile_side(g.rp, whole).us > 3 * tile_side(g.rp, triangle).us;
 }
 
 template <int R, int S, typename T, bool MUON, typename RT>
@@ -1284,9 +1367,10 @@ gsr_status run(gsr_ctx* ctx, hipStream_t s, const gsr_newton_schulz* d, const Pl
   if (g.r <= 128) return run_small(ctx, s, g, plan, src, res, stage, who);
   g.rp = round_up(g.r, 64);
   g.cp = round_up(g.c, 64);
+  const bool pairs = planes == 2 && plan.steps > 1 && pairs_pay(g);
   const size_t plane = g.rp * g.cp, square = g.rp * g.rp, parts = round_up(size_t(g.batch) * g.parts, 2);
   gsr_status st = grow(ctx, ctx->arena.feat_part,
-                       parts * sizeof(double) + g.batch * (6 * plane + 2 * planes * square) * sizeof(half));
+                       parts * sizeof(double) + g.batch * (6 * plane + (pairs ? 3 : 2) * planes * square) * sizeof(half));
   if (st) return st;
   double* part = static_cast<double*>(ctx->arena.feat_part.ptr);
   half* x = reinterpret_cast<half*>(part + parts);
@@ -1294,12 +1378,12 @@ gsr_status run(gsr_ctx* ctx, hipStream_t s, const gsr_newton_schulz* d, const Pl
   half* next = xt + 2 * plane * g.batch;
   half* am = next + 2 * plane * g.batch;
   half* pm = am + planes * square * g.batch;
+  half* tm = pairs ? pm + planes * square * g.batch : nullptr;
   timing_mark(ctx, stage, s, false);
   if constexpr (std::is_same_v<R, __bf16>) {
-    if (planes == 1)
-      launch_steps<1>(s, g, plan, src, part, x, xt, next, am, pm, res);
+    if (planes == 1) launch_steps<1>(s, g, plan, src, part, x, xt, next, am, pm, tm, res);
   }
-  if (planes == 2) launch_steps<2>(s, g, plan, src, part, x, xt, next, am, pm, res);
+  if (planes == 2) launch_steps<2>(s, g, plan, src, part, x, xt, next, am, pm, tm, res);
   timing_mark(ctx, stage, s, true);
   return check_launch(ctx, who);
 }

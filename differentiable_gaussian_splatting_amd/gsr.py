@@ -728,21 +728,33 @@ def gsr_cross_attention_backward(ctx: Context, q: torch.Tensor, k: torch.Tensor,
     return dq, dk, dv
 
 
+def _need_floats(t, name, numel, dev):
+    """_need of contiguous float32 values, in one condition where all is well."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.numel() != numel or t.device != dev or \
+            not t.is_contiguous():
+        _need(t, name, (torch.float32,), numel, dev)
+
+
+def _token_strides(t, name, tokens, channels):
+    return (tokens * channels, channels) if t.is_contiguous() else _image_strides(t, name)
+
+
 def _layer_norm_desc(ctx, x, gamma, beta, eps):
     dev = ctx.device
     _need_feature(x, "x", dev)
-    if x.dim() < 2:
+    shape = x.shape
+    if len(shape) < 2:
         raise ValueError("x must be [batch, ..., channels]")
-    C = x.shape[-1]
-    for t, name in ((gamma, "gamma"), (beta, "beta")):
-        if t is not None:
-            _need(t, name, (torch.float32,), C, dev)
-    tokens = 1
-    for n in x.shape[1:-1]:
+    batch, C, tokens = shape[0], shape[-1], 1
+    for n in shape[1:-1]:
         tokens *= n
-    _fit("batch, tokens, channels", x.shape[0] | tokens | C)
-    d = gsr_layer_norm(_DTYPES[x.dtype], x.shape[0], tokens, C, eps)
-    d.x_stride[:] = _image_strides(x, "x")
+    if gamma is not None:
+        _need_floats(gamma, "gamma", C, dev)
+    if beta is not None:
+        _need_floats(beta, "beta", C, dev)
+    _fit("batch, tokens, channels", batch | tokens | C)
+    d = gsr_layer_norm(_DTYPES[x.dtype], batch, tokens, C, eps)
+    d.x_stride[:] = _token_strides(x, "x", tokens, C)
     return d
 
 
@@ -752,15 +764,21 @@ def gsr_layer_norm_forward(ctx: Context, x: torch.Tensor, gamma: torch.Tensor | 
     """Layer norm over the last dimension of x [B, ..., C] (float32, float16 or bfloat16; gamma and beta float32 [C] or
     None). `y` may be x. Returns (y like x, stats float32 [B, ..., 2] = (mean, rstd))."""
     d = _layer_norm_desc(ctx, x, gamma, beta, eps)
+    tokens, C = d.tokens, d.channels
     if y is None:
         y = _like(x)
+        d.y_stride[:] = tokens * C, C
+    else:
+        _need_feature(y, "y", ctx.device, x.dtype, x.shape)
+        d.y_stride[:] = _token_strides(y, "y", tokens, C)
     if stats is None:
         stats = torch.empty(x.shape[:-1] + (2,), dtype=torch.float32, device=x.device)
-    _need_feature(y, "y", ctx.device, x.dtype, x.shape)
-    _need(stats, "stats", (torch.float32,), d.batch * d.tokens * 2, ctx.device)
-    d.y_stride[:] = _image_strides(y, "y")
-    ctx.check(load().gsr_layer_norm_forward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(x),
-                                            _ptr(gamma), _ptr(beta), _ptr(y), _ptr(stats)), "gsr_layer_norm_forward")
+    else:
+        _need_floats(stats, "stats", d.batch * tokens * 2, ctx.device)
+    ctx.check(load().gsr_layer_norm_forward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), x.data_ptr(),
+                                            None if gamma is None else gamma.data_ptr(),
+                                            None if beta is None else beta.data_ptr(), y.data_ptr(),
+                                            stats.data_ptr()), "gsr_layer_norm_forward")
     return y, stats
 
 
@@ -770,23 +788,28 @@ def gsr_layer_norm_backward(ctx: Context, x: torch.Tensor, gamma: torch.Tensor |
     """Returns (dx like x, dgamma float32 [C], dbeta float32 [C]) for the upstream gradient dy (like x); `dx` may be
     dy."""
     d = _layer_norm_desc(ctx, x, gamma, None, 0.0)
-    dev, C = ctx.device, x.shape[-1]
-    _need(stats, "stats", (torch.float32,), d.batch * d.tokens * 2, dev)
+    dev, tokens, C = ctx.device, d.tokens, d.channels
+    _need_floats(stats, "stats", d.batch * tokens * 2, dev)
     _need_feature(dy, "dy", dev, x.dtype, x.shape)
+    d.dy_stride[:] = _token_strides(dy, "dy", tokens, C)
     if dx is None:
         dx = _like(x)
+        d.dx_stride[:] = tokens * C, C
+    else:
+        _need_feature(dx, "dx", dev, x.dtype, x.shape)
+        d.dx_stride[:] = _token_strides(dx, "dx", tokens, C)
     if dgamma is None:
         dgamma = torch.empty(C, dtype=torch.float32, device=dev)
+    else:
+        _need_floats(dgamma, "dgamma", C, dev)
     if dbeta is None:
-        dbeta = torch.empty(C, dtype=torch.float32, device=dev)
-    _need_feature(dx, "dx", dev, x.dtype, x.shape)
-    _need(dgamma, "dgamma", (torch.float32,), C, dev)
-    _need(dbeta, "dbeta", (torch.float32,), C, dev)
-    d.dy_stride[:] = _image_strides(dy, "dy")
-    d.dx_stride[:] = _image_strides(dx, "dx")
-    ctx.check(load().gsr_layer_norm_backward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(x),
-                                             _ptr(gamma), _ptr(stats), _ptr(dy), _ptr(dx), _ptr(dgamma),
-                                             _ptr(dbeta)), "gsr_layer_norm_backward")
+        dbeta = torch.empty_like(dgamma)
+    else:
+        _need_floats(dbeta, "dbeta", C, dev)
+    ctx.check(load().gsr_layer_norm_backward(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), x.data_ptr(),
+                                             None if gamma is None else gamma.data_ptr(), stats.data_ptr(),
+                                             dy.data_ptr(), dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr()),
+              "gsr_layer_norm_backward")
     return dx, dgamma, dbeta
 
 
@@ -804,11 +827,10 @@ def _newton_schulz_desc(ctx, g, name, steps, coefficients, eps):
         table = (table,) * steps
     if len(table) != steps or any(len(c) != 3 for c in table):
         raise ValueError("coefficients must be (a, b, c), or one such triple for each step")
-    batch = g.shape[0] if g.dim() == 3 else 1
-    _fit("batch, rows, cols", batch | g.shape[-2] | g.shape[-1])
-    d = gsr_newton_schulz(_DTYPES[g.dtype], batch, g.shape[-2], g.shape[-1], steps, eps)
-    for k, c in enumerate(table):
-        d.coefficients[k][:] = c
+    shape = g.shape
+    batch, rows, cols = shape if len(shape) == 3 else (1, *shape)
+    _fit("batch, rows, cols", batch | rows | cols)
+    d = gsr_newton_schulz(_DTYPES[g.dtype], batch, rows, cols, steps, eps, table)
     d.grad_stride[:] = _matrix_strides(g)
     return d
 
@@ -826,10 +848,11 @@ def gsr_orthogonalize(ctx: Context, g: torch.Tensor, steps: int = 5, coefficient
     d = _newton_schulz_desc(ctx, g, "g", steps, coefficients, eps)
     if out is None:
         out = _like(g)
-    _need_feature(out, "out", ctx.device, g.dtype, g.shape)
+    else:
+        _need_feature(out, "out", ctx.device, g.dtype, g.shape)
     d.out_stride[:] = _matrix_strides(out)
-    ctx.check(load().gsr_orthogonalize(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(g), _ptr(out)),
-              "gsr_orthogonalize")
+    ctx.check(load().gsr_orthogonalize(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), g.data_ptr(),
+                                       out.data_ptr()), "gsr_orthogonalize")
     return out
 
 
@@ -843,5 +866,6 @@ def gsr_muon_step(ctx: Context, param: torch.Tensor, grad: torch.Tensor, momentu
     _need_feature(momentum, "momentum", ctx.device, torch.float32, grad.shape)
     d.out_stride[:] = _matrix_strides(param)
     d.momentum_stride[:] = _matrix_strides(momentum)
-    ctx.check(load().gsr_muon_step(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), _ptr(grad), _ptr(param),
-                                   _ptr(momentum), lr, mu, int(bool(nesterov)), decay), "gsr_muon_step")
+    ctx.check(load().gsr_muon_step(ctx.handle, _stream_on(ctx, stream), ctypes.byref(d), grad.data_ptr(),
+                                   param.data_ptr(), momentum.data_ptr(), lr, mu, int(bool(nesterov)), decay),
+              "gsr_muon_step")

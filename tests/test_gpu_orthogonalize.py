@@ -70,7 +70,7 @@ def check(g, got, steps, what, eps=0.0, rounded=True):
     (1, 1, 1), (2, 1, 7), (3, 5, 1), (2, 10, 64), (1, 63, 65), (4, 64, 64), (2, 192, 64), (1, 128, 128), (2, 129, 40),
     (1, 96, 513), (2, 200, 333), (1, 700, 130), (1, 512, 512), (1, 520, 640), (2, 513, 1100), (1, 30, 5000),
     (2, 65, 64), (3, 100, 300), (1, 128, 129), (2, 1500, 33), (1, 120, 2050), (1, 4000, 128), (2, 64, 129), (1, 127, 127), (2, 64, 256), (1, 511, 50),
-    (3, 17, 300), (1, 64, 513), (2, 9000, 70), (1, 90, 600)])
+    (3, 17, 300), (1, 64, 513), (2, 9000, 70), (1, 90, 600), (1, 200, 4100), (1, 2500, 300), (1, 513, 2100)])
 def test_sizes(ctx, dtype, batch, m, n):
     from differentiable_gaussian_splatting_amd import gsr
     banner(f"orthogonalize {dtype} {batch} x {m} x {n}")
@@ -82,7 +82,7 @@ def test_sizes(ctx, dtype, batch, m, n):
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("kind", ["low rank", "steep"])
-@pytest.mark.parametrize("m,n", [(64, 100), (300, 180), (530, 600)])
+@pytest.mark.parametrize("m,n", [(64, 100), (300, 180), (530, 600), (300, 4100)])
 def test_decaying_spectra(ctx, dtype, kind, m, n):
     from differentiable_gaussian_splatting_amd import gsr
     banner(f"orthogonalize {dtype} {kind} {m} x {n}")
