@@ -201,7 +201,7 @@ struct Stage {
 
 // How many stages of tiles LDS holds: copies run that many ahead, less what is being multiplied.
 template <int kTile, int PLANES>
-constexpr int kStages = kTile == 64 ? 4 : (kTile == 128 && PLANES < 4 ? 3 : 2);
+constexpr int kStages = kTile == 64 ? 4 : (kTile == 192 || (kTile == 128 && PLANES < 4) ? 3 : 2);
 
 // The sums of a workgroup's tile: wave (w / 2, w % 2) of 2 x 2 has rows row .. and columns col .. , lane l row
 // row + 32 i + l % 32 and columns col + 32 j + 8 q + 4 (l / 32) + {0..3} in acc[i][j][4 q ..].
@@ -1138,8 +1138,7 @@ uint64_t round_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 // The side of the square tiles of a product, and its time in us: the one whose rounds of workgroups take least.
 // `tiles(side)` counts them. Measured for tiles of depth 1,024 in two planes, one workgroup after the other on a compute
-// unit: 12.8, 31, 56 and 95 us, and about 4 us of a launch's own; small tiles overlap, so that part of a round of them
-// counts as part. 8 x 1,024 x 4,096: P X 243 us with tiles of 256, 278 with 128, 416 with 64; 4,096 x 1,024: X X^T 36 us
+// unit: 12.8, 31, 56 and 95 us, and about 4 us of a launch's own. 8 x 1,024 x 4,096: P X 243 us with tiles of 256, 278 with 128, 416 with 64; 4,096 x 1,024: X X^T 36 us
 // with tiles of 64, 91 with 128; 4,096 x 4,096: A A^T 205 us with 253 tiles of 192, 250 with 136 of 256, 276 with 528 of
 // 128.
 struct Side {
@@ -1152,7 +1151,9 @@ Side tile_side(uint64_t deep, F tiles) {
   Side best{0, 1e300};
   for (const auto& [side, us] : {std::pair(64, 12.8), std::pair(128, 31.0), std::pair(192, 56.0), std::pair(256, 95.0)}) {
     const double rounds = double(tiles(uint64_t(side))) / 256;
-    const double time = us * (side == 64 ? std::max(1.0, rounds) : std::ceil(rounds)) * double(deep) / 1024 + 4;
+    // tiles of 64 overlap on a compute unit, those of 128 in part
+    const double whole = std::ceil(rounds), count = side == 64 ? std::max(1.0, rounds) : (side == 128 ? (whole + rounds) / 2 : whole);
+    const double time = us * count * double(deep) / 1024 + 4;
     if (time < best.us) best = Side{side, time};
   }
   return best;
@@ -1258,7 +1259,7 @@ bool pairs_pay(const OrthShape& g) {
   auto across = [](uint64_t n, uint64_t side) { return (n + side - 1) / side; };
   auto triangle = [&](uint64_t side) { return across(g.rp, side) * (across(g.rp, side) + 1) / 2 * g.batch; };
   auto whole = [&](uint64_t side) { return across(g.rp, side) * across(g.cp, side) * g.batch; };
-  return tile_side(g.cp, triangle).us + tile_side(g.rp, whole).us > 3 * tile_side(g.rp, triangle).us;
+  return tile_side(g.cp, triangle).us + tile_side(g.rp, whole).us > 3.3 * tile_side(g.rp, triangle).us;
 }
 
 template <int R, int S, typename T, bool MUON, typename RT>
