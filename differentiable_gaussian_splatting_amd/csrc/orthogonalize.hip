@@ -119,6 +119,14 @@ __device__ __forceinline__ double first_scale(const OrthShape& g, double sum) {
   return norm - norm == 0.0 ? (norm > 0.0 ? double(g.first) / norm : 0.0) : norm - norm;
 }
 
+// Matrices in scratch: a row of n numbers is n float16 values (one plane), or 2 n, the hi and lo parts of 32 columns in
+// turn: what a stage of a product reads of a row is then one whole 128-byte line, not halves of two (every half is a
+// request to the second level of cache, whose rate bounds the large products). Where column col of plane p lies in a row:
+template <int PLANES>
+__device__ __forceinline__ uint64_t place(uint64_t col, int p) {
+  return PLANES == 2 ? col / 32 * 64 + p * 32 + col % 32 : col;
+}
+
 // X_0 and its transpose in two planes each, zeros in the padding. A workgroup takes a 64 x 64 tile.
 template <typename T, bool MUON>
 __global__ __launch_bounds__(kThreads) void k_orth_start(OrthShape g, Source<T, MUON> src,
@@ -161,17 +169,18 @@ __global__ __launch_bounds__(kThreads) void k_orth_start(OrthShape g, Source<T, 
         hi[k] = h;
         lo[k] = l;
       }
-      const uint64_t at = turned ? (c0 + i) * g.rp + r0 + j : (r0 + i) * g.cp + c0 + j;
-      *reinterpret_cast<Vec<half, 8>*>(out + at) = hi;
-      *reinterpret_cast<Vec<half, 8>*>(out + plane + at) = lo;
+      half* at = out + (turned ? (c0 + i) * g.rp : (r0 + i) * g.cp) * 2;
+      *reinterpret_cast<Vec<half, 8>*>(at + place<2>((turned ? r0 : c0) + j, 0)) = hi;
+      *reinterpret_cast<Vec<half, 8>*>(at + place<2>((turned ? r0 : c0) + j, 1)) = lo;
     }
   }
 }
 
-// One operand of a product: planes of [rows][ld] float16 from base on, `plane` elements apart.
+// One operand of a product: rows of `ld` float16 values from base on; 32 of its columns are `step` values.
 struct Operand {
   const half* base;
-  uint64_t plane, ld, rows;
+  uint64_t ld, rows;
+  int step;
 };
 
 __device__ __forceinline__ void to_lds(const half* p, char* s) {
@@ -179,29 +188,33 @@ __device__ __forceinline__ void to_lds(const half* p, char* s) {
                                    (__attribute__((address_space(3))) void*)s, 16, 0, 0);
 }
 
-// An LDS tile of kTile rows of kDeep values.
-template <int kTile>
+// An LDS tile of kTile rows of kDeep numbers in P planes, as they lie in memory.
+template <int kTile, int P>
 struct Stage {
-  using L = Tile<half, kDeep>;
-  static constexpr int kBytes = kTile * kDeep * 2;
+  using L = Tile<half, kDeep * P>;
+  static constexpr int kBytes = kTile * kDeep * 2 * P;
   static constexpr int kPass = kThreads / L::kChunks;  // rows that the workgroup copies at a time
   static constexpr int kCopies = kTile / kPass;
 
-  // Starts the copy of rows row .. , values k .. of one plane of rows x ld; rows beyond repeat the last.
-  __device__ static __forceinline__ void start(const half* p, uint64_t ld, uint64_t rows, uint64_t row, uint64_t k,
-                                               char* s) {
+  // Starts the copy of rows row .. , numbers k .. ; rows beyond repeat the last.
+  __device__ static __forceinline__ void start(const Operand& o, uint64_t row, uint64_t k, char* s) {
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
     const int r = int(threadIdx.x) / L::kChunks;
     const int c = ((int(threadIdx.x) % L::kChunks) ^ L::swizzle(r)) * 8;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
-      to_lds(p + min(row + r + i * kPass, rows - 1) * ld + k + c, s + i * kPass * L::kRowBytes + wave * 1024);
+      to_lds(o.base + min(row + r + i * kPass, o.rows - 1) * o.ld + k / kDeep * o.step + c,
+             s + i * kPass * L::kRowBytes + wave * 1024);
+  }
+  // Depths 16 kk + 8 h .. + 7 of row r0 + l % 32 of plane p.
+  __device__ static __forceinline__ Vec<half, 8> frag(const char* s, int r0, int p, int kk) {
+    return L::frag(s, r0, 2 * p + kk);
   }
 };
 
 // How many stages of tiles LDS holds: copies run that many ahead, less what is being multiplied.
 template <int kTile, int PLANES>
-constexpr int kStages = kTile == 64 ? 4 : (kTile == 192 || (kTile == 128 && PLANES < 4) ? 3 : 2);
+constexpr int kStages = kTile == 64 ? 3 : (kTile == 192 || (kTile == 128 && PLANES < 4) ? 3 : 2);
 
 // The sums of a workgroup's tile: wave (w / 2, w % 2) of 2 x 2 has rows row .. and columns col .. , lane l row
 // row + 32 i + l % 32 and columns col + 32 j + 8 q + 4 (l / 32) + {0..3} in acc[i][j][4 q ..].
@@ -244,9 +257,10 @@ struct Lds {
 template <int kTile, int LP, int RP>
 __device__ __forceinline__ void product(const Operand& left, const Operand& right, uint64_t row, uint64_t col,
                                         uint64_t deep, char* lds, Sums<kTile>& s) {
-  using S = Stage<kTile>;
+  using SL = Stage<kTile, LP>;
+  using SR = Stage<kTile, RP>;
   constexpr int kStage = Lds<kTile, LP, RP>::kStage, kCount = kStages<kTile, LP + RP>, kBlocks = kTile / 64;
-  constexpr int kCopies = (LP + RP) * S::kCopies;  // of a stage, by each wave
+  constexpr int kCopies = SL::kCopies + SR::kCopies;  // of a stage, by each wave
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
   const int wr = (wave >> 1) * (kTile / 2), wc = (wave & 1) * (kTile / 2);
   s.row = row + wr;
@@ -258,13 +272,8 @@ __device__ __forceinline__ void product(const Operand& left, const Operand& righ
 #pragma unroll
       for (int e = 0; e < 16; ++e) s.acc[i][j][e] = 0.0f;
   auto start = [&](uint64_t k, int stage) {
-    char* to = lds + stage * kStage;
-#pragma unroll
-    for (int p = 0; p < LP; ++p)
-      S::start(left.base + p * left.plane, left.ld, left.rows, row, k, to + p * S::kBytes);
-#pragma unroll
-    for (int p = 0; p < RP; ++p)
-      S::start(right.base + p * right.plane, right.ld, right.rows, col, k, to + (LP + p) * S::kBytes);
+    SL::start(left, row, k, lds + stage * kStage);
+    SR::start(right, col, k, lds + stage * kStage + SL::kBytes);
   };
   // Fragments of the two halves of a stage. While one half is multiplied the next half's are read, so that the matrix cores
   // wait for neither LDS nor the barrier, which lies between the halves: behind it this stage's tiles are read to the end
@@ -272,13 +281,13 @@ __device__ __forceinline__ void product(const Operand& left, const Operand& righ
   // repeat the last stage.
   Vec<half, 8> a[2][LP][kBlocks], b[2][RP][kBlocks];
   auto read = [&](const char* sl, int kk) {
-    const char* sr = sl + LP * S::kBytes;
+    const char* sr = sl + SL::kBytes;
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) {
 #pragma unroll
-      for (int p = 0; p < LP; ++p) a[kk][p][i] = S::L::frag(sl + p * S::kBytes, wr + 32 * i, kk);
+      for (int p = 0; p < LP; ++p) a[kk][p][i] = SL::frag(sl, wr + 32 * i, p, kk);
 #pragma unroll
-      for (int p = 0; p < RP; ++p) b[kk][p][i] = S::L::frag(sr + p * S::kBytes, wc + 32 * i, kk);
+      for (int p = 0; p < RP; ++p) b[kk][p][i] = SR::frag(sr, wc + 32 * i, p, kk);
     }
   };
   auto multiply = [&](int kk) {
@@ -331,14 +340,16 @@ struct Turn {
   __device__ static __forceinline__ Vec<half, 4>& at(char* s, int col) {
     return *reinterpret_cast<Vec<half, 4>*>(s + (threadIdx.x & 31) * kStride + col * 2);
   }
-  // Loads rows row .. and columns col .. of in, [size_r][ld], 16 bytes a lane at a time (what lies beyond repeats the last
-  // ones), and lays them into LDS.
-  __device__ static __forceinline__ void fetch(const half* in, uint64_t ld, uint64_t row, uint64_t col, uint64_t size_r,
-                                               u32x4* v) {
+  // Loads rows row .. and columns col .. of plane p of in, [size_r][size_c] in PLANES planes, 16 bytes a lane at a time (what
+  // lies beyond repeats the last ones), and lays them into LDS.
+  template <int PLANES>
+  __device__ static __forceinline__ void fetch(const half* in, int p, uint64_t size_r, uint64_t size_c, uint64_t row,
+                                               uint64_t col, u32x4* v) {
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
       const int e = t * 64 + int(threadIdx.x & 63), r = e / kChunks, c = e % kChunks;
-      v[t] = *reinterpret_cast<const u32x4*>(in + min(row + r, size_r - 1) * ld + min(col + 8 * c, ld - 8));
+      v[t] = *reinterpret_cast<const u32x4*>(in + min(row + r, size_r - 1) * size_c * PLANES +
+                                             place<PLANES>(min(col + 8 * c, size_c - 8), p));
     }
   }
   __device__ static __forceinline__ void lay(const u32x4* v, char* s) {
@@ -348,19 +359,22 @@ struct Turn {
       *reinterpret_cast<u32x4*>(s + e / kChunks * kStride + e % kChunks * 16) = v[t];
     }
   }
-  // Rows row .. and columns col .. of out, [size_r][ld], in 16-byte stores.
-  __device__ static __forceinline__ void rows(const char* s, half* out, uint64_t ld, uint64_t row, uint64_t col,
-                                              uint64_t size_r) {
+  // Rows row .. and columns col .. of plane p of out, [size_r][size_c], in 16-byte stores.
+  template <int PLANES>
+  __device__ static __forceinline__ void rows(const char* s, half* out, int p, uint64_t size_r, uint64_t size_c,
+                                              uint64_t row, uint64_t col) {
 #pragma unroll
     for (int t = 0; t < kTurns; ++t) {
       const int e = t * 64 + int(threadIdx.x & 63), r = e / kChunks, c = e % kChunks;
       const u32x4 v = *reinterpret_cast<const u32x4*>(s + r * kStride + c * 16);
-      if (row + r < size_r && col + 8 * c < ld) *reinterpret_cast<u32x4*>(out + (row + r) * ld + col + 8 * c) = v;
+      if (row + r < size_r && col + 8 * c < size_c)
+        *reinterpret_cast<u32x4*>(out + (row + r) * size_c * PLANES + place<PLANES>(col + 8 * c, p)) = v;
     }
   }
-  // The transposed 32 columns: rows col .. and columns row .. of out, 64 bytes of a row together.
-  __device__ static __forceinline__ void columns(const char* s, half* out, uint64_t ld, uint64_t row, uint64_t col,
-                                                 uint64_t size_r) {
+  // Transposed: rows col .. and the 32 columns row .. of plane p of out, [size_r][size_c], 64 bytes of a row together.
+  template <int PLANES>
+  __device__ static __forceinline__ void columns(const char* s, half* out, int p, uint64_t size_r, uint64_t size_c,
+                                                 uint64_t row, uint64_t col) {
     const int l = threadIdx.x & 63, g = l >> 4, j = l & 15;
     using s16x4 = Vec<short, 4>;
     using P = __attribute__((address_space(3))) s16x4*;
@@ -372,8 +386,8 @@ struct Turn {
       const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(at + 4 * kStride));
       using s16x8 = Vec<short, 8>;
       const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      if (col + c + j < size_r && row + 8 * g < ld)
-        *reinterpret_cast<s16x8*>(out + (col + c + j) * ld + row + 8 * g) = v;
+      if (col + c + j < size_r && row + 8 * g < size_c)
+        *reinterpret_cast<s16x8*>(out + (col + c + j) * size_c * PLANES + place<PLANES>(row + 8 * g, p)) = v;
     }
   }
 };
@@ -460,19 +474,18 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_symmetri
   const uint64_t b = id / tiles;
   uint32_t ti, tj;
   triangle(uint32_t(id - b * tiles), &ti, &tj);
-  const uint64_t plane = rp * rp;
   left.base += b * matrix;
   right.base += b * matrix;
-  in += b * PLANES * plane;
-  in2 += b * PLANES * plane;
-  out += b * PLANES * plane;
+  in += b * PLANES * rp * rp;
+  in2 += b * PLANES * rp * rp;
+  out += b * PLANES * rp * rp;
   Sums<kTile> s;
   product<kTile, PLANES, PLANES>(left, right, uint64_t(ti) * kTile, uint64_t(tj) * kTile, deep, lds, s);
   char* mine = lds + (threadIdx.x >> 6) * PLANES * L::kBytes;
   u32x4 have[PLANES][L::kTurns];
   auto fetch = [&](const half* from, uint64_t row) {
 #pragma unroll
-    for (int p = 0; p < PLANES; ++p) L::fetch(from + p * plane, rp, row, s.col, rp, have[p]);
+    for (int p = 0; p < PLANES; ++p) L::template fetch<PLANES>(from, p, rp, rp, row, s.col, have[p]);
   };
   if constexpr (ADD > 0) fetch(in, s.row);
 #pragma unroll
@@ -500,8 +513,8 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_symmetri
     wave_sync();
 #pragma unroll
     for (int p = 0; p < PLANES; ++p) {
-      L::rows(mine + p * L::kBytes, out + p * plane, rp, row, s.col, rp);
-      if (ti != tj) L::columns(mine + p * L::kBytes, out + p * plane, rp, row, s.col, rp);
+      L::template rows<PLANES>(mine + p * L::kBytes, out, p, rp, rp, row, s.col);
+      if (ti != tj) L::template columns<PLANES>(mine + p * L::kBytes, out, p, rp, rp, row, s.col);
     }
   }
 }
@@ -532,10 +545,10 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_apply(
   const uint32_t tr = uint32_t(id % tiles_r);
   id /= tiles_r;
   const uint32_t tc = uint32_t(id % tiles_c);
-  const uint64_t b = id / tiles_c, plane = g.rp * g.cp;
-  p.base += b * PP * p.plane;
-  x += b * 2 * plane;
-  const Operand right{xt + b * 2 * plane, plane, g.rp, g.cp};
+  const uint64_t b = id / tiles_c, matrix = 2 * g.rp * g.cp;
+  p.base += b * PP * g.rp * g.rp;
+  x += b * matrix;
+  const Operand right{xt + b * matrix, 2 * g.rp, g.cp, 64};
   Sums<kTile> s;
   product<kTile, PP, 2>(p, right, uint64_t(tr) * kTile, uint64_t(tc) * kTile, g.rp, lds, s);
   const int l = threadIdx.x & 63;
@@ -545,7 +558,7 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_apply(
   u32x4 have[2][L::kTurns];
   auto fetch = [&](uint64_t row) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) L::fetch(x + q * plane, g.cp, row, s.col, g.rp, have[q]);
+    for (int q = 0; q < 2; ++q) L::template fetch<2>(x, q, g.rp, g.cp, row, s.col, have[q]);
   };
   fetch(s.row);
 #pragma unroll
@@ -562,8 +575,8 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_apply(
       wave_sync();
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        L::rows(mine + q * L::kBytes, x + q * plane, g.cp, row, s.col, g.rp);
-        L::columns(mine + q * L::kBytes, next + (b * 2 + q) * plane, g.rp, row, s.col, g.cp);
+        L::template rows<2>(mine + q * L::kBytes, x, q, g.rp, g.cp, row, s.col);
+        L::template columns<2>(mine + q * L::kBytes, next + b * matrix, q, g.cp, g.rp, row, s.col);
       }
       continue;
     }
@@ -1011,6 +1024,7 @@ __global__ __launch_bounds__(4 * R) void k_orth_strips(OrthShape g, SmallStep st
     f32x16 a[C::kABlocks];
     clear(a);
     const float* in = parts_in + size_t(b) * part_stride + (row + (l & 31)) * R + acol + 4 * (l >> 5);
+#pragma unroll 4
     for (uint32_t w = 0; w < parts; ++w, in += R * R) {
 #pragma unroll
       for (int j = 0; j < C::kABlocks; ++j)
@@ -1207,11 +1221,11 @@ void launch_steps(hipStream_t s, const OrthShape& g, const Plan& plan, const Sou
   using Add0 = std::integral_constant<int, 0>;
   using Add1 = std::integral_constant<int, 1>;
   auto pow2 = [](double v, int e) { return float(std::ldexp(v, e)); };
-  auto sq = [&](const half* m) { return Operand{m, square, g.rp, g.rp}; };
+  auto sq = [&](const half* m) { return Operand{m, PLANES * g.rp, g.rp, 32 * PLANES}; };
   for (int k = 0; k < plan.steps; ++k) {
     const Step c = plan.step[k];
     const int ex = plan.x_exp[k], ea = plan.a_exp[k], ep = plan.p_exp[k];
-    const Operand xo{x, plane, g.cp, g.rp};
+    const Operand xo{x, 2 * g.cp, g.rp, 64};  // with one plane to read, its hi parts
     symmetric(Add0(), side_g, xo, xo, 2 * plane, g.cp, pow2(1, ea - 2 * ex), am, am, 0.0f, am, 0.0f);
     symmetric(Add1(), side_s, sq(am), sq(am), PLANES * square, g.rp, pow2(c.c, ep - 2 * ea), pm, am, pow2(c.b, ep - ea), am,
               0.0f);
@@ -1275,8 +1289,9 @@ void launch_strips(hipStream_t s, const OrthShape& g, const SmallPlan& plan, con
   hipLaunchKernelGGL((k_orth_norm<T, MUON>), dim3(g.parts, g.batch), dim3(kThreads), 0, s, g, src, norm);
   float* other = parts + size_t(g.batch) * ways * R * R;
   const dim3 grid(ways, g.batch);
-  // every workgroup adds up to four parts itself; more are added by a launch of their own
-  const bool sum = ways > 4;
+  // every workgroup adds up to 128 KB of parts itself; more are added by a launch of their own (64 x 1,000, 128 KB: 64.6 us
+  // against 65.4; 64 x 1,500, 192 KB: 74.1 against 62.5; 100 x 400, 256 KB: 115 against 101)
+  const bool sum = ways * R * R * sizeof(float) > (128u << 10);
   auto launch = [&](auto kernel, const SmallStep& st) {
     hipLaunchKernelGGL(kernel, grid, dim3(kT), 0, s, g, st, src, res, norm, x, other, sum ? 1 : ways,
                        size_t(ways) * R * R, parts);
