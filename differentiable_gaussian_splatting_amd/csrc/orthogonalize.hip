@@ -196,15 +196,25 @@ struct Stage {
   static constexpr int kPass = kThreads / L::kChunks;  // rows that the workgroup copies at a time
   static constexpr int kCopies = kTile / kPass;
 
-  // Starts the copy of rows row .. , numbers k .. ; rows beyond repeat the last.
-  __device__ static __forceinline__ void start(const Operand& o, uint64_t row, uint64_t k, char* s) {
-    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
+  // Where this thread's chunks lie from the tile's first row on, in bytes; rows beyond repeat the last.
+  uint32_t off[kCopies];
+  const char* at;  // the next stage of the first row
+  int step;
+  __device__ __forceinline__ void set(const Operand& o, uint64_t row) {
     const int r = int(threadIdx.x) / L::kChunks;
     const int c = ((int(threadIdx.x) % L::kChunks) ^ L::swizzle(r)) * 8;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
-      to_lds(o.base + min(row + r + i * kPass, o.rows - 1) * o.ld + k / kDeep * o.step + c,
-             s + i * kPass * L::kRowBytes + wave * 1024);
+      off[i] = uint32_t((min(row + r + i * kPass, o.rows - 1) - row) * o.ld + c) * 2;
+    at = reinterpret_cast<const char*>(o.base + row * o.ld);
+    step = o.step * 2;
+  }
+  // Starts the copy of the next stage, and moves on if there is another.
+  __device__ __forceinline__ void start(char* s, int wave, bool on) {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      to_lds(reinterpret_cast<const half*>(at + off[i]), s + i * kPass * L::kRowBytes + wave * 1024);
+    at += on ? step : 0;
   }
   // Depths 16 kk + 8 h .. + 7 of row r0 + l % 32 of plane p.
   __device__ static __forceinline__ Vec<half, 8> frag(const char* s, int r0, int p, int kk) {
@@ -245,6 +255,15 @@ __device__ __forceinline__ void spread(std::integer_sequence<int, E...>) {
   (spread_one<SYNC, PRODUCTS, READS, COPIES, E>(), ...);
 }
 
+// tile_barrier by instructions that the compiler knows: it then does not wait again for LDS reads that are done.
+template <int PENDING>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((PENDING & 15) | (PENDING >> 4 << 14) | 7 << 4);  // copies; nothing of LDS
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // One kTile x kTile tile of a product of depth `deep`: rows row .. of the left operand (LP planes) by rows col .. of the
 // right one (RP planes), depths adjacent in both. The blocks are computed transposed, so that a lane holds one row of the
 // result and adjacent columns. What lies past the operands' rows is computed and of no use. The workgroup's waves are
@@ -271,9 +290,13 @@ __device__ __forceinline__ void product(const Operand& left, const Operand& righ
     for (int j = 0; j < kBlocks; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s.acc[i][j][e] = 0.0f;
-  auto start = [&](uint64_t k, int stage) {
-    SL::start(left, row, k, lds + stage * kStage);
-    SR::start(right, col, k, lds + stage * kStage + SL::kBytes);
+  SL copy_l;
+  SR copy_r;
+  copy_l.set(left, row);
+  copy_r.set(right, col);
+  auto start = [&](int stage, bool on) {
+    copy_l.start(lds + stage * kStage, wave, on);
+    copy_r.start(lds + stage * kStage + SL::kBytes, wave, on);
   };
   // Fragments of the two halves of a stage. While one half is multiplied the next half's are read, so that the matrix cores
   // wait for neither LDS nor the barrier, which lies between the halves: behind it this stage's tiles are read to the end
@@ -302,27 +325,28 @@ __device__ __forceinline__ void product(const Operand& left, const Operand& righ
             for (int j = 0; j < kBlocks; ++j) s.acc[i][j] = mma(b[kk][q][j], a[kk][p][i], s.acc[i][j]);
   };
   constexpr int kReads = (LP + RP) * kBlocks, kProducts = (LP + RP - 1) * kBlocks * kBlocks;
+  int more = int(deep / kDeep) - 1;  // stages past the one whose copy starts next; then the last repeats
 #pragma unroll
-  for (int i = 0; i < kCount; ++i) start(min(uint64_t(i) * kDeep, deep - kDeep), i);
-  tile_barrier<(kCount - 1) * kCopies>();
+  for (int i = 0; i < kCount; ++i) start(i, more-- > 0);
+  stage_barrier<(kCount - 1) * kCopies>();
   read(lds, 0);
   int now = 0;
-  for (uint64_t k = 0; k < deep; k += kDeep) {
+  for (int stages = int(deep / kDeep); stages > 0; --stages) {
     read(lds + now * kStage, 1);
     multiply(0);
     spread<0, kProducts, kReads, 0>(std::make_integer_sequence<int, kProducts>());
     __builtin_amdgcn_sched_barrier(0);
-    tile_barrier<(kCount - 2) * kCopies>();
+    stage_barrier<(kCount - 2) * kCopies>();
     __builtin_amdgcn_sched_barrier(0);
     const int done = now;
     now = now + 1 == kCount ? 0 : now + 1;
     read(lds + now * kStage, 0);
-    start(min(k + kCount * kDeep, deep - kDeep), done);
+    start(done, more-- > 0);
     multiply(1);
     spread<1, kProducts, kReads, kCopies>(std::make_integer_sequence<int, kProducts>());
     __builtin_amdgcn_sched_barrier(0);
   }
-  tile_barrier<0>();
+  stage_barrier<0>();
 }
 
 // Orders a wave's LDS writes before its reads of what other lanes wrote.
