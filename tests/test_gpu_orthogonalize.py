@@ -136,8 +136,26 @@ def test_scales_zeros_and_bad_values(ctx, m, n):
             assert torch.equal(out[1], clean[1]) and torch.equal(out[4], clean[4])
 
 
+# tiles of 64 to 256, in both kinds of products, by the number of matrices; odd counts of tiles; two steps at a time
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("m,n", [(40, 72), (72, 40), (300, 180), (530, 650)])
+@pytest.mark.parametrize("batch,m,n", [
+    (16, 520, 640), (40, 520, 640), (64, 500, 500), (85, 500, 500), (24, 1900, 600), (3, 1100, 1030), (7, 300, 2500)])
+def test_stacks(ctx, dtype, batch, m, n):
+    """Copies of three matrices: the copies have the same bits, the three are held to the oracle. (Bits differ between
+    stacks of other sizes: a tile on the diagonal adds hi lo before lo hi on both of its sides, mirrored tiles on one.)"""
+    from differentiable_gaussian_splatting_amd import gsr
+    banner(f"orthogonalize {dtype} {batch} x {m} x {n}, copies")
+    few = gradient(2, 3, m, n, DTYPES[dtype]).cuda()
+    stack = few.repeat(batch // 3 + 1, 1, 1)[:batch]
+    for steps in (2, 5):
+        got = gsr.gsr_orthogonalize(ctx, stack, steps)
+        for i in range(batch):
+            assert torch.equal(got[i], got[i % 3]), i
+        check(few, got[:3], [QUINTIC] * steps, f"{dtype} of {batch}, {steps} steps", 1e-7)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n", [(40, 72), (72, 40), (300, 180), (530, 650), (70, 900), (260, 1200)])
 def test_strided_broadcast_in_place_repeated(ctx, dtype, m, n):
     from differentiable_gaussian_splatting_amd import gsr
     banner(f"orthogonalize strided, in place, repeated, {dtype} {m} x {n}")
@@ -164,7 +182,7 @@ def test_strided_broadcast_in_place_repeated(ctx, dtype, m, n):
     assert torch.equal(wide, before)
 
 
-@pytest.mark.parametrize("m,n", [(40, 72), (300, 180)])
+@pytest.mark.parametrize("m,n", [(40, 72), (300, 180), (70, 900), (1200, 260)])
 def test_graph_replays(ctx, m, n):
     from differentiable_gaussian_splatting_amd import gsr
     banner(f"orthogonalize and step in a graph, {m} x {n}")
@@ -191,7 +209,8 @@ def test_graph_replays(ctx, m, n):
 
 @pytest.mark.parametrize("grad", list(DTYPES))
 @pytest.mark.parametrize("nesterov", [True, False])
-@pytest.mark.parametrize("batch,m,n", [(2, 64, 64), (1, 192, 64), (3, 10, 64), (2, 150, 333), (1, 640, 520)])
+@pytest.mark.parametrize("batch,m,n", [(2, 64, 64), (1, 192, 64), (3, 10, 64), (2, 150, 333), (1, 640, 520), (2, 100, 700),
+                                       (1, 1100, 90), (60, 256, 140)])
 def test_muon_step(ctx, grad, nesterov, batch, m, n):
     from differentiable_gaussian_splatting_amd import gsr
     banner(f"muon step {grad} nesterov {nesterov} {batch} x {m} x {n}")
@@ -223,7 +242,7 @@ def test_muon_step(ctx, grad, nesterov, batch, m, n):
 def test_muon_step_of_strided_stacks(ctx):
     from differentiable_gaussian_splatting_amd import gsr
     banner("muon step of strided parameters")
-    for m, n in ((40, 72), (300, 180)):
+    for m, n in ((40, 72), (300, 180), (70, 900), (900, 70)):
         big_p, big_m = normal(1, (3, m + 3, n + 5)).cuda(), normal(2, (3, m + 1, n + 2)).cuda()
         big_g = gradient(3, 3, m, n + 9, torch.bfloat16).cuda()
         p, mom, g = big_p[:, 2:-1, 3:n + 3], big_m[:, 1:, 1:n + 1], big_g[:, :, 4:n + 4]
