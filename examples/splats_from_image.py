@@ -3,9 +3,10 @@
 The image's 8 x 8 patches become tokens (a linear layer, group norm with SiLU), learned splat queries on a grid attend to
 them (rotary positions with two axes on queries and keys, cross attention), and a linear head turns each query's result
 into one Gaussian, which is projected, binned and rendered; the L1 + SSIM loss runs back the same way and one fused Adam
-step updates every weight. Everything but the linear layers (torch matrix products) is the library's.
+step updates every weight, or, with --optimiser muon, Adam the norm and the queries and orthogonalised momentum the
+matrices. Everything but the linear layers (torch matrix products) is the library's.
 
-    python examples/splats_from_image.py [--steps 60]
+    python examples/splats_from_image.py [--steps 60] [--optimiser muon]
 """
 from __future__ import annotations
 
@@ -95,7 +96,20 @@ def gaussians(out):
     return means, (-2.5 + out[:, 3:6]).contiguous(), quats, out[:, 6].contiguous(), sh
 
 
-def train(steps=60, seed=0, say=print):
+MATRICES = ("embed", "key", "value", "head")
+
+
+def update(ctx, w, grads, state, step, optimiser):
+    """One step of the optimiser on every weight; `state` holds two buffers a weight (a momentum is the first)."""
+    by_adam = [k for k in w if optimiser == "adam" or k not in MATRICES]
+    groups = [(w[k], grads[k].contiguous(), *state[k], 2e-3) for k in by_adam]
+    gsr.gsr_adam_step(ctx, groups, 0.9, 0.999, 1e-8, 1 - 0.9 ** step, 1 - 0.999 ** step)
+    for k in w:
+        if k not in by_adam:  # an update whose elements are about as large as Adam's, whatever the matrix's shape
+            gsr.gsr_muon_step(ctx, w[k], grads[k].contiguous(), state[k][0], 2e-3 * max(w[k].shape) ** 0.5)
+
+
+def train(steps=60, seed=0, say=print, optimiser="adam"):
     """Fits the decoder to one synthetic image; returns the losses."""
     ctx = gsr.Context(0)
     yx = grid(SIZE, 1.0)[0].reshape(SIZE, SIZE, 2)
@@ -119,8 +133,7 @@ def train(steps=60, seed=0, say=print):
         dmeans, dscales, _, dopacity, dsh = gsr.gsr_project_backward(ctx, cam, *params, dsplats)
         dout = torch.cat([0.1 * dmeans, dscales, dopacity[:, None], dsh[:, 0]], -1)
         grads = decoder_backward(ctx, w, saved, pos_q, pos_k, dout)
-        groups = [(w[k], grads[k].contiguous(), *state[k], 2e-3) for k in w]
-        gsr.gsr_adam_step(ctx, groups, 0.9, 0.999, 1e-8, 1 - 0.9 ** step, 1 - 0.999 ** step)
+        update(ctx, w, grads, state, step, optimiser)
         losses.append(float(loss[0]))
         if step == 1 or step % 20 == 0:
             say(f"step {step}: loss {losses[-1]:.4f}", flush=True)
@@ -131,4 +144,6 @@ def train(steps=60, seed=0, say=print):
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=60)
-    train(ap.parse_args().steps)
+    ap.add_argument("--optimiser", choices=("adam", "muon"), default="adam")
+    args = ap.parse_args()
+    train(args.steps, optimiser=args.optimiser)
