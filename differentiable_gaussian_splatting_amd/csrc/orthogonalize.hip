@@ -20,7 +20,6 @@ namespace gsr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kDeep = 32;  // depth of a stage of a product
 using half = _Float16;
 
 // The matrices of a call and where their planes lie in the scratch. rp and cp: r and c padded with zeros to whole tiles.
@@ -188,11 +187,16 @@ __device__ __forceinline__ void to_lds(const half* p, char* s) {
                                    (__attribute__((address_space(3))) void*)s, 16, 0, 0);
 }
 
-// An LDS tile of kTile rows of kDeep numbers in P planes, as they lie in memory.
-template <int kTile, int P>
+// The depth of a stage of a product. Small tiles have little to multiply between two barriers: 4,096 x 1,024 float32 340 us
+// with stages of 64, 373 of 32. (Larger tiles of one plane lose by them: 2,048 x 2,048 bfloat16 471 us of 32, 504 of 64.)
+template <int kTile>
+constexpr int kDeep = kTile == 64 ? 64 : 32;
+
+// An LDS tile of kTile rows of DEEP numbers in P planes, as they lie in memory.
+template <int kTile, int P, int DEEP>
 struct Stage {
-  using L = Tile<half, kDeep * P>;
-  static constexpr int kBytes = kTile * kDeep * 2 * P;
+  using L = Tile<half, DEEP * P>;
+  static constexpr int kBytes = kTile * DEEP * 2 * P;
   static constexpr int kPass = kThreads / L::kChunks;  // rows that the workgroup copies at a time
   static constexpr int kCopies = kTile / kPass;
 
@@ -202,12 +206,13 @@ struct Stage {
   int step;
   __device__ __forceinline__ void set(const Operand& o, uint64_t row) {
     const int r = int(threadIdx.x) / L::kChunks;
-    const int c = ((int(threadIdx.x) % L::kChunks) ^ L::swizzle(r)) * 8;
+    const int c = (int(threadIdx.x) % L::kChunks) ^ L::swizzle(r);
+    const int in_row = P == 2 ? c * 8 : c / 4 * o.step + c % 4 * 8;  // one plane of two: every other 32 columns
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
-      off[i] = uint32_t((min(row + r + i * kPass, o.rows - 1) - row) * o.ld + c) * 2;
+      off[i] = uint32_t((min(row + r + i * kPass, o.rows - 1) - row) * o.ld + in_row) * 2;
     at = reinterpret_cast<const char*>(o.base + row * o.ld);
-    step = o.step * 2;
+    step = o.step * 2 * (DEEP / 32);
   }
   // Starts the copy of the next stage, and moves on if there is another.
   __device__ __forceinline__ void start(char* s, int wave, bool on) {
@@ -218,13 +223,13 @@ struct Stage {
   }
   // Depths 16 kk + 8 h .. + 7 of row r0 + l % 32 of plane p.
   __device__ static __forceinline__ Vec<half, 8> frag(const char* s, int r0, int p, int kk) {
-    return L::frag(s, r0, 2 * p + kk);
+    return L::frag(s, r0, P == 2 ? kk / 2 * 4 + 2 * p + kk % 2 : kk);
   }
 };
 
 // How many stages of tiles LDS holds: copies run that many ahead, less what is being multiplied.
 template <int kTile, int PLANES>
-constexpr int kStages = kTile == 64 ? 3 : (kTile == 192 || (kTile == 128 && PLANES < 4) ? 3 : 2);
+constexpr int kStages = kTile == 64 || kTile == 192 || (kTile == 128 && PLANES < 4) ? 3 : 2;
 
 // The sums of a workgroup's tile: wave (w / 2, w % 2) of 2 x 2 has rows row .. and columns col .. , lane l row
 // row + 32 i + l % 32 and columns col + 32 j + 8 q + 4 (l / 32) + {0..3} in acc[i][j][4 q ..].
@@ -270,14 +275,15 @@ __device__ __forceinline__ void stage_barrier() {
 // past the LDS `lds` (Lds::kBytes of it) when this returns.
 template <int kTile, int LP, int RP>
 struct Lds {
-  static constexpr int kStage = (LP + RP) * kTile * kDeep * 2, kBytes = kStage * kStages<kTile, LP + RP>;
+  static constexpr int kStage = (LP + RP) * kTile * kDeep<kTile> * 2, kBytes = kStage * kStages<kTile, LP + RP>;
 };
 
 template <int kTile, int LP, int RP>
 __device__ __forceinline__ void product(const Operand& left, const Operand& right, uint64_t row, uint64_t col,
                                         uint64_t deep, char* lds, Sums<kTile>& s) {
-  using SL = Stage<kTile, LP>;
-  using SR = Stage<kTile, RP>;
+  constexpr int DEEP = kDeep<kTile>, kHalf = DEEP / 32;  // steps of 16 in half a stage
+  using SL = Stage<kTile, LP, DEEP>;
+  using SR = Stage<kTile, RP, DEEP>;
   constexpr int kStage = Lds<kTile, LP, RP>::kStage, kCount = kStages<kTile, LP + RP>, kBlocks = kTile / 64;
   constexpr int kCopies = SL::kCopies + SR::kCopies;  // of a stage, by each wave
   const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
@@ -302,36 +308,40 @@ __device__ __forceinline__ void product(const Operand& left, const Operand& righ
   // wait for neither LDS nor the barrier, which lies between the halves: behind it this stage's tiles are read to the end
   // by every wave, the next stage's have landed, and the copies of the stage kCount on may start. Those past the end
   // repeat the last stage.
-  Vec<half, 8> a[2][LP][kBlocks], b[2][RP][kBlocks];
-  auto read = [&](const char* sl, int kk) {
+  Vec<half, 8> a[2][kHalf][LP][kBlocks], b[2][kHalf][RP][kBlocks];
+  auto read = [&](const char* sl, int part) {
     const char* sr = sl + SL::kBytes;
 #pragma unroll
-    for (int i = 0; i < kBlocks; ++i) {
+    for (int k = 0; k < kHalf; ++k)
 #pragma unroll
-      for (int p = 0; p < LP; ++p) a[kk][p][i] = SL::frag(sl, wr + 32 * i, p, kk);
+      for (int i = 0; i < kBlocks; ++i) {
 #pragma unroll
-      for (int p = 0; p < RP; ++p) b[kk][p][i] = SR::frag(sr, wc + 32 * i, p, kk);
-    }
+        for (int p = 0; p < LP; ++p) a[part][k][p][i] = SL::frag(sl, wr + 32 * i, p, part * kHalf + k);
+#pragma unroll
+        for (int p = 0; p < RP; ++p) b[part][k][p][i] = SR::frag(sr, wc + 32 * i, p, part * kHalf + k);
+      }
   };
-  auto multiply = [&](int kk) {
+  auto multiply = [&](int part) {
 #pragma unroll
-    for (int p = 0; p < LP; ++p)
+    for (int k = 0; k < kHalf; ++k)
 #pragma unroll
-      for (int q = 0; q < RP; ++q)
-        if (p + q < (LP > RP ? LP : RP))  // not lo lo
+      for (int p = 0; p < LP; ++p)
 #pragma unroll
-          for (int i = 0; i < kBlocks; ++i)
+        for (int q = 0; q < RP; ++q)
+          if (p + q < (LP > RP ? LP : RP))  // not lo lo
 #pragma unroll
-            for (int j = 0; j < kBlocks; ++j) s.acc[i][j] = mma(b[kk][q][j], a[kk][p][i], s.acc[i][j]);
+            for (int i = 0; i < kBlocks; ++i)
+#pragma unroll
+              for (int j = 0; j < kBlocks; ++j) s.acc[i][j] = mma(b[part][k][q][j], a[part][k][p][i], s.acc[i][j]);
   };
-  constexpr int kReads = (LP + RP) * kBlocks, kProducts = (LP + RP - 1) * kBlocks * kBlocks;
-  int more = int(deep / kDeep) - 1;  // stages past the one whose copy starts next; then the last repeats
+  constexpr int kReads = (LP + RP) * kBlocks * kHalf, kProducts = (LP + RP - 1) * kBlocks * kBlocks * kHalf;
+  int more = int(deep / DEEP) - 1;  // stages past the one whose copy starts next; then the last repeats
 #pragma unroll
   for (int i = 0; i < kCount; ++i) start(i, more-- > 0);
   stage_barrier<(kCount - 1) * kCopies>();
   read(lds, 0);
   int now = 0;
-  for (int stages = int(deep / kDeep); stages > 0; --stages) {
+  for (int stages = int(deep / DEEP); stages > 0; --stages) {
     read(lds + now * kStage, 1);
     multiply(0);
     spread<0, kProducts, kReads, 0>(std::make_integer_sequence<int, kProducts>());
