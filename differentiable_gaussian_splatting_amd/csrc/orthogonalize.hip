@@ -67,19 +67,6 @@ __device__ __forceinline__ void take_new(const Source<T, MUON>& s, uint32_t b, u
   }
 }
 
-// One element, read once: the momentum is updated here.
-template <typename T, bool MUON>
-__device__ __forceinline__ float take_one(const Source<T, MUON>& s, uint32_t b, uint32_t row, uint32_t col) {
-  const float u = float(s.grad[int64_t(b) * s.gb + int64_t(row) * s.gr + col]);
-  if constexpr (MUON) {
-    float* p = s.momentum + int64_t(b) * s.mb + int64_t(row) * s.mr + col;
-    const float m = fmaf(s.mu, *p, u);
-    *p = m;
-    return s.nesterov ? fmaf(s.mu, m, u) : m;
-  }
-  return u;
-}
-
 // The same elements again, the momentum as take_new left it.
 template <typename T, bool MUON>
 __device__ __forceinline__ float take_again(const Source<T, MUON>& s, uint32_t b, uint32_t row, uint32_t col) {
@@ -949,12 +936,34 @@ __global__ __launch_bounds__(4 * R) void k_orth_one(OrthShape g, SmallPlan plan,
   {
     float u[C::kEach];
     double sum = 0.0;
-#pragma unroll
-    for (int e = 0; e < C::kEach; ++e) {
+    auto source = [&](int e, uint32_t* row, uint32_t* col) {
       int i, j;
       strip_place<C>(g.tall, e, &i, &j);
-      const uint32_t sr = g.tall ? j : i, sc = g.tall ? i : j;
-      u[e] = sr < g.rows && sc < g.cols ? take_one(src, b, sr, sc) : 0.0f;
+      *row = g.tall ? j : i;
+      *col = g.tall ? i : j;
+      return *row < g.rows && *col < g.cols;
+    };
+#pragma unroll
+    for (int e = 0; e < C::kEach; ++e) {
+      uint32_t sr, sc;
+      u[e] = source(e, &sr, &sc) ? float(src.grad[int64_t(b) * src.gb + int64_t(sr) * src.gr + sc]) : 0.0f;
+    }
+    if constexpr (MUON) {
+      // every load before the first store, which the compiler must take for one of what is loaded next
+      float m[C::kEach];
+      float* const from = src.momentum + int64_t(b) * src.mb;
+#pragma unroll
+      for (int e = 0; e < C::kEach; ++e) {
+        uint32_t sr, sc;
+        m[e] = source(e, &sr, &sc) ? from[int64_t(sr) * src.mr + sc] : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < C::kEach; ++e) {
+        uint32_t sr, sc;
+        m[e] = fmaf(src.mu, m[e], u[e]);
+        if (source(e, &sr, &sc)) from[int64_t(sr) * src.mr + sc] = m[e];
+        u[e] = src.nesterov ? fmaf(src.mu, m[e], u[e]) : m[e];
+      }
     }
 #pragma unroll
     for (int e = 0; e < C::kEach; ++e) sum = fma(double(u[e]), double(u[e]), sum);
