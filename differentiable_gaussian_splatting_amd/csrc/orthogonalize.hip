@@ -50,24 +50,7 @@ struct Source {
   bool nesterov;
 };
 
-// Elements col .. of a row, read once: the momentum is updated here.
-template <typename T, bool MUON>
-__device__ __forceinline__ void take_new(const Source<T, MUON>& s, uint32_t b, uint32_t row, uint32_t col, int n,
-                                         float* u) {
-  load_f32<kNormVec>(s.grad + int64_t(b) * s.gb + int64_t(row) * s.gr + col, n, u);
-  if constexpr (MUON) {
-    float m[kNormVec];
-    float* p = s.momentum + int64_t(b) * s.mb + int64_t(row) * s.mr + col;
-    load_f32<kNormVec>(p, n, m);
-#pragma unroll
-    for (int i = 0; i < kNormVec; ++i) m[i] = fmaf(s.mu, m[i], u[i]);
-    store_f32<kNormVec>(p, n, m);
-#pragma unroll
-    for (int i = 0; i < kNormVec; ++i) u[i] = s.nesterov ? fmaf(s.mu, m[i], u[i]) : m[i];
-  }
-}
-
-// The same elements again, the momentum as take_new left it.
+// An element, the momentum as k_orth_norm left it.
 template <typename T, bool MUON>
 __device__ __forceinline__ float take_again(const Source<T, MUON>& s, uint32_t b, uint32_t row, uint32_t col) {
   const float g = float(s.grad[int64_t(b) * s.gb + int64_t(row) * s.gr + col]);
@@ -78,19 +61,44 @@ __device__ __forceinline__ float take_again(const Source<T, MUON>& s, uint32_t b
   return g;
 }
 
-// Partial sums of squares in float64 (no gradient is too small or too large for it), and the new momentum.
+// Partial sums of squares in float64 (no gradient is too small or too large for it), and the new momentum. Bound by memory:
+// a thread loads four vectors before it stores the first, which the compiler must take for one of what is loaded next.
 template <typename T, bool MUON>
 __global__ __launch_bounds__(kThreads) void k_orth_norm(OrthShape g, Source<T, MUON> src, double* __restrict__ part) {
+  constexpr int kAtOnce = 4;
   __shared__ double s[kThreads / 64];
-  const uint32_t b = blockIdx.y, vecs = g.by_vec.d * g.rows;
+  const uint32_t b = blockIdx.y, vecs = g.by_vec.d * g.rows, step = g.parts * kThreads;
   double sum = 0.0;
-  for (uint32_t v = blockIdx.x * kThreads + threadIdx.x; v < vecs; v += g.parts * kThreads) {
-    const uint32_t row = g.by_vec.div(v), col = (v - row * g.by_vec.d) * kNormVec;
-    float u[kNormVec];
-    take_new(src, b, row, col, int(g.cols - col), u);
+  for (uint32_t v0 = blockIdx.x * kThreads + threadIdx.x; v0 < vecs; v0 += kAtOnce * step) {
+    float u[kAtOnce][kNormVec], m[kAtOnce][kNormVec];
+    auto place = [&](int k, uint32_t* row, uint32_t* col) {
+      const uint32_t v = v0 + k * step;
+      *row = g.by_vec.div(v);
+      *col = (v - *row * g.by_vec.d) * kNormVec;
+      return v < vecs ? int(g.cols - *col) : 0;
+    };
 #pragma unroll
-    for (int i = 0; i < kNormVec; ++i)
-      if (col + i < g.cols) sum = fma(double(u[i]), double(u[i]), sum);
+    for (int k = 0; k < kAtOnce; ++k) {
+      uint32_t row, col;
+      const int n = place(k, &row, &col);
+      load_f32<kNormVec>(src.grad + int64_t(b) * src.gb + int64_t(row) * src.gr + col, n, u[k]);
+      if constexpr (MUON) load_f32<kNormVec>(src.momentum + int64_t(b) * src.mb + int64_t(row) * src.mr + col, n, m[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      uint32_t row, col;
+      const int n = place(k, &row, &col);
+      if constexpr (MUON) {
+#pragma unroll
+        for (int i = 0; i < kNormVec; ++i) m[k][i] = fmaf(src.mu, m[k][i], u[k][i]);
+        store_f32<kNormVec>(src.momentum + int64_t(b) * src.mb + int64_t(row) * src.mr + col, n, m[k]);
+#pragma unroll
+        for (int i = 0; i < kNormVec; ++i) u[k][i] = src.nesterov ? fmaf(src.mu, m[k][i], u[k][i]) : m[k][i];
+      }
+#pragma unroll
+      for (int i = 0; i < kNormVec; ++i)
+        if (i < n) sum = fma(double(u[k][i]), double(u[k][i]), sum);
+    }
   }
   for (int k = 32; k > 0; k >>= 1) sum += __shfl_xor(sum, k);
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = sum;
@@ -131,15 +139,37 @@ __global__ __launch_bounds__(kThreads) void k_orth_start(OrthShape g, Source<T, 
   const double scale = scale_s;
   // tile[i][j] is X[r0 + i][c0 + j]; the source's rows are walked along its own columns
   const uint32_t row0 = g.tall ? c0 : r0, col0 = g.tall ? r0 : c0;
-#pragma unroll 4
-  for (int e = threadIdx.x; e < 64 * 64; e += kThreads) {
-    const uint32_t i = e / 64, j = e % 64, row = row0 + i, col = col0 + j;
-    float v = 0.0f;
-    if (row < g.rows && col < g.cols) v = float(double(take_again(src, b, row, col)) * scale);
-    if (g.tall)
-      tile[j][i] = v;
-    else
-      tile[i][j] = v;
+  constexpr int kVecs = 64 * 64 / kNormVec / kThreads;
+  float u[kVecs][kNormVec], m[kVecs][kNormVec];
+  auto vector = [&](int k, uint32_t* i, uint32_t* j) {
+    const uint32_t e = k * kThreads + threadIdx.x;
+    *i = e / (64 / kNormVec);
+    *j = e % (64 / kNormVec) * kNormVec;
+  };
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    uint32_t i, j;
+    vector(k, &i, &j);
+    const uint32_t row = row0 + i, col = col0 + j;
+    const int n = row < g.rows ? int(g.cols) - int(col) : 0;
+    load_f32<kNormVec>(src.grad + int64_t(b) * src.gb + int64_t(row) * src.gr + col, n, u[k]);
+    if constexpr (MUON) load_f32<kNormVec>(src.momentum + int64_t(b) * src.mb + int64_t(row) * src.mr + col, n, m[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    uint32_t i, j;
+    vector(k, &i, &j);
+#pragma unroll
+    for (int q = 0; q < kNormVec; ++q) {
+      float v = u[k][q];
+      if constexpr (MUON) v = src.nesterov ? fmaf(src.mu, m[k][q], v) : m[k][q];
+      const bool live = row0 + i < g.rows && col0 + j + q < g.cols;
+      v = live ? float(double(v) * scale) : 0.0f;
+      if (g.tall)
+        tile[j + q][i] = v;
+      else
+        tile[i][j + q] = v;
+    }
   }
   __syncthreads();
   const uint64_t plane = g.rp * g.cp;
