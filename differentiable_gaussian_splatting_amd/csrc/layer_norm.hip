@@ -94,7 +94,9 @@ struct Token {
   }
 };
 
-// Bound by memory: 40,000 x 1,024 bfloat16 (164 MB) 38 us, 4.3 TB/s.
+// A token in registers, so that it is read once; the next one's loads are on their way while this one is summed.
+// Bound by memory: 40,000 x 1,024 bfloat16 (164 MB) 33.5 us, 4.9 TB/s; 10,000 x 640 float32 (51 MB) 13.6 us. One token is
+// one launch, 5.4 us.
 template <typename T, int TEAM, int K>
 __global__ __launch_bounds__(threads_of(TEAM)) void k_ln(LnShape g, const T* x, LnRows xr,
                                                          const float* __restrict__ gamma,
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(threads_of(TEAM)) void k_ln(LnShape g, const T* x, 
 
 // dx, and the team's sums of dy xh and dy over its tokens; the workgroup's teams are added through LDS, and `part` gets
 // [workgroup][2][channels], or with one workgroup dgamma and dbeta get them.
-// Bound by memory: 40,000 x 1,024 bfloat16 (246 MB) 52 us, 4.7 TB/s.
+// Bound by memory: 40,000 x 1,024 bfloat16 (246 MB) 45.5 us, 5.4 TB/s; 10,000 x 640 float32 (77 MB) 18 us.
 template <typename T, int TEAM, int K, int THREADS>
 __global__ __launch_bounds__(THREADS) void k_ln_back(LnShape g, const T* __restrict__ x, LnRows xr,
                                                      const float* __restrict__ gamma,
@@ -255,7 +257,7 @@ __global__ __launch_bounds__(THREADS) void k_ln_back(LnShape g, const T* __restr
 }
 
 // dgamma and dbeta: the parts added, a workgroup to 64 columns of [dgamma | dbeta], its 16 rows of threads each taking
-// every 16th part.
+// every 16th part. Bound by latency: 500 parts of 2 x 1,024 sums 5.1 us.
 __global__ __launch_bounds__(1024) void k_ln_join(uint32_t channels, uint32_t parts, const float* __restrict__ part,
                                                   float* __restrict__ dgamma, float* __restrict__ dbeta) {
   __shared__ float s[16][64];
@@ -279,10 +281,26 @@ __global__ __launch_bounds__(1024) void k_ln_join(uint32_t channels, uint32_t pa
 
 constexpr int kWide = 1024;  // threads of a workgroup that reads a token again for each step
 
+// Tokens of more than 2,048 vectors of 16 bytes, the most that a workgroup's registers hold beside gamma: three reads of
+// a token (two of the backward's) instead of one, the later ones from cache, and the column sums in a launch of their
+// own. 2,000 x 20,000 bfloat16 48 us forward, 109 backward; of 16,384 channels, in registers, 38 and 123.
+
 // f(channel, number of adjacent channels from it that exist (at most V)) over a token's channels.
 template <int V, typename F>
 __device__ __forceinline__ void for_channels(uint32_t channels, F f) {
+#pragma unroll 2
   for (uint32_t c = threadIdx.x * V; c < channels; c += kWide * V) f(c, int(channels - c));
+}
+
+// n of V adjacent gamma or beta, or what stands for none.
+template <int V>
+__device__ __forceinline__ void load_param(const float* p, uint32_t c, int n, float none, float* f) {
+  if (p) {
+    load_f32<V>(p + c, n, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = none;
+  }
 }
 
 template <typename T>
@@ -312,11 +330,12 @@ __global__ __launch_bounds__(kWide) void k_ln_wide(LnShape g, const T* x, LnRows
     const float rstd = 1.0f / sqrtf(team_sum<kWide>(sq, s[1]) / width + g.eps);
     T* yp = y + yr.at(g, row);
     for_channels<V>(g.channels, [&](uint32_t c, int n) {
-      float f[V];
+      float f[V], gm[V], bt[V];
       load_f32<V>(xp + c, n, f);
+      load_param<V>(gamma, c, n, 1.0f, gm);
+      load_param<V>(beta, c, n, 0.0f, bt);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i < n) f[i] = fmaf((f[i] - mean) * rstd, gamma ? gamma[c + i] : 1.0f, beta ? beta[c + i] : 0.0f);
+      for (int i = 0; i < V; ++i) f[i] = fmaf((f[i] - mean) * rstd, gm[i], bt[i]);
       store_f32<V>(yp + c, n, f);
     });
     if (threadIdx.x == 0) stats[row] = LnStats{mean, rstd};
@@ -337,14 +356,15 @@ __global__ __launch_bounds__(kWide) void k_ln_wide_back(LnShape g, const T* __re
     float a = 0.0f, b = 0.0f;
     // xh and dh of the token's channels from c on
     auto take = [&](uint32_t c, int n, float* f, float* d) {
+      float gm[V];
       load_f32<V>(xp + c, n, f);
       load_f32<V>(dp + c, n, d);
+      load_param<V>(gamma, c, n, 1.0f, gm);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i < n) {
-          f[i] = (f[i] - st.mean) * st.rstd;
-          d[i] *= gamma ? gamma[c + i] : 1.0f;
-        }
+      for (int i = 0; i < V; ++i) {
+        f[i] = (f[i] - st.mean) * st.rstd;
+        d[i] *= gm[i];
+      }
     };
     for_channels<V>(g.channels, [&](uint32_t c, int n) {
       float f[V], d[V];
@@ -437,11 +457,11 @@ LnShape shape_of(const gsr_layer_norm* d) {
   return g;
 }
 
-// Workgroups of `teams` teams whose lanes hold `load` vectors (of 256 threads): each reads gamma (and writes its sums) once,
-// so that few long-lived ones cost least, as many as keep memory busy. Forward and backward with 256, 512, 1,024 and 2,048
-// of them: 40,000 x 1,024 bfloat16 (two vectors) 45, 38, 42 and 46 us; 57, 56, 61 and (with 1,024 threads each) 66. 40,000 x
-// 1,024 float32 (four) 60, 64, 65 and 63; 94, 99, 102 and 158. 40,000 x 512 float16 (one) 32, 26, 25 and 26; 43, 34, 34
-// and 34. Each gets as many tokens as the others.
+// Workgroups of `teams` teams whose lanes hold `load` vectors (of 256 threads): each reads gamma (and writes its sums)
+// once, so that few long-lived ones cost least, as many as keep memory busy. Forward and backward with 256, 512, 1,024
+// and 2,048 of them: 40,000 x 1,024 bfloat16 (two vectors) 45, 38, 42 and 46 us; 57, 56, 61 and (with 1,024 threads each)
+// 66. 40,000 x 1,024 float32 (four) 60, 64, 65 and 63; 94, 99, 102 and 158. 40,000 x 512 float16 (one) 32, 26, 25 and 26;
+// 43, 34, 34 and 34. Each gets as many tokens as the others.
 uint32_t workgroups(uint32_t rows, uint32_t teams, uint32_t load) {
   const uint64_t most = uint64_t(load >= 4 ? 256 : (load >= 2 ? 512 : 1024)) * teams, per = (rows + most - 1) / most;
   return uint32_t((rows + teams * per - 1) / (teams * per));
@@ -580,8 +600,8 @@ extern "C" gsr_status gsr_layer_norm_backward(gsr_ctx* ctx, void* stream, const 
         parts = std::min<uint32_t>(g.rows, 64);
         wide = true;
       });
-  if (sums && (parts > 1 || wide) && (st = grow(ctx, ctx->arena.feat_part, size_t(parts) * 2 * g.channels * sizeof(float))))
-    return st;
+  const size_t room = size_t(parts) * 2 * g.channels * sizeof(float);
+  if (sums && (parts > 1 || wide) && (st = grow(ctx, ctx->arena.feat_part, room))) return st;
   float* part = static_cast<float*>(ctx->arena.feat_part.ptr);
   bool joined = false;
   timing_mark(ctx, GSR_STAGE_LAYER_NORM_BACKWARD, s, false);
