@@ -13,7 +13,8 @@
 // too, and every product is hi hi + hi lo + lo hi on the 16-bit matrix cores with float32 sums (three products of
 // 2.5 PFLOP/s against one of 157 TFLOP/s in float32; the missing lo lo is 2^-24 of a term): the error of a float32
 // evaluation, 1e-6 of the result's norm for flat spectra and 1e-5 for steep ones. bfloat16 results, which round by
-// 1.7e-3 of their norm, keep A and P in one float16 number and take A from X's hi alone: 1.0e-3 to 1.6e-3.
+// 1.7e-3 of their norm, keep A and P in one float16 number and take A from X's hi alone where the products take the time
+// (more than 256 rows and columns): 1.0e-3 to 1.6e-3 of the norm, 12 x 1,024 x 1,024 in five steps 628 us.
 #include "attention_common.hpp"
 
 namespace gsr {
@@ -22,7 +23,7 @@ namespace {
 constexpr int kThreads = 256;
 using half = _Float16;
 
-// The matrices of a call and where their planes lie in the scratch. rp and cp: r and c padded with zeros to whole tiles.
+// The matrices of a call. rp and cp: r and c padded with zeros to whole tiles of 64 (cp, of few rows, to strips of 128).
 struct OrthShape {
   uint32_t batch, rows, cols, r, c;
   uint64_t rp, cp;
@@ -63,6 +64,8 @@ __device__ __forceinline__ float take_again(const Source<T, MUON>& s, uint32_t b
 
 // Partial sums of squares in float64 (no gradient is too small or too large for it), and the new momentum. Bound by memory:
 // a thread loads four vectors before it stores the first, which the compiler must take for one of what is loaded next.
+// 8 x 1,024 x 4,096 bfloat16 with momentum (336 MB) 65 us, 5.1 TB/s; 4,096 x 4,096 float32 (201 MB) 36 us, with one vector
+// at a time 96.
 template <typename T, bool MUON>
 __global__ __launch_bounds__(kThreads) void k_orth_norm(OrthShape g, Source<T, MUON> src, double* __restrict__ part) {
   constexpr int kAtOnce = 4;
@@ -115,13 +118,15 @@ __device__ __forceinline__ double first_scale(const OrthShape& g, double sum) {
 
 // Matrices in scratch: a row of n numbers is n float16 values (one plane), or 2 n, the hi and lo parts of 32 columns in
 // turn: what a stage of a product reads of a row is then one whole 128-byte line, not halves of two (every half is a
-// request to the second level of cache, whose rate bounds the large products). Where column col of plane p lies in a row:
+// request to the second level of cache, whose rate bounds the large products). Where column col of plane p lies in a
+// row:
 template <int PLANES>
 __device__ __forceinline__ uint64_t place(uint64_t col, int p) {
   return PLANES == 2 ? col / 32 * 64 + p * 32 + col % 32 : col;
 }
 
-// X_0 and its transpose in two planes each, zeros in the padding. A workgroup takes a 64 x 64 tile.
+// X_0 and its transpose in two planes each, zeros in the padding. A workgroup takes a 64 x 64 tile, so that both are
+// written in 128-byte pieces. Bound by memory: 8 x 1,024 x 4,096 bfloat16 with momentum (470 MB) 93 us, 5.0 TB/s.
 template <typename T, bool MUON>
 __global__ __launch_bounds__(kThreads) void k_orth_start(OrthShape g, Source<T, MUON> src,
                                                          const double* __restrict__ part, half* __restrict__ x,
@@ -204,8 +209,9 @@ __device__ __forceinline__ void to_lds(const half* p, char* s) {
                                    (__attribute__((address_space(3))) void*)s, 16, 0, 0);
 }
 
-// The depth of a stage of a product. Small tiles have little to multiply between two barriers: 4,096 x 1,024 float32 340 us
-// with stages of 64, 373 of 32. (Larger tiles of one plane lose by them: 2,048 x 2,048 bfloat16 471 us of 32, 504 of 64.)
+// The depth of a stage of a product. Small tiles have little to multiply between two barriers: 4,096 x 1,024 float32
+// 343 us with stages of 64, 373 of 32. (Larger tiles of one plane lose by them: 2,048 x 2,048 bfloat16 471 us of 32, 504
+// of 64.)
 template <int kTile>
 constexpr int kDeep = kTile == 64 ? 64 : 32;
 
@@ -257,8 +263,8 @@ struct Sums {
   uint64_t row, col;
 };
 
-// Asks the compiler to issue PRODUCTS matrix products with READS LDS reads spread over the first half of them (the whole,
-// if there are no copies) and COPIES copies over the rest.
+// Asks the compiler to issue PRODUCTS matrix products with READS LDS reads spread over the first half of them (three
+// quarters, if there are no copies) and COPIES copies over the rest.
 template <int SYNC, int PRODUCTS, int READS, int COPIES, int E>
 __device__ __forceinline__ void spread_one() {
   constexpr int kFirst = COPIES ? (PRODUCTS + 1) / 2 : (PRODUCTS * 3 + 3) / 4, kRest = PRODUCTS - kFirst;
@@ -286,15 +292,15 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// One kTile x kTile tile of a product of depth `deep`: rows row .. of the left operand (LP planes) by rows col .. of the
-// right one (RP planes), depths adjacent in both. The blocks are computed transposed, so that a lane holds one row of the
-// result and adjacent columns. What lies past the operands' rows is computed and of no use. The workgroup's waves are
-// past the LDS `lds` (Lds::kBytes of it) when this returns.
 template <int kTile, int LP, int RP>
 struct Lds {
   static constexpr int kStage = (LP + RP) * kTile * kDeep<kTile> * 2, kBytes = kStage * kStages<kTile, LP + RP>;
 };
 
+// One kTile x kTile tile of a product of depth `deep`: rows row .. of the left operand (LP planes) by rows col .. of the
+// right one (RP planes), depths adjacent in both. The blocks are computed transposed, so that a lane holds one row of the
+// result and adjacent columns. What lies past the operands' rows is computed and of no use. The workgroup's waves are
+// past the LDS `lds` (Lds::kBytes of it) when this returns.
 template <int kTile, int LP, int RP>
 __device__ __forceinline__ void product(const Operand& left, const Operand& right, uint64_t row, uint64_t col,
                                         uint64_t deep, char* lds, Sums<kTile>& s) {
@@ -321,10 +327,10 @@ __device__ __forceinline__ void product(const Operand& left, const Operand& righ
     copy_l.start(lds + stage * kStage, wave, on);
     copy_r.start(lds + stage * kStage + SL::kBytes, wave, on);
   };
-  // Fragments of the two halves of a stage. While one half is multiplied the next half's are read, so that the matrix cores
-  // wait for neither LDS nor the barrier, which lies between the halves: behind it this stage's tiles are read to the end
-  // by every wave, the next stage's have landed, and the copies of the stage kCount on may start. Those past the end
-  // repeat the last stage.
+  // Fragments of the two halves of a stage. While one half is multiplied the next half's are read, so that the matrix
+  // cores wait for neither LDS nor the barrier, which lies between the halves: behind it this stage's tiles are read to
+  // the end by every wave, the next stage's have landed, and the copies of the stage kCount on may start. Those past the
+  // end repeat the last stage.
   Vec<half, 8> a[2][kHalf][LP][kBlocks], b[2][kHalf][RP][kBlocks];
   auto read = [&](const char* sl, int part) {
     const char* sr = sl + SL::kBytes;
@@ -379,8 +385,8 @@ __device__ __forceinline__ void product(const Operand& left, const Operand& righ
 // Orders a wave's LDS writes before its reads of what other lanes wrote.
 __device__ __forceinline__ void wave_sync() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// 32 rows of kTile / 2 float16 values in a wave's part of LDS, by which a wave turns its sums into whole lines: rows lie 16
-// bytes more than their length apart, so that lanes of adjacent rows meet different banks.
+// 32 rows of kTile / 2 float16 values in a wave's part of LDS, by which a wave turns its sums into whole lines: rows lie
+// 16 bytes more than their length apart, so that lanes of adjacent rows meet different banks.
 template <int kTile>
 struct Turn {
   static constexpr int kCols = kTile / 2, kStride = kCols * 2 + 16, kBytes = 32 * kStride;
@@ -509,9 +515,15 @@ __device__ __forceinline__ void add_rows(char* mine, f32x16* acc, float alpha) {
     }
 }
 
-// out = beta (left right^T) + alpha in + alpha2 in2 [rp, rp], symmetric (left and right are one matrix, or commute), PLANES
-// planes each of left, right, in, in2 and out; ADD of in and in2 are read. Strides from matrix to matrix: of left and right
-// `matrix`, of the others PLANES planes.
+// out = beta (left right^T) + alpha in + alpha2 in2 [rp, rp], symmetric (left and right are one matrix, or commute),
+// PLANES planes each of left, right, in, in2 and out; ADD of in and in2 are read. Strides from matrix to matrix: of left
+// and right `matrix`, of the others PLANES planes. Only tiles on and below the diagonal are computed; the others are
+// those, transposed by LDS on their way out.
+// Bound by the matrix cores where the tiles fill the card: 4,096 x 4,096 times its transpose in two planes 195 us for 253
+// tiles of 192, 1.18 PFLOP/s of float16 products (a large library product reaches 1.19 to 1.24), which at the 1.85 GHz
+// the card then runs at is 59 % of the cores' cycles. 8 x 1,024 x 4,096: 147 us, 0.79 PFLOP/s (288 tiles of 128 on 256
+// compute units). With fewer tiles than compute units by the latency of a stage: 1,024 x 1,024 in two planes 12.6 us for
+// 136 tiles of 64.
 template <int kTile, int PLANES, int ADD>
 __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_symmetric(
     Works w, uint32_t tiles, Operand left, Operand right, uint64_t matrix, uint64_t deep, const half* __restrict__ in,
@@ -570,7 +582,8 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_symmetri
   }
 }
 
-// What the last product is for: the next step (X' is written in two planes), a result in type T, or a parameter's update.
+// What the last product is for: the next step (X' is written in two planes), a result in type T, or a parameter's
+// update.
 template <typename T>
 struct Result {
   T* p;
@@ -580,16 +593,21 @@ struct Result {
 
 enum { kNext = 0, kWrite = 1, kUpdate = 2 };
 
-// X' = alpha X + beta (P X), PP planes of P, from X (written in place: only its own tile is read) and its transpose xt; the
-// transpose goes to next.
+// X' = alpha X + beta (P X), PP planes of P, from X (written in place: only its own tile is read) and its transpose xt;
+// the transpose goes to next. alpha X is added in float32 behind the product (as a diagonal of P it would be rounded with
+// every term's sum).
+// Bound by the matrix cores: 4,096 x 4,096 353 us, 1.17 PFLOP/s; 8 x 1,024 x 4,096 235 us, 0.88 (two rounds of tiles of
+// 256, whose first copies and results no product hides); 12 x 1,024 x 1,024 with P in one plane 72 us, 0.72 (768 tiles
+// of 128).
 template <int kTile, int PP, int WHAT, typename T>
 __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_apply(
-    Works w, OrthShape g, uint32_t tiles_r, uint32_t tiles_c, Operand p, half* x,
-    const half* __restrict__ xt, half* __restrict__ next, float alpha, float beta, Result<T> res) {
+    Works w, OrthShape g, uint32_t tiles_r, uint32_t tiles_c, Operand p, half* x, const half* __restrict__ xt,
+    half* __restrict__ next, float alpha, float beta, Result<T> res) {
   using Mem = Lds<kTile, PP, 2>;
   using L = Turn<kTile>;
   constexpr int kStride = kTile / 2 * 4 + 16;  // of rows of float32, as L's
-  static_assert(4 * 2 * L::kBytes <= Mem::kBytes && 2 * L::kBytes >= 32 * kStride, "the results pass through the stages' LDS");
+  static_assert(4 * 2 * L::kBytes <= Mem::kBytes && 2 * L::kBytes >= 32 * kStride,
+                "the results pass through the stages' LDS");
   __shared__ alignas(16) char lds[Mem::kBytes];
   uint64_t id;
   if (!w.mine(&id)) return;
@@ -705,13 +723,17 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_apply(
   }
 }
 
-// ---- matrices of at most 128 rows (or columns) --------------------------------------------------------------------------
+// ---- matrices of at most 128 rows (or columns) -----------------------------------------------------------------------
 //
-// Where r is at most 128, A and P fit into one compute unit's LDS beside a strip of X's columns, and all three products of
-// a step can be done there: a workgroup keeps P, applies it to its strips and adds what they give to the next step's A.
-// With one workgroup to a matrix (c within one strip) a launch does all steps and the norm too; with several, each step is
-// a launch that adds the workgroups' parts of A first (in their order), finds P from them again in every workgroup and
-// leaves its own part for the next. All numbers are in two float16.
+// Where r is at most 128, A and P fit into one compute unit's LDS beside a strip of X's columns, and all three products
+// of a step can be done there: a workgroup keeps P, applies it to its strips and adds what they give to the next step's
+// A. With one workgroup to a matrix (c within one strip) a launch does all steps and the norm too; with several, each
+// step is a launch that adds the workgroups' parts of A first (in their order), finds P from them again in every
+// workgroup and leaves its own part for the next. All numbers are in two float16.
+//
+// Bound by latency: a step's three products wait for each other, with a turn through LDS and a barrier between them. Five
+// steps of 2 x 64 x 64 float32 take 17.5 us, the step of 192 x 64 parameters 43 (by the large products' kernels 69 and
+// 87), of 100 x 1,000 in strips 109 us with their twelve launches.
 
 // An LDS tile of R rows of S values, in panels of at most 128 columns.
 template <int R, int S>
@@ -736,9 +758,8 @@ struct Small {
   using LX = Panels<R, S>;
   using LA = Tile<half, R>;
   static constexpr int kX = R * S * 2, kA = R * LA::kRowBytes;  // bytes of a plane
-  static constexpr int kLds = 2 * kX + 2 * kA;
-  static constexpr int kXBlocks = S / 64, kABlocks = R / 64;            // 32-column blocks of a wave
-  static constexpr int kEach = R * S / kT;                              // a strip's elements by each thread
+  static constexpr int kXBlocks = S / 64, kABlocks = R / 64;  // 32-column blocks of a wave
+  static constexpr int kEach = R * S / kT;                    // a strip's elements by each thread
 };
 
 // Depths 16 kk + 8 h .. + 7 of column at + l % 32 of a tile whose rows are the depths.
@@ -756,9 +777,9 @@ __device__ __forceinline__ Vec<half, 8> frag_of_columns(const char* s, int at, i
   return Vec<half, 8>{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// acc[j] += rows row .. of `left` by rows (or, with COLUMNS, columns) col + 32 j .. of `right`, both in two planes, transposed
-// as the large products' blocks are. With few blocks hi hi has a chain of sums of its own: the next product on the same
-// sums waits for the last.
+// acc[j] += rows row .. of `left` by rows (or, with COLUMNS, columns) col + 32 j .. of `right`, both in two planes,
+// transposed as the large products' blocks are. With few blocks hi hi has a chain of sums of its own: the next product on
+// the same sums waits for the last.
 template <typename LL, int LP, typename LR, int RP, bool COLUMNS, int BLOCKS, int DEEP>
 __device__ __forceinline__ void small_product(const char* left, int row, const char* right, int col, f32x16* acc) {
   constexpr int kRest = BLOCKS <= 2 ? BLOCKS : 0;
@@ -824,7 +845,8 @@ __device__ __forceinline__ Vec<float, 4> four_of(const f32x16& a, int q) {
   return Vec<float, 4>{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
 }
 
-// The factors of one step (see launch_steps): A = sums times a_scale; P = p_in A + p_sum A A^T; X' = x_in X + x_sum P X.
+// The factors of one step (see launch_steps): A = sums times a_scale; P = p_in A + p_sum A A^T;
+// X' = x_in X + x_sum P X.
 struct SmallStep {
   float a_scale, p_in, p_sum, x_in, x_sum;
 };
@@ -915,7 +937,8 @@ __device__ __forceinline__ void small_result(const OrthShape& g, const Result<T>
     for (int q = 0; q < 4; ++q) {
       float o[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = UPDATE ? res.decay * old[4 * q + k] - res.lr * x[j][4 * q + k] : x[j][4 * q + k];
+      for (int k = 0; k < 4; ++k)
+        o[k] = UPDATE ? res.decay * old[4 * q + k] - res.lr * x[j][4 * q + k] : x[j][4 * q + k];
       if (!g.tall)
         store_f32<4>(at[q], n[q], o);
       else
@@ -940,8 +963,8 @@ __device__ __forceinline__ void strip_place(bool tall, int e, int* i, int* j) {
   }
 }
 
-// The parts of A added: a thread's four adjacent elements, eight loads in flight. parts: [batch][ways][R R], its first part
-// replaced.
+// The parts of A added: a thread's four adjacent elements, eight loads in flight. parts: [batch][ways][R R], its first
+// part replaced.
 template <int R>
 __global__ __launch_bounds__(256) void k_orth_sum(float* parts, uint32_t ways) {
   using F4 = Vec<float, 4>;
@@ -955,7 +978,7 @@ __global__ __launch_bounds__(256) void k_orth_sum(float* parts, uint32_t ways) {
 // A matrix in one launch.
 template <int R, int S, typename T, bool MUON, typename RT>
 __global__ __launch_bounds__(4 * R) void k_orth_one(OrthShape g, SmallPlan plan, Source<T, MUON> src,
-                                                              Result<RT> res) {
+                                                    Result<RT> res) {
   using C = Small<R, S>;
   __shared__ alignas(16) char xs[2 * C::kX];
   __shared__ alignas(16) char as[2 * C::kA];
@@ -1039,15 +1062,14 @@ __global__ __launch_bounds__(4 * R) void k_orth_one(OrthShape g, SmallPlan plan,
   }
 }
 
-// X_0's strips (FIRST), or one step on them, and the next step's part of A. Workgroup w of a matrix has every gridDim.x-th
-// strip from w on. x: [batch][2][R][cp]; parts_in: `parts` parts of A to be added, [R][R] float32, part_stride from matrix to
-// matrix; parts_out: [batch][gridDim.x][R][R].
+// X_0's strips (FIRST), or one step on them, and the next step's part of A. Workgroup w of a matrix has every
+// gridDim.x-th strip from w on. x: [batch][2][R][cp]; parts_in: `parts` parts of A to be added, [R][R] float32,
+// part_stride from matrix to matrix; parts_out: [batch][gridDim.x][R][R].
 template <int R, int S, bool FIRST, bool LAST, typename T, bool MUON, typename RT>
-__global__ __launch_bounds__(4 * R) void k_orth_strips(OrthShape g, SmallStep st, Source<T, MUON> src,
-                                                                 Result<RT> res, const double* __restrict__ norm,
-                                                                 half* x, const float* __restrict__ parts_in,
-                                                                 uint32_t parts, size_t part_stride,
-                                                                 float* __restrict__ parts_out) {
+__global__ __launch_bounds__(4 * R) void k_orth_strips(OrthShape g, SmallStep st, Source<T, MUON> src, Result<RT> res,
+                                                       const double* __restrict__ norm, half* x,
+                                                       const float* __restrict__ parts_in, uint32_t parts,
+                                                       size_t part_stride, float* __restrict__ parts_out) {
   using C = Small<R, S>;
   __shared__ alignas(16) char xs[2 * C::kX];
   __shared__ alignas(16) char as[2 * C::kA];
@@ -1225,9 +1247,9 @@ uint64_t round_up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
 // The side of the square tiles of a product, and its time in us: the one whose rounds of workgroups take least.
 // `tiles(side)` counts them. Measured for tiles of depth 1,024 in two planes, one workgroup after the other on a compute
-// unit: 12.8, 31, 56 and 95 us, and about 4 us of a launch's own. 8 x 1,024 x 4,096: P X 243 us with tiles of 256, 278 with 128, 416 with 64; 4,096 x 1,024: X X^T 36 us
-// with tiles of 64, 91 with 128; 4,096 x 4,096: A A^T 205 us with 253 tiles of 192, 250 with 136 of 256, 276 with 528 of
-// 128.
+// unit: 12.8, 31, 56 and 95 us, and about 4 us of a launch's own. 8 x 1,024 x 4,096: P X 243 us with tiles of 256, 278
+// with 128, 416 with 64; 4,096 x 1,024: X X^T 36 us with tiles of 64, 91 with 128; 4,096 x 4,096: A A^T 205 us with 253
+// tiles of 192, 250 with 136 of 256, 276 with 528 of 128.
 struct Side {
   int side;
   double us;
@@ -1236,10 +1258,11 @@ struct Side {
 template <typename F>
 Side tile_side(uint64_t deep, F tiles) {
   Side best{0, 1e300};
-  for (const auto& [side, us] : {std::pair(64, 12.8), std::pair(128, 31.0), std::pair(192, 56.0), std::pair(256, 95.0)}) {
-    const double rounds = double(tiles(uint64_t(side))) / 256;
+  for (const auto& [side, us] :
+       {std::pair(64, 12.8), std::pair(128, 31.0), std::pair(192, 56.0), std::pair(256, 95.0)}) {
+    const double rounds = double(tiles(uint64_t(side))) / 256, whole = std::ceil(rounds);
     // tiles of 64 overlap on a compute unit, those of 128 in part
-    const double whole = std::ceil(rounds), count = side == 64 ? std::max(1.0, rounds) : (side == 128 ? (whole + rounds) / 2 : whole);
+    const double count = side == 64 ? std::max(1.0, rounds) : (side == 128 ? (whole + rounds) / 2 : whole);
     const double time = us * count * double(deep) / 1024 + 4;
     if (time < best.us) best = Side{side, time};
   }
@@ -1259,11 +1282,12 @@ void by_side(int side, F f) {
     f(std::integral_constant<int, 256>());
 }
 
-// The steps, each by its three products, or, where that is less work, two at a time: with P~ = P + a I, A of the second step
-// is P~ A P~ (all of them are polynomials of one matrix), and both steps are one product with X:
+// The steps, each by its three products, or, where that is less work, two at a time: with P~ = P + a I, A of the second
+// step is P~ A P~ (all of them are polynomials of one matrix), and both steps are one product with X:
 //   T = A P~;  A' = T P~;  P' from A';  Q = P' P~ + a' P;  X <- a a' X + Q X,
 // five products of r x r instead of a second X X^T and P X. Two steps cost no accuracy (a rounding of A' reaches P' like
-// one of X); more would, because A' loses the small singular values' squares. 8 x 1,024 x 4,096: 2,030 us against 2,540.
+// one of X); more would, because A' loses the small singular values' squares. 8 x 1,024 x 4,096 1,823 us against 2,293,
+// 4,096 x 1,024 float32 355 against 411.
 template <int PLANES, typename T, bool MUON, typename R>
 void launch_steps(hipStream_t s, const OrthShape& g, const Plan& plan, const Source<T, MUON>& src, double* part, half* x,
                   half* xt, half* next, half* am, half* pm, half* tm, const Result<R>& res) {
@@ -1392,8 +1416,8 @@ gsr_status check_desc(gsr_ctx* ctx, const gsr_newton_schulz* d, const char* who,
   return GSR_OK;
 }
 
-// Matrices of at most 128 rows (or columns). What one workgroup's LDS holds (128 columns, or 256 of at most 64 rows) is done
-// in one launch; more columns are dealt to at most 64 workgroups a matrix by strips of 128.
+// Matrices of at most 128 rows (or columns). What one workgroup's LDS holds (128 columns, or 256 of at most 64 rows) is
+// done in one launch; more columns are dealt to at most 64 workgroups a matrix by strips of 128.
 template <typename T, bool MUON, typename RT>
 gsr_status run_small(gsr_ctx* ctx, hipStream_t s, OrthShape g, const Plan& plan, const Source<T, MUON>& src,
                      const Result<RT>& res, int stage, const char* who) {
@@ -1423,7 +1447,8 @@ gsr_status run_small(gsr_ctx* ctx, hipStream_t s, OrthShape g, const Plan& plan,
   const uint32_t R = narrow ? 64 : 128, ways = uint32_t(std::min<uint64_t>(g.cp / 128, 64));
   const size_t norms = round_up(size_t(g.batch) * g.parts, 2), plane = size_t(R) * g.cp;
   gsr_status st = grow(ctx, ctx->arena.feat_part,
-                       norms * sizeof(double) + g.batch * (2 * plane * sizeof(half) + 2 * size_t(ways) * R * R * sizeof(float)));
+                       norms * sizeof(double) +
+                           g.batch * (2 * plane * sizeof(half) + 2 * size_t(ways) * R * R * sizeof(float)));
   if (st) return st;
   double* norm = static_cast<double*>(ctx->arena.feat_part.ptr);
   half* x = reinterpret_cast<half*>(norm + norms);
@@ -1438,8 +1463,8 @@ gsr_status run_small(gsr_ctx* ctx, hipStream_t s, OrthShape g, const Plan& plan,
 }
 
 template <typename T, bool MUON, typename R>
-gsr_status run(gsr_ctx* ctx, hipStream_t s, const gsr_newton_schulz* d, const Plan& plan,
-               const Source<T, MUON>& src, const Result<R>& res, int stage, const char* who) {
+gsr_status run(gsr_ctx* ctx, hipStream_t s, const gsr_newton_schulz* d, const Plan& plan, const Source<T, MUON>& src,
+               const Result<R>& res, int stage, const char* who) {
   // bfloat16: the left factors in one number where the products take the time
   const int planes = std::is_same_v<R, __bf16> && std::min(d->rows, d->cols) > 256 ? 1 : 2;
   OrthShape g{};

@@ -568,10 +568,13 @@ typedef struct gsr_newton_schulz {
   int64_t momentum_stride[2]; /* read by gsr_muon_step only                                                       */
 } gsr_newton_schulz;
 
-/*   g    the matrices;  out  written, of g's type; may be g itself (same strides)
- * float32 and float16 results have the accuracy of a float32 evaluation, rounded once at the end; bfloat16 results are
- * within 2^-9 of their norm before their own rounding. Uses the context arena as scratch (8 bytes an element, padded to
- * whole tiles, and 8 an element of two squares of the shorter side).
+/*   g    the matrices;  out  written, of g's type; may be g itself (same strides), or must not overlap it
+ * Results have the accuracy of a float32 evaluation, rounded once at the end; bfloat16 results of more than 256 rows
+ * and columns are within 2^-9 of their norm before that rounding. Uses the context arena as scratch: of matrices with
+ * more than 128 rows and columns 12 bytes an element and 4 (of bfloat16 results 2) an element of two or three squares of
+ * the shorter side, both sides padded to multiples of 64; of narrower ones 4 bytes an element, the shorter side padded to
+ * 64 or 128 and the longer to 128, and 32 or 128 KiB for each 128 of the longer side (at most 64 times); of matrices
+ * within 128 x 128 or 64 x 256 none.
  * Errors: GSR_EINVAL (null pointers, unknown dtype, steps, eps or coefficients out of range, output strides that
  * overlap, pointers not aligned to their element), GSR_EOVERFLOW (batch >= 2^16, rows or cols >= 2^20, rows * cols >=
  * 2^31), GSR_ENOMEM, GSR_EHIP. */
