@@ -1,5 +1,5 @@
-// Element types, wide loads and argument checks shared by the feature operators (group norm, rotary positions, cross
-// attention).
+// Element types, wide loads and argument checks shared by the feature operators (norms, rotary positions, cross
+// attention) and the orthogonalised updates.
 #pragma once
 
 #include <algorithm>

@@ -47,7 +47,7 @@ struct Arena {
   DevBuf loss_part;   // double [2 tiles] per-tile sums of the SSIM map and |x - y| (the loss)
   DevBuf loss_maps;   // float [9][H][W] the SSIM map's three derivatives per channel, between the loss's passes
   DevBuf grad_fixed;  // the deterministic backward's sums: uint64 [n][9][2] fixed point, then uint32 [n] flags
-  DevBuf feat_part;   // float: the feature operators' partial results (group norm sums, attention parts and deltas)
+  DevBuf feat_part;   // float: the feature operators' partial results (norms' sums, attention parts and deltas, matrices)
   size_t limit = 0;                // GSR_OPT_ARENA_LIMIT: most bytes the buffers above may hold together (0: none)
   uint64_t* host_total = nullptr;  // pinned host word for the one pair-count readback (written by a kernel)
   uint64_t* host_total_dev = nullptr;  // its device-side address
