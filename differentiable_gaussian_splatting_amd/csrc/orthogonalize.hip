@@ -732,7 +732,7 @@ __global__ __launch_bounds__(kThreads, kTile > 128 ? 1 : 2) void k_orth_apply(
 // workgroup and leaves its own part for the next. All numbers are in two float16.
 //
 // Bound by latency: a step's three products wait for each other, with a turn through LDS and a barrier between them. Five
-// steps of 2 x 64 x 64 float32 take 17.5 us, the step of 192 x 64 parameters 43 (by the large products' kernels 69 and
+// steps of 2 x 64 x 64 float32 take 17.5 us, the step of 192 x 64 parameters 35 (by the large products' kernels 69 and
 // 87), of 100 x 1,000 in strips 109 us with their twelve launches.
 
 // An LDS tile of R rows of S values, in panels of at most 128 columns.
@@ -750,16 +750,17 @@ struct Panels {
   }
 };
 
-// R: r padded to 64 or 128; S: the strip's columns. R / 32 x 2 waves: wave (w / 2, w % 2) has rows 32 (w / 2) .. of each
-// product and half of its columns.
-template <int R, int S>
+// R: r padded to 64 or 128; S: the strip's columns. R / 32 x 2 x H waves: wave (w / 2H, w / H % 2, w % H) has rows
+// 32 (w / 2H) .. of each product and columns of the (w / H % 2)-th half of them: of A and P all, the first of H waves with
+// the sums of the others, each of whose depth is an H-th of X's columns; of X an H-th.
+template <int R, int S, int H = 1>
 struct Small {
-  static constexpr int kT = 4 * R, kWaves = R / 16;
+  static constexpr int kR = R, kT = 4 * R * H, kWaves = R / 16 * H;
   using LX = Panels<R, S>;
   using LA = Tile<half, R>;
-  static constexpr int kX = R * S * 2, kA = R * LA::kRowBytes;  // bytes of a plane
-  static constexpr int kXBlocks = S / 64, kABlocks = R / 64;  // 32-column blocks of a wave
-  static constexpr int kEach = R * S / kT;                    // a strip's elements by each thread
+  static constexpr int kX = R * S * 2, kA = R * LA::kRowBytes;    // bytes of a plane
+  static constexpr int kXBlocks = S / 64 / H, kABlocks = R / 64;  // 32-column blocks of a wave
+  static constexpr int kEach = R * S / kT;                        // a strip's elements by each thread
 };
 
 // Depths 16 kk + 8 h .. + 7 of column at + l % 32 of a tile whose rows are the depths.
@@ -781,7 +782,8 @@ __device__ __forceinline__ Vec<half, 8> frag_of_columns(const char* s, int at, i
 // transposed as the large products' blocks are. With few blocks hi hi has a chain of sums of its own: the next product on
 // the same sums waits for the last.
 template <typename LL, int LP, typename LR, int RP, bool COLUMNS, int BLOCKS, int DEEP>
-__device__ __forceinline__ void small_product(const char* left, int row, const char* right, int col, f32x16* acc) {
+__device__ __forceinline__ void small_product(const char* left, int row, const char* right, int col, f32x16* acc,
+                                              int first = 0) {
   constexpr int kRest = BLOCKS <= 2 ? BLOCKS : 0;
   f32x16 rest[kRest + 1];
 #pragma unroll
@@ -790,7 +792,7 @@ __device__ __forceinline__ void small_product(const char* left, int row, const c
     for (int e = 0; e < 16; ++e) rest[j][e] = 0.0f;
 #pragma unroll
   for (int kk = 0; kk < DEEP / 16; ++kk) {
-    const Vec<half, 8> ah = LL::frag(left, row, kk), al = LL::frag(left + LP, row, kk);
+    const Vec<half, 8> ah = LL::frag(left, row, first + kk), al = LL::frag(left + LP, row, first + kk);
 #pragma unroll
     for (int j = 0; j < BLOCKS; ++j) {
       Vec<half, 8> bh, bl;
@@ -798,8 +800,8 @@ __device__ __forceinline__ void small_product(const char* left, int row, const c
         bh = frag_of_columns<LR>(right, col + 32 * j, kk);
         bl = frag_of_columns<LR>(right + RP, col + 32 * j, kk);
       } else {
-        bh = LR::frag(right, col + 32 * j, kk);
-        bl = LR::frag(right + RP, col + 32 * j, kk);
+        bh = LR::frag(right, col + 32 * j, first + kk);
+        bl = LR::frag(right + RP, col + 32 * j, first + kk);
       }
       f32x16& low = kRest ? rest[kRest ? j : 0] : acc[j];
       acc[j] = mma(bh, ah, acc[j]);
@@ -864,31 +866,38 @@ __device__ __forceinline__ void clear(f32x16 (&a)[N]) {
     for (int e = 0; e < 16; ++e) a[j][e] = 0.0f;
 }
 
-// From the wave's sums of A: A to LDS, P = p_in A + p_sum A A^T in its place.
+// From the sums of A of the waves that `have` them: A to LDS, P = p_in A + p_sum A A^T in its place.
 template <typename C>
-__device__ __forceinline__ void small_to_p(char* as, int row, int col, f32x16 (&a)[C::kABlocks], const SmallStep& st) {
+__device__ __forceinline__ void small_to_p(char* as, int row, int col, f32x16 (&a)[C::kABlocks], const SmallStep& st,
+                                           bool have = true) {
   using L = typename C::LA;
+  if (have) {
 #pragma unroll
-  for (int j = 0; j < C::kABlocks; ++j)
+    for (int j = 0; j < C::kABlocks; ++j)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) put_four<L, C::kA>(as, row, col + 32 * j, q, four_of(a[j], q) * st.a_scale);
+      for (int q = 0; q < 4; ++q) put_four<L, C::kA>(as, row, col + 32 * j, q, four_of(a[j], q) * st.a_scale);
+  }
   __syncthreads();
   f32x16 s[C::kABlocks];
-  clear(s);
-  small_product<L, C::kA, L, C::kA, false, C::kABlocks, C::kWaves * 16>(as, row, as, col, s);
+  if (have) {
+    clear(s);
+    small_product<L, C::kA, L, C::kA, false, C::kABlocks, C::kR>(as, row, as, col, s);
 #pragma unroll
-  for (int j = 0; j < C::kABlocks; ++j)
+    for (int j = 0; j < C::kABlocks; ++j)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const Vec<float, 4> v = get_four<L, C::kA>(as, row, col + 32 * j, q);
+      for (int q = 0; q < 4; ++q) {
+        const Vec<float, 4> v = get_four<L, C::kA>(as, row, col + 32 * j, q);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s[j][4 * q + k] = fmaf(st.p_in, v[k], s[j][4 * q + k] * st.p_sum);
-    }
+        for (int k = 0; k < 4; ++k) s[j][4 * q + k] = fmaf(st.p_in, v[k], s[j][4 * q + k] * st.p_sum);
+      }
+  }
   __syncthreads();
+  if (have) {
 #pragma unroll
-  for (int j = 0; j < C::kABlocks; ++j)
+    for (int j = 0; j < C::kABlocks; ++j)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) put_four<L, C::kA>(as, row, col + 32 * j, q, four_of(s[j], q));
+      for (int q = 0; q < 4; ++q) put_four<L, C::kA>(as, row, col + 32 * j, q, four_of(s[j], q));
+  }
   __syncthreads();
 }
 
@@ -953,7 +962,7 @@ __device__ __forceinline__ void small_result(const OrthShape& g, const Result<T>
 template <typename C>
 __device__ __forceinline__ void strip_place(bool tall, int e, int* i, int* j) {
   const int at = e * C::kT + int(threadIdx.x);
-  constexpr int kRows = C::kWaves * 16, kCols = C::kEach * C::kT / kRows;
+  constexpr int kRows = C::kR, kCols = C::kEach * C::kT / kRows;
   if (tall) {
     *j = at / kRows;
     *i = at % kRows;
@@ -975,17 +984,20 @@ __global__ __launch_bounds__(256) void k_orth_sum(float* parts, uint32_t ways) {
   *at = sum;
 }
 
-// A matrix in one launch.
-template <int R, int S, typename T, bool MUON, typename RT>
-__global__ __launch_bounds__(4 * R) void k_orth_one(OrthShape g, SmallPlan plan, Source<T, MUON> src,
-                                                    Result<RT> res) {
-  using C = Small<R, S>;
+// A matrix in one launch, by twice the waves where a wave would have more than 32 columns of X and its registers allow:
+// 64 x 192 float32 34 us by H = 2, 39.5 by 1; 60 x 100 22.1 and 24.3; 128 x 128 63.6 and 49.9 (1,024 threads leave each
+// too few registers).
+template <int R, int S, int H, typename T, bool MUON, typename RT>
+__global__ __launch_bounds__(4 * R * H) void k_orth_one(OrthShape g, SmallPlan plan, Source<T, MUON> src,
+                                                        Result<RT> res) {
+  static_assert(H == 1 || H == 2);
+  using C = Small<R, S, H>;
   __shared__ alignas(16) char xs[2 * C::kX];
   __shared__ alignas(16) char as[2 * C::kA];
   __shared__ double sums[C::kWaves];
   const uint32_t b = blockIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-  const int row = 32 * (wave / 2), xcol = (wave % 2) * (S / 2), acol = (wave % 2) * (R / 2);
+  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6), w = wave / H, h = wave % H;
+  const int row = 32 * (w / 2), xcol = (w % 2) * (S / 2) + h * (S / 2 / H), acol = (w % 2) * (R / 2);
   {
     float u[C::kEach];
     double sum = 0.0;
@@ -1043,8 +1055,28 @@ __global__ __launch_bounds__(4 * R) void k_orth_one(OrthShape g, SmallPlan plan,
     const SmallStep st = plan.step[k];
     f32x16 a[C::kABlocks];
     clear(a);
-    small_product<typename C::LX, C::kX, typename C::LX, C::kX, false, C::kABlocks, S>(xs, row, xs, acol, a);
-    small_to_p<C>(as, row, acol, a, st);
+    small_product<typename C::LX, C::kX, typename C::LX, C::kX, false, C::kABlocks, S / H>(xs, row, xs, acol, a,
+                                                                                           h * (S / H / 16));
+    if constexpr (H > 1) {  // the second waves' sums pass through the space of A, whose last use is behind a barrier
+      static_assert(C::kWaves / H * C::kABlocks * 64 * sizeof(f32x16) <= sizeof(as));
+      using F4 = Vec<float, 4>;
+      F4* const other = reinterpret_cast<F4*>(as) + w * C::kABlocks * 4 * 64 + (threadIdx.x & 63);
+      if (h) {
+#pragma unroll
+        for (int e = 0; e < C::kABlocks * 4; ++e) other[e * 64] = four_of(a[e / 4], e % 4);
+      }
+      __syncthreads();
+      if (!h) {
+#pragma unroll
+        for (int e = 0; e < C::kABlocks * 4; ++e) {
+          const F4 v = other[e * 64];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[e / 4][e % 4 * 4 + i] += v[i];
+        }
+      }
+      __syncthreads();
+    }
+    small_to_p<C>(as, row, acol, a, st, h == 0);
     f32x16 x[C::kXBlocks];
     clear(x);
     small_product<typename C::LA, C::kA, typename C::LX, C::kX, true, C::kXBlocks, R>(as, row, xs, xcol, x);
@@ -1373,10 +1405,11 @@ bool pairs_pay(const OrthShape& g) {
   return tile_side(g.cp, triangle).us + tile_side(g.rp, whole).us > 3.3 * tile_side(g.rp, triangle).us;
 }
 
-template <int R, int S, typename T, bool MUON, typename RT>
+template <int R, int S, int H, typename T, bool MUON, typename RT>
 void launch_one(hipStream_t s, const OrthShape& g, const SmallPlan& plan, const Source<T, MUON>& src,
                 const Result<RT>& res) {
-  hipLaunchKernelGGL((k_orth_one<R, S, T, MUON, RT>), dim3(g.batch), dim3(Small<R, S>::kT), 0, s, g, plan, src, res);
+  hipLaunchKernelGGL((k_orth_one<R, S, H, T, MUON, RT>), dim3(g.batch), dim3(Small<R, S, H>::kT), 0, s, g, plan, src,
+                     res);
 }
 
 template <int R, int S, typename T, bool MUON, typename RT>
@@ -1433,13 +1466,13 @@ gsr_status run_small(gsr_ctx* ctx, hipStream_t s, OrthShape g, const Plan& plan,
   if (g.c <= 128 || (narrow && g.c <= 256)) {
     timing_mark(ctx, stage, s, false);
     if (g.c <= 64)
-      launch_one<64, 64>(s, g, sp, src, res);
+      launch_one<64, 64, 1>(s, g, sp, src, res);
     else if (!narrow)
-      launch_one<128, 128>(s, g, sp, src, res);
+      launch_one<128, 128, 1>(s, g, sp, src, res);
     else if (g.c <= 128)
-      launch_one<64, 128>(s, g, sp, src, res);
+      launch_one<64, 128, 2>(s, g, sp, src, res);
     else
-      launch_one<64, 256>(s, g, sp, src, res);
+      launch_one<64, 256, 2>(s, g, sp, src, res);
     timing_mark(ctx, stage, s, true);
     return check_launch(ctx, who);
   }
