@@ -361,3 +361,11 @@ def test_the_arena_limit_refuses_and_leaves_the_state(ctx):
         assert torch.equal(p, keep) and (m == 0).all()
     finally:
         c.close()
+
+
+def test_no_coefficients_are_refused(ctx):
+    from differentiable_gaussian_splatting_amd import gsr
+    g = torch.ones(4, 4, device="cuda")
+    for table in ((), [(1.0, 0.0)] * 5, [(1.0, 0.0, 0.0)] * 4):
+        with pytest.raises(ValueError, match="coefficients"):
+            gsr.gsr_orthogonalize(ctx, g, 5, table)
